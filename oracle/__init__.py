@@ -32,6 +32,7 @@ from .layer import OracleMoE
 from .mx import e4m3_decode, mxfp8_quantize, mxfp8_dequant, mxfp8_round, expert_ffn_mx
 from .placement import (POLICY_LRU, POLICY_PREFILL, POLICY_STATIC, POLICY_PINNED_RING, replay as placement_replay,
                         routing_counts, top_keys, static_resident)
+from . import norm, tokens
 
 __all__ = [
     "bf16_to_f64", "e2m1_decode", "dequant_fp4", "e8m0_decode", "dequant_mxfp4", "expert_weights_f64",
@@ -42,4 +43,5 @@ __all__ = [
     "e4m3_decode", "mxfp8_quantize", "mxfp8_dequant", "mxfp8_round", "expert_ffn_mx",
     "POLICY_LRU", "POLICY_PREFILL", "POLICY_STATIC", "POLICY_PINNED_RING", "placement_replay",
     "routing_counts", "top_keys", "static_resident",
+    "norm", "tokens",
 ]
