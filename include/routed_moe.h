@@ -588,6 +588,145 @@ MOE_API moe_status moe_bank_read(const char* path, const moe_config* cfg, void* 
 MOE_API moe_status moe_pool_load(moe_ctx* ctx, const char* path, int32_t threads, void** host_pool,
                                  moe_bank_stats* out);
 
+/* ------------------------------------------------------------------ around the experts
+ *
+ * Tokens sorted by expert, moved and brought back with their gates, the norms around a
+ * block, and the gradients of all of it: the steps between the residual stream and the
+ * experts' products, for experts that run outside this library (a shared expert, adapters)
+ * and for training (a router or norms over frozen experts).  None needs a context.
+ *
+ * Conventions of these calls, beside those above:
+ *  - They only enqueue kernels on `stream` (no allocation, no host read, no synchronisation), may
+ *    be captured into a graph, keep nothing between calls and share no scratch: the caller passes
+ *    a workspace where one is needed, one per call that may be in flight (two graphs that may
+ *    run at once need two).  Kernels run on the device of `stream`.
+ *  - Matrices of tokens are [T,H] with a row stride ld in elements (0 = H; ld >= H).  Matrices of
+ *    sorted rows are [T*k,H], dense.  Every pointer is aligned to its element, no further: any H
+ *    and any ld are taken.  `*_fmt` is a moe_afmt.
+ *  - Sums run in fp32 in a fixed order (the same bits every time, whatever the load) and each output
+ *    element is rounded once, to nearest even, to its format.
+ *  - An output shares no byte with an input or another output unless the call says so (blocks side
+ *    by side in the rows of one buffer are told apart when their strides in bytes are equal).
+ *  - Limits: 1 <= T <= 2^22, 1 <= k <= 1024, T*k <= 2^26, n_experts <= 1024, H <= 65536 (moves) or
+ *    16384 (norms).
+ *  - MOE_EINVAL for a null pointer, shape, format, stride, alignment, overlap or short workspace
+ *    (nothing is enqueued); MOE_EHIP if a launch fails.
+ */
+
+/* Bytes of workspace moe_dispatch needs for T tokens of k ranks over n_experts; -1 for shapes out
+ * of range.  Pure host function. */
+MOE_API int64_t moe_dispatch_workspace(int32_t T, int32_t k, int32_t n_experts);
+
+/*
+ * Sort the (token, rank) pairs p = t*k + j by expert and move the tokens' rows to their places.
+ *   topk_idx device int32 [T,k] expert ids; an id outside [0, n_experts) leaves its pair out
+ *            (the same expert may occur twice in a token)
+ *   perm     device int32 [T*k] out: the kept pairs, stably ordered by (expert, p); entries
+ *            behind the last kept pair are left as they were
+ *   inv      device int32 [T,k] out: the position of each pair in perm, -1 for a pair left out
+ *   offsets  device int32 [n_experts+1] out: expert e's rows are [offsets[e], offsets[e+1])
+ *   x, xs    device [T,H] and [T*k,H] of format fmt: xs[i] = x[perm[i] / k]; rows of xs behind the
+ *            last kept pair are left as they were.  Both NULL: sort only (fmt, H, ld_x unused).
+ *   ws       device, moe_dispatch_workspace(T, k, n_experts) bytes (NULL when that is 0)
+ */
+MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, int32_t k, int32_t n_experts, const void* x,
+                                int32_t fmt, int32_t H, int64_t ld_x, void* xs, int32_t* perm, int32_t* inv,
+                                int32_t* offsets, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * The gradient of the move: dx[t] = sum_j dxs[inv[t,j]] over the token's kept pairs in rank order
+ * (zeros for a token without one).  inv as moe_dispatch wrote it; an entry outside [0, T*k) counts
+ * as a pair left out, here and in the calls below.
+ */
+MOE_API moe_status moe_dispatch_backward(const void* dxs, int32_t dxs_fmt, const int32_t* inv, int32_t T, int32_t k,
+                                         int32_t H, void* dx, int32_t dx_fmt, int64_t ld_dx, moe_stream_t stream);
+
+/*
+ * Expert outputs weighted by their gates and brought back to their tokens:
+ *   y[t] = sum_j w[t,j] ys[inv[t,j]]    over the token's kept pairs in rank order
+ * ys: device [T*k,H] sorted rows; w: device fp32 [T,k] (the gate of a pair left out is not read into
+ * the sum, whatever its value); y: device [T,H].
+ */
+MOE_API moe_status moe_combine(const void* ys, int32_t ys_fmt, const int32_t* inv, const float* w, int32_t T, int32_t k,
+                               int32_t H, void* y, int32_t y_fmt, int64_t ld_y, moe_stream_t stream);
+
+/*
+ * Its gradient:  dys[inv[t,j]] = w[t,j] dy[t],   dw[t,j] = <dy[t], ys[inv[t,j]]>.
+ * dys: [T*k,H] of ys_fmt (rows behind the last kept pair are left as they were), may be ys itself
+ * where every row has one pair, as moe_dispatch leaves it; dw: fp32 [T,k], 0 for a pair left out.
+ * Either output may be NULL: without dw, ys is not read; without dys, w is not.
+ */
+MOE_API moe_status moe_combine_backward(const void* dy, int32_t dy_fmt, int64_t ld_dy, const void* ys, int32_t ys_fmt,
+                                        const int32_t* inv, const float* w, int32_t T, int32_t k, int32_t H, void* dys,
+                                        float* dw, moe_stream_t stream);
+
+/*
+ * The gradient of the gates of moe_topk / moe_route with respect to the logits z, the choice held:
+ *   renorm 0: dz[e] = p_e (sum_{j: idx_j = e} dw_j - sum_j p_{idx_j} dw_j),  p = softmax(z)
+ *   renorm 1: the same with p the softmax over the chosen logits alone; dz = 0 elsewhere
+ * logits, dlogits: device fp32 [T,E] (dlogits may be logits); topk_idx int32 and dw fp32 [T,k]; a pair
+ * whose id is outside [0, E) is left out.  Logits of -inf have p = 0; a token with no logit above
+ * -inf, or with renorm 1 and no pair kept, gets zeros.
+ */
+MOE_API moe_status moe_topk_backward(const float* logits, int32_t T, int32_t n_experts, const int32_t* topk_idx,
+                                     int32_t k, const float* dw, int32_t renorm, float* dlogits, moe_stream_t stream);
+
+/* The gate of a block's output in moe_block_norm: none, fp32 [T], or fp32 [H]. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2 } moe_gate_kind;
+
+typedef struct {
+  int32_t T, H;
+  int32_t h_fmt, y_fmt, x_fmt; /* moe_afmt of the residual stream, the block's output, the norm's output */
+  int32_t gate_kind;           /* moe_gate_kind */
+  float alpha;                 /* residual scale, finite */
+  float eps;                   /* added to the mean square, in (0, 1] */
+  int64_t ld_h, ld_y, ld_x;    /* row strides (0 = H) of h, h_out and their gradients; y and dy; x_out and dx */
+} moe_norm_config;
+
+/*
+ * The step between two blocks: the norm behind the first, its gate and scale into the residual
+ * stream, the norm before the second (rms(v) = sqrt(mean(v^2) + eps) over a row):
+ *   u     = w_post * y / rms(y)        (w_post = NULL: u = y)
+ *   h_out = h + alpha * gate * u
+ *   x_out = w_pre * h_out / rms(h_out) (of h_out before it is rounded to h_fmt)
+ * h, h_out device [T,H] (h_out may be h); y [T,H] the block's output; w_post, w_pre fp32 [H]; gate fp32
+ * [T] or [H] (NULL with MOE_GATE_NONE).  x_out = w_pre = NULL: no second norm.  y = h_out = w_post =
+ * gate = NULL: the second norm alone, of h.
+ */
+MOE_API moe_status moe_block_norm(const moe_norm_config* cfg, const void* h, const void* y, const float* w_post,
+                                  const float* gate, const float* w_pre, void* h_out, void* x_out, moe_stream_t stream);
+
+/* Bytes of workspace moe_block_norm_backward needs when it writes dw_post, dw_pre or a channel gate's
+ * gradient; -1 for shapes out of range.  Pure host function. */
+MOE_API int64_t moe_block_norm_workspace(int32_t T, int32_t H);
+
+/*
+ * Its gradient, from dh_out (of h_out, from the stream behind the step; NULL = 0) and dx (of x_out;
+ * NULL = 0, then w_pre and dw_pre are NULL and h_out is not read):
+ *   dh [T,H] of h_fmt (may be dh_out); dy [T,H] of y_fmt (may be y); dw_post, dw_pre fp32 [H]; dgate fp32
+ *   [T] or [H].  Any output may be NULL (not all).
+ * h_out is the forward's output as stored (with y = NULL there, its h); y, w_post, gate, w_pre are the
+ * forward's.  ws as moe_block_norm_workspace says; not used (may be NULL) when none of dw_post, dw_pre
+ * and a channel gate's dgate is asked for.
+ */
+MOE_API moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* h_out, const void* y,
+                                           const float* w_post, const float* gate, const float* w_pre,
+                                           const void* dh_out, const void* dx, void* dh, void* dy, float* dw_post,
+                                           float* dgate, float* dw_pre, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * One decode layer step with the step to the next block: moe_decode_layer into y, then
+ * moe_block_norm of y into the residual stream h (in place) and, unless x_next is NULL, the next
+ * block's input.  norm->T must be T and norm->H the context's hidden size, norm->y_fmt
+ * MOE_AFMT_F32 with dense rows (y is the [T,H] fp32 output of moe_decode_layer).  x_next may be x.
+ * Errors and capture as moe_decode_layer; MOE_EINVAL for what moe_block_norm refuses, before
+ * anything is enqueued.
+ */
+MOE_API moe_status moe_decode_block(moe_ctx* ctx, int32_t layer, const void* x, int32_t T, const float* logit_bias,
+                                    int32_t* topk_idx, float* topk_w, int32_t* slot_idx, float* y,
+                                    const moe_norm_config* norm, void* h, const float* w_post, const float* gate,
+                                    const float* w_pre, void* x_next, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -80,6 +80,15 @@ class moe_replay_result(ctypes.Structure):
     _fields_ = [(n, ctypes.c_uint64) for n in ("keys", "misses", "reads")]
 
 
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL = 0, 1, 2
+
+
+class moe_norm_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "h_fmt", "y_fmt", "x_fmt", "gate_kind")] + [
+        ("alpha", ctypes.c_float), ("eps", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in ("ld_h", "ld_y", "ld_x")]
+
+
 class moe_bank_header(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_layers", "n_experts", "hidden", "inter", "wfmt", "pad")] + [
         ("record_bytes", ctypes.c_int64), ("n_records", ctypes.c_int64)]
@@ -138,6 +147,17 @@ def _load():
         "moe_bank_info": (I32, [ctypes.c_char_p, ctypes.POINTER(moe_bank_header)]),
         "moe_bank_read": (I32, [ctypes.c_char_p, ctypes.POINTER(moe_config), VP, I64, I32,
                                 ctypes.POINTER(moe_bank_stats)]),
+        "moe_dispatch_workspace": (I64, [I32, I32, I32]),
+        "moe_dispatch": (I32, [VP, I32, I32, I32, VP, I32, I32, I64, VP, VP, VP, VP, VP, ctypes.c_size_t, VP]),
+        "moe_dispatch_backward": (I32, [VP, I32, VP, I32, I32, I32, VP, I32, I64, VP]),
+        "moe_combine": (I32, [VP, I32, VP, VP, I32, I32, I32, VP, I32, I64, VP]),
+        "moe_combine_backward": (I32, [VP, I32, I64, VP, I32, VP, VP, I32, I32, I32, VP, VP, VP]),
+        "moe_topk_backward": (I32, [VP, I32, I32, VP, I32, VP, I32, VP, VP]),
+        "moe_block_norm": (I32, [ctypes.POINTER(moe_norm_config), VP, VP, VP, VP, VP, VP, VP, VP]),
+        "moe_block_norm_workspace": (I64, [I32, I32]),
+        "moe_block_norm_backward": (I32, [ctypes.POINTER(moe_norm_config)] + [VP] * 13 + [ctypes.c_size_t, VP]),
+        "moe_decode_block": (I32, [P, I32, VP, I32, VP, VP, VP, VP, VP, ctypes.POINTER(moe_norm_config), VP, VP, VP,
+                                   VP, VP, VP]),
         "moe_pool_load": (I32, [P, ctypes.c_char_p, I32, ctypes.POINTER(VP), ctypes.POINTER(moe_bank_stats)]),
     }
     for name, (res, args) in sig.items():
@@ -448,3 +468,244 @@ def moe_permute_noalloc(slot_idx, P: int, n_slot_range: int, perm, offsets, grou
                                  _ptr(n_groups), _stream(stream))
     if st != MOE_OK:
         raise MoeError(st, "moe_permute_noalloc", "sizes out of range, null pointer or launch failure")
+
+
+# ---------------------------------------------------------------------------
+# Around the experts.  These take torch tensors only and read shapes, formats and row strides
+# from them; a tensor the library would misread (type, shape, stride, device) is refused here.
+_FMT = {torch.float32: MOE_AFMT_F32, torch.bfloat16: MOE_AFMT_BF16}
+
+
+class _Args:
+    """Checks the tensors of one call and holds the device they share."""
+
+    def __init__(self, where: str):
+        self.where = where
+        self.device = None
+
+    def refuse(self, msg: str):
+        raise MoeError(MOE_EINVAL, self.where, msg)
+
+    def _place(self, name, t):
+        if not t.is_cuda:
+            self.refuse(f"{name} must be on the GPU")
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            self.refuse(f"{name} is on {t.device}, other tensors on {self.device}")
+
+    def rows(self, name, t, n_rows=None, width=None, dense=False, like=None):
+        """(pointer, format, row stride) of a [rows, H] matrix with contiguous rows."""
+        if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _FMT:
+            self.refuse(f"{name} must be a two-dimensional fp32 or bf16 tensor")
+        n, h = t.shape
+        if n < 1 or h < 1 or (n_rows is not None and n != n_rows) or (width is not None and h != width):
+            self.refuse(f"{name} has shape {tuple(t.shape)}, not {(n_rows or 'T', width or 'H')}")
+        ld = h if n == 1 else t.stride(0)
+        if (h > 1 and t.stride(1) != 1) or ld < h or (dense and ld != h):
+            self.refuse(f"{name} needs contiguous rows" + (" without gaps" if dense else ""))
+        if like is not None and (t.dtype != like.dtype or (n > 1 and ld != like.stride(0))):
+            self.refuse(f"{name} must have the type and row stride of the tensor it belongs to")
+        self._place(name, t)
+        return t.data_ptr(), _FMT[t.dtype], ld
+
+    def flat(self, name, t, dtype, *shape):
+        """Pointer of a dense tensor of this type and shape (the shape as a whole: numel for one number)."""
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
+            self.refuse(f"{name} must be a contiguous {dtype} tensor")
+        if tuple(t.shape) != shape and not (len(shape) == 1 and t.numel() == shape[0]):
+            self.refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
+        self._place(name, t)
+        return t.data_ptr()
+
+    def workspace(self, t, need):
+        """(pointer, bytes) of the caller's workspace."""
+        if need < 0:
+            self.refuse("shape out of range")
+        if t is None:
+            return None, 0
+        if not isinstance(t, torch.Tensor) or not t.is_contiguous():
+            self.refuse("ws must be a contiguous tensor")
+        if t.numel():
+            self._place("ws", t)
+        return t.data_ptr() or None, t.numel() * t.element_size()
+
+    def call(self, stream, *args):
+        """Forward to the C entry point on `stream` (default: the current stream of the tensors' device)."""
+        dev = self.device.index
+        if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+            self.refuse(f"stream is on {stream.device}, tensors on {self.device}")
+        s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+        if torch.cuda.current_device() == dev:
+            st = getattr(lib, self.where)(*args, s)
+        else:
+            with torch.cuda.device(dev):
+                st = getattr(lib, self.where)(*args, s)
+        if st != MOE_OK:
+            raise MoeError(st, self.where, "launch failure" if st == MOE_EHIP else
+                           "shape out of range, overlapping tensors, missing argument or short workspace")
+
+
+def moe_dispatch_workspace(T: int, k: int, n_experts: int) -> int:
+    """Bytes of workspace of moe_dispatch."""
+    n = int(lib.moe_dispatch_workspace(T, k, n_experts))
+    if n < 0:
+        raise MoeError(MOE_EINVAL, "moe_dispatch_workspace", "shape out of range")
+    return n
+
+
+def _pairs(a: _Args, name, idx):
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 2 or idx.numel() < 1:
+        a.refuse(f"{name} must be an int32 tensor [T, k]")
+    T, k = idx.shape
+    return T, k, a.flat(name, idx, torch.int32, T, k)
+
+
+def moe_dispatch(topk_idx, n_experts: int, x, xs, perm, inv, offsets, ws=None, stream=None) -> None:
+    """Sort the pairs of topk_idx [T,k] by expert into perm [T*k], inv [T,k] and offsets [n_experts+1], and
+    move the rows of x [T,H] to xs [T*k,H] (both None: sort only).  ws: uint8 workspace."""
+    a = _Args("moe_dispatch")
+    T, k, idx = _pairs(a, "topk_idx", topk_idx)
+    xp = xsp = None
+    fmt = H = ld = 0
+    if x is not None or xs is not None:
+        xp, fmt, ld = a.rows("x", x, T)
+        H = x.shape[1]
+        xsp, xs_fmt, _ = a.rows("xs", xs, T * k, H, dense=True)
+        if xs_fmt != fmt:
+            a.refuse("xs must have x's type")
+    p = a.flat("perm", perm, torch.int32, T * k)
+    i = a.flat("inv", inv, torch.int32, T, k)
+    o = a.flat("offsets", offsets, torch.int32, n_experts + 1)
+    w, wn = a.workspace(ws, lib.moe_dispatch_workspace(T, k, n_experts))
+    a.call(stream, idx, T, k, n_experts, xp, fmt, H, ld, xsp, p, i, o, w, wn)
+
+
+def moe_dispatch_backward(dxs, inv, dx, stream=None) -> None:
+    """dx [T,H] = the sum of each token's rows of dxs [T*k,H]."""
+    a = _Args("moe_dispatch_backward")
+    T, k, i = _pairs(a, "inv", inv)
+    g, fmt, _ = a.rows("dxs", dxs, T * k, dense=True)
+    H = dxs.shape[1]
+    o, o_fmt, ld = a.rows("dx", dx, T, H)
+    a.call(stream, g, fmt, i, T, k, H, o, o_fmt, ld)
+
+
+def moe_combine(ys, inv, w, y, stream=None) -> None:
+    """y [T,H] = the sum of each token's rows of ys [T*k,H] weighted by w [T,k] (fp32)."""
+    a = _Args("moe_combine")
+    T, k, i = _pairs(a, "inv", inv)
+    r, fmt, _ = a.rows("ys", ys, T * k, dense=True)
+    H = ys.shape[1]
+    wp = a.flat("w", w, torch.float32, T, k)
+    o, o_fmt, ld = a.rows("y", y, T, H)
+    a.call(stream, r, fmt, i, wp, T, k, H, o, o_fmt, ld)
+
+
+def moe_combine_backward(dy, ys, inv, w, dys, dw, stream=None) -> None:
+    """From dy [T,H]: dys [T*k,H] (or None; may be ys) and dw [T,k] (or None, then ys may be None)."""
+    a = _Args("moe_combine_backward")
+    T, k, i = _pairs(a, "inv", inv)
+    d, d_fmt, ld = a.rows("dy", dy, T)
+    H = dy.shape[1]
+    r = o = wp = g = None
+    fmt = d_fmt
+    if dys is not None:
+        o, fmt, _ = a.rows("dys", dys, T * k, H, dense=True)
+        wp = a.flat("w", w, torch.float32, T, k)
+    if dw is not None:
+        r, r_fmt, _ = a.rows("ys", ys, T * k, H, dense=True)
+        if dys is not None and r_fmt != fmt:
+            a.refuse("dys must have ys's type")
+        fmt = r_fmt
+        g = a.flat("dw", dw, torch.float32, T, k)
+    a.call(stream, d, d_fmt, ld, r, fmt, i, wp, T, k, H, o, g)
+
+
+def moe_topk_backward(logits, topk_idx, dw, renorm: int, dlogits, stream=None) -> None:
+    """dlogits [T,E] from the gates' gradients dw [T,k] at the chosen experts topk_idx [T,k]."""
+    a = _Args("moe_topk_backward")
+    T, k, idx = _pairs(a, "topk_idx", topk_idx)
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        a.refuse("logits must be fp32 [T, E]")
+    E = logits.shape[1]
+    z = a.flat("logits", logits, torch.float32, T, E)
+    g = a.flat("dw", dw, torch.float32, T, k)
+    o = a.flat("dlogits", dlogits, torch.float32, T, E)
+    a.call(stream, z, T, E, idx, k, g, int(renorm), o)
+
+
+def _norm_inputs(a: _Args, T, H, w_post, gate, w_pre, gate_kind):
+    q = None if w_post is None else a.flat("w_post", w_post, torch.float32, H)
+    p = None if w_pre is None else a.flat("w_pre", w_pre, torch.float32, H)
+    if (gate is None) != (gate_kind == MOE_GATE_NONE):
+        a.refuse("gate and gate_kind must go together")
+    g = None if gate is None else a.flat("gate", gate, torch.float32, T if gate_kind == MOE_GATE_TOKEN else H)
+    return q, g, p
+
+
+def moe_block_norm(h, y=None, w_post=None, gate=None, w_pre=None, h_out=None, x_out=None,
+                   gate_kind: int = MOE_GATE_NONE, alpha: float = 1.0, eps: float = 1e-6, stream=None) -> None:
+    """h_out = h + alpha gate norm(y; w_post), x_out = norm(h_out; w_pre): the step between two blocks."""
+    a = _Args("moe_block_norm")
+    hp, h_fmt, ld_h = a.rows("h", h)
+    T, H = h.shape
+    yp = ho = xo = None
+    y_fmt = x_fmt = h_fmt
+    ld_y = ld_x = H
+    if y is not None:
+        yp, y_fmt, ld_y = a.rows("y", y, T, H)
+    if h_out is not None:
+        ho = a.rows("h_out", h_out, T, H, like=h)[0]
+    if x_out is not None:
+        xo, x_fmt, ld_x = a.rows("x_out", x_out, T, H)
+    q, g, p = _norm_inputs(a, T, H, w_post, gate, w_pre, gate_kind)
+    cfg = moe_norm_config(T, H, h_fmt, y_fmt, x_fmt, gate_kind, alpha, eps, ld_h, ld_y, ld_x)
+    a.call(stream, ctypes.byref(cfg), hp, yp, q, g, p, ho, xo)
+
+
+def moe_block_norm_workspace(T: int, H: int) -> int:
+    """Bytes of workspace of moe_block_norm_backward."""
+    n = int(lib.moe_block_norm_workspace(T, H))
+    if n < 0:
+        raise MoeError(MOE_EINVAL, "moe_block_norm_workspace", "shape out of range")
+    return n
+
+
+def moe_block_norm_backward(h_out, y, w_post, gate, w_pre, dh_out, dx, dh, dy, dw_post, dgate, dw_pre, ws=None,
+                            gate_kind: int = MOE_GATE_NONE, alpha: float = 1.0, eps: float = 1e-6,
+                            stream=None) -> None:
+    """The gradient of moe_block_norm from dh_out and dx (either may be None); any output may be None."""
+    a = _Args("moe_block_norm_backward")
+    lead = next((t for t in (dh_out, dx) if t is not None), None)
+    if not isinstance(lead, torch.Tensor) or lead.dim() != 2:
+        a.refuse("dh_out or dx must be given")
+    T, H = lead.shape
+    ptr = {}
+    fmt = {"h": None, "y": None, "x": None}
+    ld = {"h": H, "y": H, "x": H}
+    first = {"h": None, "y": None, "x": None}
+    for name, t, kind in (("h_out", h_out, "h"), ("dh_out", dh_out, "h"), ("dh", dh, "h"), ("y", y, "y"), ("dy", dy, "y"),
+                          ("dx", dx, "x")):
+        if t is None:
+            ptr[name] = None
+            continue
+        ptr[name], fmt[kind], ld[kind] = a.rows(name, t, T, H, like=first[kind])
+        first[kind] = t if first[kind] is None else first[kind]
+    q, g, p = _norm_inputs(a, T, H, w_post, gate, w_pre, gate_kind)
+    dq = None if dw_post is None else a.flat("dw_post", dw_post, torch.float32, H)
+    dp = None if dw_pre is None else a.flat("dw_pre", dw_pre, torch.float32, H)
+    dg = None if dgate is None else a.flat("dgate", dgate, torch.float32, T if gate_kind == MOE_GATE_TOKEN else H)
+    w, wn = a.workspace(ws, lib.moe_block_norm_workspace(T, H))
+    cfg = moe_norm_config(T, H, fmt["h"] or 0, fmt["y"] or 0, fmt["x"] or 0, gate_kind, alpha, eps,
+                          ld["h"], ld["y"], ld["x"])
+    a.call(stream, ctypes.byref(cfg), ptr["h_out"], ptr["y"], q, g, p, ptr["dh_out"], ptr["dx"], ptr["dh"], ptr["dy"],
+           dq, dg, dp, w, wn)
+
+
+def moe_decode_block(ctx: Ctx, layer, x, T, logit_bias, topk_idx, topk_w, slot_idx, y, norm: moe_norm_config, h,
+                     w_post=None, gate=None, w_pre=None, x_next=None, stream=None) -> None:
+    """One decode layer step (moe_decode_layer into y) and moe_block_norm of y into h, in place, and x_next."""
+    _check(ctx, lib.moe_decode_block(ctx.handle, layer, _ptr(x), T, _ptr(logit_bias), _ptr(topk_idx), _ptr(topk_w),
+                                     _ptr(slot_idx), _ptr(y), ctypes.byref(norm), _ptr(h), _ptr(w_post), _ptr(gate),
+                                     _ptr(w_pre), _ptr(x_next), _stream(stream)), "moe_decode_block")

@@ -243,6 +243,9 @@ void launch_mx_quant(int afmt, const void* x, uint8_t* codes, uint8_t* scales, i
 void launch_prefill_gemm1_mx(const PrefillArgs& a, int max_tiles_m, hipStream_t s, Timing tm = {});
 void launch_prefill_gemm2_mx(const PrefillArgs& a, int max_tiles_m, hipStream_t s, Timing tm = {});
 void launch_prefill_combine(const PrefillArgs& a, hipStream_t s);
+// moe_block_norm; check_only: its argument checks alone (nothing is enqueued).
+moe_status block_norm(const moe_norm_config* cfg, const void* h, const void* y, const float* w_post, const float* gate,
+                      const float* w_pre, void* h_out, void* x_out, hipStream_t s, bool check_only);
 
 // ---------------------------------------------------------------- CPU branch
 struct CpuPool {

@@ -913,6 +913,23 @@ MOE_API moe_status moe_decode_layer(moe_ctx* ctx, int32_t layer, const void* x, 
   return moe_ffn_decode(ctx, layer, x, T, topk_idx, topk_w, slot_idx, y, stream);
 }
 
+MOE_API moe_status moe_decode_block(moe_ctx* ctx, int32_t layer, const void* x, int32_t T, const float* logit_bias,
+                                    int32_t* topk_idx, float* topk_w, int32_t* slot_idx, float* y,
+                                    const moe_norm_config* norm, void* h, const float* w_post, const float* gate,
+                                    const float* w_pre, void* x_next, moe_stream_t stream) {
+  if (!ctx) return MOE_EINVAL;
+  CHECK_ARG(norm && norm->T == T && norm->H == ctx->cfg.hidden, "norm: T and H must be the step's");
+  CHECK_ARG(norm->y_fmt == MOE_AFMT_F32 && (norm->ld_y == 0 || norm->ld_y == norm->H), "norm: y is fp32 with dense rows");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  CHECK_ARG(y && block_norm(norm, h, y, w_post, gate, w_pre, h, x_next, s, true) == MOE_OK,
+            "norm: bad format, stride, gate, alignment or overlap");
+  const moe_status st = moe_decode_layer(ctx, layer, x, T, logit_bias, topk_idx, topk_w, slot_idx, y, stream);
+  if (st != MOE_OK) return st;
+  if (block_norm(norm, h, y, w_post, gate, w_pre, h, x_next, s, false) != MOE_OK)
+    return fail(ctx, MOE_EHIP, "block norm launch failed");
+  return MOE_OK;
+}
+
 MOE_API moe_status moe_ffn_decode(moe_ctx* ctx, int32_t layer, const void* x, int32_t T, const int32_t* topk_idx,
                                   const float* topk_w, const int32_t* slot_idx, float* y, moe_stream_t stream) {
   if (!ctx) return MOE_EINVAL;
