@@ -9,6 +9,7 @@ this package fails when the compiled library is missing.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch  # noqa: F401  (loads the HIP runtime the library links against)
@@ -476,72 +477,94 @@ def moe_permute_noalloc(slot_idx, P: int, n_slot_range: int, perm, offsets, grou
 _FMT = {torch.float32: MOE_AFMT_F32, torch.bfloat16: MOE_AFMT_BF16}
 
 
+# the current stream's handle and the current device without the objects around them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 class _Args:
-    """Checks the tensors of one call and holds the device they share."""
+    """Checks the tensors of one call and holds the device they share.  A decode step makes these
+    calls once a layer, so a check reads each property of a tensor once."""
+    __slots__ = ("where", "dev")
 
     def __init__(self, where: str):
         self.where = where
-        self.device = None
+        self.dev = None
 
     def refuse(self, msg: str):
         raise MoeError(MOE_EINVAL, self.where, msg)
 
-    def _place(self, name, t):
-        if not t.is_cuda:
-            self.refuse(f"{name} must be on the GPU")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            self.refuse(f"{name} is on {t.device}, other tensors on {self.device}")
+    def place(self, name, t):
+        d = t.get_device()
+        if d != self.dev:
+            if d < 0:
+                self.refuse(f"{name} must be on the GPU")
+            if self.dev is not None:
+                self.refuse(f"{name} is on cuda:{d}, other tensors on cuda:{self.dev}")
+            self.dev = d
 
     def rows(self, name, t, n_rows=None, width=None, dense=False, like=None):
-        """(pointer, format, row stride) of a [rows, H] matrix with contiguous rows."""
-        if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _FMT:
+        """(pointer, format, row stride, rows, H) of a [rows, H] matrix with contiguous rows."""
+        try:
+            fmt = _FMT[t.dtype]
+            n, h = t.shape
+            ld, step = t.stride()
+        except (AttributeError, KeyError, ValueError):
             self.refuse(f"{name} must be a two-dimensional fp32 or bf16 tensor")
-        n, h = t.shape
         if n < 1 or h < 1 or (n_rows is not None and n != n_rows) or (width is not None and h != width):
-            self.refuse(f"{name} has shape {tuple(t.shape)}, not {(n_rows or 'T', width or 'H')}")
-        ld = h if n == 1 else t.stride(0)
-        if (h > 1 and t.stride(1) != 1) or ld < h or (dense and ld != h):
+            self.refuse(f"{name} has shape {(n, h)}, not {(n_rows or 'T', width or 'H')}")
+        if n == 1:
+            ld = h
+        if (step != 1 and h > 1) or ld < h or (dense and ld != h):
             self.refuse(f"{name} needs contiguous rows" + (" without gaps" if dense else ""))
-        if like is not None and (t.dtype != like.dtype or (n > 1 and ld != like.stride(0))):
+        if like is not None and (fmt, ld) != like:
             self.refuse(f"{name} must have the type and row stride of the tensor it belongs to")
-        self._place(name, t)
-        return t.data_ptr(), _FMT[t.dtype], ld
+        self.place(name, t)
+        return t.data_ptr(), fmt, ld, n, h
 
     def flat(self, name, t, dtype, *shape):
-        """Pointer of a dense tensor of this type and shape (the shape as a whole: numel for one number)."""
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_contiguous():
+        """Pointer of a dense tensor of this type and shape (one number: that many elements)."""
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous():
             self.refuse(f"{name} must be a contiguous {dtype} tensor")
-        if tuple(t.shape) != shape and not (len(shape) == 1 and t.numel() == shape[0]):
+        if t.shape != shape and not (len(shape) == 1 and t.numel() == shape[0]):
             self.refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
-        self._place(name, t)
+        self.place(name, t)
         return t.data_ptr()
 
-    def workspace(self, t, need):
+    def pairs(self, name, t):
+        """(T, k, pointer) of an int32 [T, k] table."""
+        if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.numel() < 1:
+            self.refuse(f"{name} must be an int32 tensor [T, k]")
+        T, k = t.shape
+        return T, k, self.flat(name, t, torch.int32, T, k)
+
+    def workspace(self, t):
         """(pointer, bytes) of the caller's workspace."""
-        if need < 0:
-            self.refuse("shape out of range")
         if t is None:
             return None, 0
         if not isinstance(t, torch.Tensor) or not t.is_contiguous():
             self.refuse("ws must be a contiguous tensor")
-        if t.numel():
-            self._place("ws", t)
-        return t.data_ptr() or None, t.numel() * t.element_size()
+        n = t.numel() * t.element_size()
+        if not n:
+            return None, 0
+        self.place("ws", t)
+        return t.data_ptr(), n
 
-    def call(self, stream, *args):
+    def call(self, fn, stream, *args):
         """Forward to the C entry point on `stream` (default: the current stream of the tensors' device)."""
-        dev = self.device.index
-        if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
-            self.refuse(f"stream is on {stream.device}, tensors on {self.device}")
-        s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
-        if torch.cuda.current_device() == dev:
-            st = getattr(lib, self.where)(*args, s)
+        dev = self.dev
+        if stream is None:
+            s = _raw_stream(dev)
+        else:
+            if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+                self.refuse(f"stream is on {stream.device}, tensors on cuda:{dev}")
+            s = _stream(stream)
+        if _current_device() == dev:
+            st = fn(*args, s)
         else:
             with torch.cuda.device(dev):
-                st = getattr(lib, self.where)(*args, s)
-        if st != MOE_OK:
+                st = fn(*args, s)
+        if st:
             raise MoeError(st, self.where, "launch failure" if st == MOE_EHIP else
                            "shape out of range, overlapping tensors, missing argument or short workspace")
 
@@ -554,85 +577,79 @@ def moe_dispatch_workspace(T: int, k: int, n_experts: int) -> int:
     return n
 
 
-def _pairs(a: _Args, name, idx):
-    if not isinstance(idx, torch.Tensor) or idx.dim() != 2 or idx.numel() < 1:
-        a.refuse(f"{name} must be an int32 tensor [T, k]")
-    T, k = idx.shape
-    return T, k, a.flat(name, idx, torch.int32, T, k)
-
-
 def moe_dispatch(topk_idx, n_experts: int, x, xs, perm, inv, offsets, ws=None, stream=None) -> None:
     """Sort the pairs of topk_idx [T,k] by expert into perm [T*k], inv [T,k] and offsets [n_experts+1], and
     move the rows of x [T,H] to xs [T*k,H] (both None: sort only).  ws: uint8 workspace."""
     a = _Args("moe_dispatch")
-    T, k, idx = _pairs(a, "topk_idx", topk_idx)
+    T, k, idx = a.pairs("topk_idx", topk_idx)
+    P = T * k
     xp = xsp = None
     fmt = H = ld = 0
     if x is not None or xs is not None:
-        xp, fmt, ld = a.rows("x", x, T)
-        H = x.shape[1]
-        xsp, xs_fmt, _ = a.rows("xs", xs, T * k, H, dense=True)
+        xp, fmt, ld, _, H = a.rows("x", x, T)
+        xsp, xs_fmt, _, _, _ = a.rows("xs", xs, P, H, True)
         if xs_fmt != fmt:
             a.refuse("xs must have x's type")
-    p = a.flat("perm", perm, torch.int32, T * k)
+    p = a.flat("perm", perm, torch.int32, P)
     i = a.flat("inv", inv, torch.int32, T, k)
     o = a.flat("offsets", offsets, torch.int32, n_experts + 1)
-    w, wn = a.workspace(ws, lib.moe_dispatch_workspace(T, k, n_experts))
-    a.call(stream, idx, T, k, n_experts, xp, fmt, H, ld, xsp, p, i, o, w, wn)
+    w, wn = a.workspace(ws)
+    a.call(lib.moe_dispatch, stream, idx, T, k, n_experts, xp, fmt, H, ld, xsp, p, i, o, w, wn)
 
 
 def moe_dispatch_backward(dxs, inv, dx, stream=None) -> None:
     """dx [T,H] = the sum of each token's rows of dxs [T*k,H]."""
     a = _Args("moe_dispatch_backward")
-    T, k, i = _pairs(a, "inv", inv)
-    g, fmt, _ = a.rows("dxs", dxs, T * k, dense=True)
-    H = dxs.shape[1]
-    o, o_fmt, ld = a.rows("dx", dx, T, H)
-    a.call(stream, g, fmt, i, T, k, H, o, o_fmt, ld)
+    T, k, i = a.pairs("inv", inv)
+    g, fmt, _, _, H = a.rows("dxs", dxs, T * k, None, True)
+    o, o_fmt, ld, _, _ = a.rows("dx", dx, T, H)
+    a.call(lib.moe_dispatch_backward, stream, g, fmt, i, T, k, H, o, o_fmt, ld)
 
 
 def moe_combine(ys, inv, w, y, stream=None) -> None:
     """y [T,H] = the sum of each token's rows of ys [T*k,H] weighted by w [T,k] (fp32)."""
     a = _Args("moe_combine")
-    T, k, i = _pairs(a, "inv", inv)
-    r, fmt, _ = a.rows("ys", ys, T * k, dense=True)
-    H = ys.shape[1]
+    T, k, i = a.pairs("inv", inv)
+    r, fmt, _, _, H = a.rows("ys", ys, T * k, None, True)
     wp = a.flat("w", w, torch.float32, T, k)
-    o, o_fmt, ld = a.rows("y", y, T, H)
-    a.call(stream, r, fmt, i, wp, T, k, H, o, o_fmt, ld)
+    o, o_fmt, ld, _, _ = a.rows("y", y, T, H)
+    a.call(lib.moe_combine, stream, r, fmt, i, wp, T, k, H, o, o_fmt, ld)
 
 
 def moe_combine_backward(dy, ys, inv, w, dys, dw, stream=None) -> None:
     """From dy [T,H]: dys [T*k,H] (or None; may be ys) and dw [T,k] (or None, then ys may be None)."""
     a = _Args("moe_combine_backward")
-    T, k, i = _pairs(a, "inv", inv)
-    d, d_fmt, ld = a.rows("dy", dy, T)
-    H = dy.shape[1]
+    T, k, i = a.pairs("inv", inv)
+    d, d_fmt, ld, _, H = a.rows("dy", dy, T)
     r = o = wp = g = None
     fmt = d_fmt
     if dys is not None:
-        o, fmt, _ = a.rows("dys", dys, T * k, H, dense=True)
+        o, fmt, _, _, _ = a.rows("dys", dys, T * k, H, True)
         wp = a.flat("w", w, torch.float32, T, k)
     if dw is not None:
-        r, r_fmt, _ = a.rows("ys", ys, T * k, H, dense=True)
+        r, r_fmt, _, _, _ = a.rows("ys", ys, T * k, H, True)
         if dys is not None and r_fmt != fmt:
             a.refuse("dys must have ys's type")
         fmt = r_fmt
         g = a.flat("dw", dw, torch.float32, T, k)
-    a.call(stream, d, d_fmt, ld, r, fmt, i, wp, T, k, H, o, g)
+    a.call(lib.moe_combine_backward, stream, d, d_fmt, ld, r, fmt, i, wp, T, k, H, o, g)
 
 
 def moe_topk_backward(logits, topk_idx, dw, renorm: int, dlogits, stream=None) -> None:
     """dlogits [T,E] from the gates' gradients dw [T,k] at the chosen experts topk_idx [T,k]."""
     a = _Args("moe_topk_backward")
-    T, k, idx = _pairs(a, "topk_idx", topk_idx)
+    T, k, idx = a.pairs("topk_idx", topk_idx)
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         a.refuse("logits must be fp32 [T, E]")
     E = logits.shape[1]
     z = a.flat("logits", logits, torch.float32, T, E)
     g = a.flat("dw", dw, torch.float32, T, k)
     o = a.flat("dlogits", dlogits, torch.float32, T, E)
-    a.call(stream, z, T, E, idx, k, g, int(renorm), o)
+    a.call(lib.moe_topk_backward, stream, z, T, E, idx, k, g, renorm, o)
+
+
+# The configuration of a norm call, by its values (the library reads it during the call only).
+_norm_config = functools.lru_cache(maxsize=1024)(lambda *fields: ctypes.pointer(moe_norm_config(*fields)))
 
 
 def _norm_inputs(a: _Args, T, H, w_post, gate, w_pre, gate_kind):
@@ -648,20 +665,19 @@ def moe_block_norm(h, y=None, w_post=None, gate=None, w_pre=None, h_out=None, x_
                    gate_kind: int = MOE_GATE_NONE, alpha: float = 1.0, eps: float = 1e-6, stream=None) -> None:
     """h_out = h + alpha gate norm(y; w_post), x_out = norm(h_out; w_pre): the step between two blocks."""
     a = _Args("moe_block_norm")
-    hp, h_fmt, ld_h = a.rows("h", h)
-    T, H = h.shape
+    hp, h_fmt, ld_h, T, H = a.rows("h", h)
     yp = ho = xo = None
     y_fmt = x_fmt = h_fmt
     ld_y = ld_x = H
     if y is not None:
-        yp, y_fmt, ld_y = a.rows("y", y, T, H)
+        yp, y_fmt, ld_y, _, _ = a.rows("y", y, T, H)
     if h_out is not None:
-        ho = a.rows("h_out", h_out, T, H, like=h)[0]
+        ho = hp if h_out is h else a.rows("h_out", h_out, T, H, False, (h_fmt, ld_h))[0]
     if x_out is not None:
-        xo, x_fmt, ld_x = a.rows("x_out", x_out, T, H)
+        xo, x_fmt, ld_x, _, _ = a.rows("x_out", x_out, T, H)
     q, g, p = _norm_inputs(a, T, H, w_post, gate, w_pre, gate_kind)
-    cfg = moe_norm_config(T, H, h_fmt, y_fmt, x_fmt, gate_kind, alpha, eps, ld_h, ld_y, ld_x)
-    a.call(stream, ctypes.byref(cfg), hp, yp, q, g, p, ho, xo)
+    a.call(lib.moe_block_norm, stream, _norm_config(T, H, h_fmt, y_fmt, x_fmt, gate_kind, alpha, eps, ld_h, ld_y, ld_x),
+           hp, yp, q, g, p, ho, xo)
 
 
 def moe_block_norm_workspace(T: int, H: int) -> int:
@@ -681,26 +697,36 @@ def moe_block_norm_backward(h_out, y, w_post, gate, w_pre, dh_out, dx, dh, dy, d
     if not isinstance(lead, torch.Tensor) or lead.dim() != 2:
         a.refuse("dh_out or dx must be given")
     T, H = lead.shape
-    ptr = {}
-    fmt = {"h": None, "y": None, "x": None}
-    ld = {"h": H, "y": H, "x": H}
-    first = {"h": None, "y": None, "x": None}
-    for name, t, kind in (("h_out", h_out, "h"), ("dh_out", dh_out, "h"), ("dh", dh, "h"), ("y", y, "y"), ("dy", dy, "y"),
-                          ("dx", dx, "x")):
-        if t is None:
-            ptr[name] = None
-            continue
-        ptr[name], fmt[kind], ld[kind] = a.rows(name, t, T, H, like=first[kind])
-        first[kind] = t if first[kind] is None else first[kind]
+    h_like = y_like = None
+    hp = yp = dhp = dxp = o_h = o_y = None
+    x_fmt, ld_x = 0, H
+    if dh_out is not None:
+        dhp, *h_like = a.rows("dh_out", dh_out, T, H)[:3]
+        h_like = tuple(h_like)
+    if h_out is not None:
+        hp, *like = a.rows("h_out", h_out, T, H, False, h_like)[:3]
+        h_like = tuple(like)
+    if dh is not None:
+        o_h, *like = a.rows("dh", dh, T, H, False, h_like)[:3]
+        h_like = tuple(like)
+    if y is not None:
+        yp, *like = a.rows("y", y, T, H)[:3]
+        y_like = tuple(like)
+    if dy is not None:
+        o_y, *like = a.rows("dy", dy, T, H, False, y_like)[:3]
+        y_like = tuple(like)
+    if dx is not None:
+        dxp, x_fmt, ld_x, _, _ = a.rows("dx", dx, T, H)
+    h_fmt, ld_h = h_like or (0, H)
+    y_fmt, ld_y = y_like or (0, H)
     q, g, p = _norm_inputs(a, T, H, w_post, gate, w_pre, gate_kind)
     dq = None if dw_post is None else a.flat("dw_post", dw_post, torch.float32, H)
     dp = None if dw_pre is None else a.flat("dw_pre", dw_pre, torch.float32, H)
     dg = None if dgate is None else a.flat("dgate", dgate, torch.float32, T if gate_kind == MOE_GATE_TOKEN else H)
-    w, wn = a.workspace(ws, lib.moe_block_norm_workspace(T, H))
-    cfg = moe_norm_config(T, H, fmt["h"] or 0, fmt["y"] or 0, fmt["x"] or 0, gate_kind, alpha, eps,
-                          ld["h"], ld["y"], ld["x"])
-    a.call(stream, ctypes.byref(cfg), ptr["h_out"], ptr["y"], q, g, p, ptr["dh_out"], ptr["dx"], ptr["dh"], ptr["dy"],
-           dq, dg, dp, w, wn)
+    w, wn = a.workspace(ws)
+    a.call(lib.moe_block_norm_backward, stream,
+           _norm_config(T, H, h_fmt, y_fmt, x_fmt, gate_kind, alpha, eps, ld_h, ld_y, ld_x),
+           hp, yp, q, g, p, dhp, dxp, o_h, o_y, dq, dg, dp, w, wn)
 
 
 def moe_decode_block(ctx: Ctx, layer, x, T, logit_bias, topk_idx, topk_w, slot_idx, y, norm: moe_norm_config, h,

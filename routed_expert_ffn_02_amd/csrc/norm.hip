@@ -49,21 +49,17 @@ __device__ __forceinline__ void block_sum(float (&v)[NV], float (*s_red)[NV]) {
   }
 }
 
-// fp32 weights of a chunk, `fill` behind the row's end and where there are none.
-__device__ __forceinline__ void load_w(const float* w, int i, int H, float fill, float (&v)[kNormN]) {
-  if (!w) {
-#pragma unroll
-    for (int n = 0; n < kNormN; ++n) v[n] = fill;
-    return;
-  }
+// fp32 weights of a chunk, 1 where there are none.
+__device__ __forceinline__ void load_w(const float* w, const Piece<kNormN>& at, float (&v)[kNormN]) {
   Chunk<MOE_AFMT_F32, kNormN> q;
-  q.load(reinterpret_cast<const uint8_t*>(w + i), H - i);
+  if (w && at.on) q.load(reinterpret_cast<const uint8_t*>(w), at);
 #pragma unroll
-  for (int n = 0; n < kNormN; ++n) v[n] = q.get(n);
+  for (int n = 0; n < kNormN; ++n) v[n] = w && at.on ? q.get(n) : 1.f;
 }
 
-// One workgroup per row, C chunks of 8 elements per thread.  h_out may be h: a thread has
-// read its own chunks before it writes them.
+// One workgroup per row, C chunks of 8 elements per thread.  h_out may be h: a thread writes
+// only elements that it alone has read for sums and sums, and no other thread's reads of
+// them count.
 template <int HF, int YF, int XF, int C>
 __global__ __launch_bounds__(64 * kNormMaxWaves) void block_norm_kernel(NormArgs a) {
   constexpr int N = kNormN;
@@ -72,11 +68,15 @@ __global__ __launch_bounds__(64 * kNormMaxWaves) void block_norm_kernel(NormArgs
   const int H = a.H;
   Chunk<HF, N> qh[C];
   Chunk<YF, N> qy[C];
+  float wq[C][N], g[C][N], wp[C][N];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int i = (threadIdx.x + c * blockDim.x) * N;
-    qh[c].load(a.h + t * a.h_pitch + (int64_t)i * kElemBytes<HF>, H - i);
-    if (a.y) qy[c].load(a.y + t * a.y_pitch + (int64_t)i * kElemBytes<YF>, H - i);
+    const Piece<N> at(threadIdx.x + c * blockDim.x, H);
+    if (a.y) qy[c].load_own(a.y + t * a.y_pitch, at);
+    qh[c].load_own(a.h + t * a.h_pitch, at);
+    load_w(a.w_post, at, wq[c]);
+    load_w(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, at, g[c]);
+    load_w(a.w_pre, at, wp[c]);
   }
   float h[C][N];
 #pragma unroll
@@ -97,17 +97,12 @@ __global__ __launch_bounds__(64 * kNormMaxWaves) void block_norm_kernel(NormArgs
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int i = (threadIdx.x + c * blockDim.x) * N;
-      float wq[N], g[N];
-      load_w(a.w_post, i, H, 1.f, wq);
-      load_w(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, i, H, 1.f, g);
+      const Piece<N> at(threadIdx.x + c * blockDim.x, H);
 #pragma unroll
-      for (int n = 0; n < N; ++n) h[c][n] = fmaf(scale * qy[c].get(n), wq[n] * g[n], h[c][n]);
-      if (a.h_out) {
-        Chunk<HF, N> o;
-        o.set(h[c]);
-        o.store(a.h_out + t * a.h_pitch + (int64_t)i * kElemBytes<HF>, H - i);
-      }
+      for (int n = 0; n < N; ++n) h[c][n] = fmaf(scale * qy[c].get(n), wq[c][n] * g[c][n], h[c][n]);
+      Chunk<HF, N> o;
+      o.set(h[c]);
+      o.template store_own<true>(a.h_out + t * a.h_pitch, at);
     }
   }
   if (!a.x_out) return;
@@ -120,16 +115,38 @@ __global__ __launch_bounds__(64 * kNormMaxWaves) void block_norm_kernel(NormArgs
   const float r = 1.f / sqrtf(s[0] / H + a.eps);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int i = (threadIdx.x + c * blockDim.x) * N;
-    float wp[N];
-    load_w(a.w_pre, i, H, 1.f, wp);
+    const Piece<N> at(threadIdx.x + c * blockDim.x, H);
 #pragma unroll
-    for (int n = 0; n < N; ++n) wp[n] = h[c][n] * r * wp[n];
+    for (int n = 0; n < N; ++n) wp[c][n] = h[c][n] * r * wp[c][n];
     Chunk<XF, N> o;
-    o.set(wp);
-    o.store(a.x_out + t * a.x_pitch + (int64_t)i * kElemBytes<XF>, H - i);
+    o.set(wp[c]);
+    o.template store_own<true>(a.x_out + t * a.x_pitch, at);
   }
 }
+
+// The rows of one token in the gradient, as stored; zeros for a gradient that does not come in.
+template <int HF, int YF, int XF, int C>
+struct NormRows {
+  Chunk<HF, kNormN> h[C], d[C];
+  Chunk<YF, kNormN> y[C];
+  Chunk<XF, kNormN> x[C];
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t t) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const Piece<kNormN> at(threadIdx.x + c * blockDim.x, a.H);
+      h[c].zero();
+      x[c].zero();
+      d[c].zero();
+      y[c].zero();
+      if (a.dx) {
+        h[c].load_own(a.h + t * a.h_pitch, at);
+        x[c].load_own(a.dx + t * a.x_pitch, at);
+      }
+      if (a.dh_in) d[c].load_own(a.dh_in + t * a.h_pitch, at);
+      if (a.y) y[c].load_own(a.y + t * a.y_pitch, at);
+    }
+  }
+};
 
 // The gradient.  With r = 1 / rms(h'), d = w_pre dx, ry = 1 / rms(y), D = sum(dh' g_c w_post y):
 //   dh = dh' + r (d - h' r^2 mean(d h'))          (dh' from the stream behind the block)
@@ -137,42 +154,41 @@ __global__ __launch_bounds__(64 * kNormMaxWaves) void block_norm_kernel(NormArgs
 //   dw_pre = sum_t dx h' r,  dw_post = sum_t du y ry,  dgate = alpha sum dh u
 // A workgroup walks rows b, b + G, ...; its threads keep the weights' gradients of their
 // own channels in registers over those rows and write one partial row at the end, which
-// norm_reduce adds in workgroup order: no atomics, the same bits every time.
-template <int HF, int YF, int XF, int C>
-__global__ __launch_bounds__(64 * kNormMaxWaves) void block_norm_backward_kernel(NormArgs a) {
+// norm_reduce adds in workgroup order: no atomics, the same bits every time.  AHEAD: the
+// next row is loaded before the current one's sums.
+template <int HF, int YF, int XF, int C, int WAVES, bool AHEAD>
+__global__ __launch_bounds__(64 * WAVES) void block_norm_backward_kernel(NormArgs a) {
   constexpr int N = kNormN;
-  __shared__ float s_a[kNormMaxWaves][3], s_b[kNormMaxWaves][1];
+  __shared__ float s_a[WAVES][3], s_b[WAVES][1];
   const int H = a.H;
   float wp[C][N], wq[C][N], gc[C][N], acc_pre[C][N], acc_post[C][N], acc_gate[C][N];
+  NormRows<HF, YF, XF, C> next;
+  if (AHEAD) next.load(a, blockIdx.x);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int i = (threadIdx.x + c * blockDim.x) * N;
-    load_w(a.w_pre, i, H, 1.f, wp[c]);
-    load_w(a.w_post, i, H, 1.f, wq[c]);
-    load_w(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, i, H, 1.f, gc[c]);
+    const Piece<N> at(threadIdx.x + c * blockDim.x, H);
+    load_w(a.w_pre, at, wp[c]);
+    load_w(a.w_post, at, wq[c]);
+    load_w(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, at, gc[c]);
 #pragma unroll
     for (int n = 0; n < N; ++n) acc_pre[c][n] = acc_post[c][n] = acc_gate[c][n] = 0.f;
   }
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    Chunk<HF, N> qh[C], qd[C];
-    Chunk<YF, N> qy[C];
-    Chunk<XF, N> qx[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int i = (threadIdx.x + c * blockDim.x) * N;
-      qh[c].load(a.h + t * a.h_pitch + (int64_t)i * kElemBytes<HF>, a.dx ? H - i : 0);
-      qx[c].load(a.dx + t * a.x_pitch + (int64_t)i * kElemBytes<XF>, a.dx ? H - i : 0);
-      qd[c].load(a.dh_in + t * a.h_pitch + (int64_t)i * kElemBytes<HF>, a.dh_in ? H - i : 0);
-      qy[c].load(a.y + t * a.y_pitch + (int64_t)i * kElemBytes<YF>, a.y ? H - i : 0);
+    NormRows<HF, YF, XF, C> q;
+    if (AHEAD) {
+      q = next;
+      if (t + gridDim.x < a.T) next.load(a, t + gridDim.x);
+    } else {
+      q.load(a, t);
     }
     float s[3] = {0.f, 0.f, 0.f};  // sums of h'^2, d h', y^2
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const float hv = qh[c].get(n), yv = qy[c].get(n);
+        const float hv = q.h[c].get(n), yv = q.y[c].get(n);
         s[0] = fmaf(hv, hv, s[0]);
-        s[1] = fmaf(wp[c][n] * qx[c].get(n), hv, s[1]);
+        s[1] = fmaf(wp[c][n] * q.x[c].get(n), hv, s[1]);
         s[2] = fmaf(yv, yv, s[2]);
       }
     block_sum(s, s_a);
@@ -183,16 +199,15 @@ __global__ __launch_bounds__(64 * kNormMaxWaves) void block_norm_backward_kernel
     for (int c = 0; c < C; ++c) {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const float hv = qh[c].get(n), xv = qx[c].get(n);
-        dh[c][n] = fmaf(r, wp[c][n] * xv - hv * hm, qd[c].get(n));
+        const float hv = q.h[c].get(n), xv = q.x[c].get(n);
+        dh[c][n] = fmaf(r, wp[c][n] * xv - hv * hm, q.d[c].get(n));
         acc_pre[c][n] = fmaf(xv, hv * r, acc_pre[c][n]);
-        dot[0] = fmaf(dh[c][n] * gc[c][n] * wq[c][n], qy[c].get(n), dot[0]);
+        dot[0] = fmaf(dh[c][n] * gc[c][n] * wq[c][n], q.y[c].get(n), dot[0]);
       }
-      const int i = (threadIdx.x + c * blockDim.x) * N;
       if (a.dh) {
         Chunk<HF, N> o;
         o.set(dh[c]);
-        o.store(a.dh + t * a.h_pitch + (int64_t)i * kElemBytes<HF>, H - i);
+        o.template store_own<true>(a.dh + t * a.h_pitch, Piece<N>(threadIdx.x + c * blockDim.x, H));
       }
     }
     if (!a.y) continue;
@@ -205,27 +220,26 @@ __global__ __launch_bounds__(64 * kNormMaxWaves) void block_norm_backward_kernel
       float v[N];
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const float yv = qy[c].get(n), du = ag * gc[c][n] * dh[c][n], yr = yv * ry;
+        const float yv = q.y[c].get(n), du = ag * gc[c][n] * dh[c][n], yr = yv * ry;
         v[n] = ry * (wq[c][n] * du - yv * ym);
         acc_post[c][n] = fmaf(du, yr, acc_post[c][n]);
         acc_gate[c][n] = fmaf(a.alpha * dh[c][n], wq[c][n] * yr, acc_gate[c][n]);
       }
-      const int i = (threadIdx.x + c * blockDim.x) * N;
       if (a.dy) {
         Chunk<YF, N> o;
         o.set(v);
-        o.store(a.dy + t * a.y_pitch + (int64_t)i * kElemBytes<YF>, H - i);
+        o.template store_own<true>(a.dy + t * a.y_pitch, Piece<N>(threadIdx.x + c * blockDim.x, H));
       }
     }
   }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int i = (threadIdx.x + c * blockDim.x) * N;
+    const Piece<N> at(threadIdx.x + c * blockDim.x, H);
     const auto put = [&](int kind, const float(&v)[N]) {
       if (kind < 0) return;
       Chunk<MOE_AFMT_F32, N> o;
       o.set(v);
-      o.store(reinterpret_cast<uint8_t*>(a.part + ((int64_t)kind * gridDim.x + blockIdx.x) * H + i), H - i);
+      o.store_own(reinterpret_cast<uint8_t*>(a.part + ((int64_t)kind * gridDim.x + blockIdx.x) * H), at);
     };
     put(a.part_pre, acc_pre[c]);
     put(a.part_post, acc_post[c]);
@@ -244,7 +258,7 @@ __global__ __launch_bounds__(1024) void norm_reduce(const float* __restrict__ pa
   const float* p = part + (int64_t)blockIdx.y * G * H;
   float v = 0.f;
   if (i < H) {
-#pragma unroll 4
+#pragma unroll 16
     for (int g = wave; g < G; g += 16) v += p[(int64_t)g * H + i];
   }
   s_v[wave][lane] = v;
@@ -266,11 +280,13 @@ int norm_groups(int T) { return std::min(T, kNormGroups); }
 
 template <bool BACK, int HF, int YF, int XF>
 moe_status launch_norm_f(const NormArgs& a, int groups, hipStream_t s) {
-  const dim3 grid(groups), block(64 * norm_waves(a.H));
+  const int waves = norm_waves(a.H);
+  const dim3 grid(groups), block(64 * waves);
   const bool two = a.H > 64 * kNormMaxWaves * kNormN;
   if constexpr (BACK) {
-    if (two) return launch(block_norm_backward_kernel<HF, YF, XF, 2>, grid, block, s, a);
-    return launch(block_norm_backward_kernel<HF, YF, XF, 1>, grid, block, s, a);
+    if (two) return launch(block_norm_backward_kernel<HF, YF, XF, 2, kNormMaxWaves, false>, grid, block, s, a);
+    if (waves > 8) return launch(block_norm_backward_kernel<HF, YF, XF, 1, kNormMaxWaves, false>, grid, block, s, a);
+    return launch(block_norm_backward_kernel<HF, YF, XF, 1, 8, true>, grid, block, s, a);
   } else {
     if (two) return launch(block_norm_kernel<HF, YF, XF, 2>, grid, block, s, a);
     return launch(block_norm_kernel<HF, YF, XF, 1>, grid, block, s, a);

@@ -19,19 +19,47 @@ constexpr int kMoveMaxK = 1024;          // ranks
 constexpr int64_t kMoveMaxPairs = 1 << 26;
 
 // ---------------------------------------------------------------------------
-// The sort: a counting sort in two launches over at most kSortBlocks chunks of pairs (their
-// number, not their size, is bounded, so a chunk's base stays a sum over at most that many
-// histogram rows however long the prompt).
-constexpr int kSortBlocks = 256;
-constexpr int kSortThreads = 256;
+// The sort: a counting sort, stable by construction (a pair's place is the number of kept
+// pairs before it under (expert, pair)).  Three forms by the number of pairs P:
+//   P <= kTinyPairs   the kernel that moves the rows counts for itself: every wavefront holds
+//                     all keys in registers and a place is one compare and count per 64 pairs
+//   P <= kSolePairs   one launch sorts: each workgroup counts all pairs in LDS, those before
+//                     its own chunk apart from the others
+//   beyond            dispatch_count leaves one histogram per chunk, dispatch_place sums them;
+//                     the chunks grow with P so that there are at most kSortChunks of them
+constexpr int kTinyPairs = 1024;
+constexpr int kSolePairs = 1 << 16;
+constexpr int kSortChunks = 256;
+constexpr int kSortThreads = 1024;
 
 struct SortPlan {
   int chunk, blocks;  // pairs per workgroup (a multiple of kSortThreads) and workgroups
 };
 inline SortPlan sort_plan(int64_t P) {
-  const int64_t per = (P + kSortBlocks - 1) / kSortBlocks;
+  const int64_t per = (P + kSortChunks - 1) / kSortChunks;
   const int chunk = (int)((per + kSortThreads - 1) / kSortThreads * kSortThreads);
   return {chunk, (int)((P + chunk - 1) / chunk)};
+}
+
+// Exclusive prefix of one int per thread over the workgroup (a multiple of 64 threads);
+// *total receives the sum.  s_wave: one int per wavefront.
+__device__ __forceinline__ int group_prefix(int v, int* s_wave, int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 63) s_wave[wave] = x;
+  __syncthreads();
+  int base = 0, sum = 0;
+  for (int w = 0; w < nw; ++w) {
+    base += w < wave ? s_wave[w] : 0;
+    sum += s_wave[w];
+  }
+  *total = sum;
+  return base + x - v;
 }
 
 __global__ __launch_bounds__(kSortThreads) void dispatch_count(const int32_t* __restrict__ idx, int P, int E, int chunk,
@@ -48,8 +76,8 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_count(const int32_t* __
   for (int e = threadIdx.x; e < E; e += kSortThreads) hist[(size_t)blockIdx.x * E + e] = s_n[e];
 }
 
-// Lanes of the wavefront whose key equals this lane's (key < 2^bits; the inactive pass
-// valid = false and get 0).
+// Lanes of the wavefront whose key equals this lane's (key < 2^bits; a lane with valid =
+// false gets 0).
 __device__ __forceinline__ uint64_t wave_peers(int key, bool valid, int bits) {
   uint64_t m = __ballot(valid);
   for (int b = 0; b < bits; ++b) {
@@ -59,117 +87,234 @@ __device__ __forceinline__ uint64_t wave_peers(int key, bool valid, int bits) {
   return valid ? m : 0;
 }
 
+// One workgroup per chunk.  SOLE: counts all pairs itself (hist unused); otherwise sums the
+// chunks' histograms.  Within the chunk a pair's place is its expert's base plus its rank
+// among the wavefront's lanes of the same expert plus what earlier wavefronts have of it.
+template <bool SOLE>
 __global__ __launch_bounds__(kSortThreads) void dispatch_place(const int32_t* __restrict__ idx, int P, int E, int bits,
                                                                int chunk, const int32_t* __restrict__ hist,
                                                                int32_t* __restrict__ perm, int32_t* __restrict__ inv,
                                                                int32_t* __restrict__ offsets) {
-  __shared__ int s_base[kMaxExperts];
-  __shared__ int s_wave[kSortThreads / 64];
+  constexpr int kWaves = kSortThreads / 64;
+  __shared__ int s_before[kMaxExperts], s_rest[kMaxExperts];
+  __shared__ uint16_t s_cnt[kWaves][kMaxExperts];
+  __shared__ int s_wave[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int nblk = gridDim.x, blk = blockIdx.x;
-  // an expert's first position in this chunk: kept pairs of lower experts, then its own
-  // pairs in earlier chunks
-  int carry = 0;
-  for (int e0 = 0; e0 < E; e0 += kSortThreads) {
-    const int e = e0 + tid;
-    int total = 0, before = 0;
-    if (e < E) {
-#pragma unroll 8
-      for (int c = 0; c < nblk; ++c) {
-        const int v = hist[(size_t)c * E + e];
-        total += v;
-        before += c < blk ? v : 0;
+  const int blk = blockIdx.x, lo = blk * chunk, hi = min(lo + chunk, P);
+  int mine = lo + tid < hi ? idx[lo + tid] : -1;  // the first round's pair
+  if (tid < E) s_before[tid] = s_rest[tid] = 0;
+  __syncthreads();
+  if constexpr (SOLE) {
+    // 32 pairs per thread in flight, four to a load (chunks are multiples of four, so four
+    // neighbours lie on one side of lo)
+    constexpr int kLoads = 8;
+    for (int p0 = 4 * tid; p0 < P; p0 += 4 * kLoads * kSortThreads) {
+      u32x4 e[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int p = p0 + 4 * u * kSortThreads;
+        e[u] = ~(u32x4)0;
+        if (p + 4 <= P) e[u] = load16<false>(reinterpret_cast<const uint8_t*>(idx + p));
+        else
+          for (int i = 0; i < 4; ++i)
+            if (p + i < P) e[u][i] = idx[p + i];
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        int* side = p0 + 4 * u * kSortThreads < lo ? s_before : s_rest;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (e[u][i] < (unsigned)E) atomicAdd(&side[e[u][i]], 1);
       }
     }
-    int x = total;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int y = __shfl_up(x, off);
-      if (lane >= off) x += y;
+  } else {
+    // the threads of an expert share its column of the histograms
+    const int parts = kSortThreads / E, e = tid % E, part = tid / E, nblk = gridDim.x;
+    if (part < parts) {
+      int before = 0, rest = 0;
+#pragma unroll 16
+      for (int c = part; c < nblk; c += parts) {
+        const int v = hist[(size_t)c * E + e];
+        before += c < blk ? v : 0;
+        rest += c < blk ? 0 : v;
+      }
+      atomicAdd(&s_before[e], before);
+      atomicAdd(&s_rest[e], rest);
     }
-    if (lane == 63) s_wave[wave] = x;
-    __syncthreads();
-    int base = carry;
-    for (int w = 0; w < kSortThreads / 64; ++w) {
-      if (w < wave) base += s_wave[w];
-      carry += s_wave[w];
-    }
-    base += x - total;
-    if (e < E) {
-      s_base[e] = base + before;
-      if (blk == 0) offsets[e] = base;
-    }
-    __syncthreads();
   }
-  if (blk == 0 && tid == 0) offsets[E] = carry;
-  // the chunk's pairs in order, 256 at a time, wavefront after wavefront
-  const int lo = blk * chunk, hi = min(lo + chunk, P);
+  __syncthreads();
+  // an expert's first place in this chunk: kept pairs of lower experts, then its own pairs
+  // in earlier chunks
+  const int before = tid < E ? s_before[tid] : 0;
+  int kept_all;
+  const int base = group_prefix(before + (tid < E ? s_rest[tid] : 0), s_wave, &kept_all);
+  if (blk == 0) {
+    if (tid < E) offsets[tid] = base;
+    if (tid == 0) offsets[E] = kept_all;
+  }
+  if (tid < E) s_before[tid] = base + before;
   for (int r0 = lo; r0 < hi; r0 += kSortThreads) {
-    const int p = r0 + tid;
-    const int e = p < hi ? idx[p] : -1;
+    for (int w = 0; w < kWaves; ++w)
+      if (tid < E) s_cnt[w][tid] = 0;
+    __syncthreads();  // also: the bases of the last round
+    const int p = r0 + tid, e = mine;
+    mine = p + kSortThreads < hi ? idx[p + kSortThreads] : -1;
     const bool kept = (unsigned)e < (unsigned)E;
     const uint64_t peers = wave_peers(e, kept, bits);
     const int rank = __popcll(peers & ((1ull << lane) - 1));
-    for (int w = 0; w < kSortThreads / 64; ++w) {
-      if (w == wave) {
-        const int pos = kept ? s_base[e] + rank : -1;
-        __builtin_amdgcn_wave_barrier();  // every lane has read the base before its first peer moves it
-        if (kept && rank == 0) s_base[e] = pos + __popcll(peers);
-        if (kept) perm[pos] = p;
-        if (p < hi) inv[p] = pos;
-      }
-      __syncthreads();
+    if (kept && rank == 0) s_cnt[wave][e] = (uint16_t)__popcll(peers);
+    __syncthreads();
+    int pos = -1;
+    if (kept) {
+      pos = s_before[e] + rank;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) pos += w < wave ? s_cnt[w][e] : 0;
+      perm[pos] = p;
+    }
+    if (p < hi) inv[p] = pos;
+    __syncthreads();
+    if (tid < E) {
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) n += s_cnt[w][tid];
+      s_before[tid] += n;
     }
   }
 }
 
-// ---------------------------------------------------------------------------
-// Rows of x to their sorted places: a wavefront takes one token and one segment of its row
-// (4 KB), reads it once and writes it k times.
-constexpr int kSegLoads = 4;  // 16-byte loads per lane and segment
+// Between a wavefront's writes to LDS and its other lanes' reads: LDS serves one wavefront in
+// order, so only the compiler has to keep the order.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
-template <int EB>  // bytes of an element
+// The token of a wavefront, four to a workgroup, as a uniform value: its table entries and row
+// addresses are then scalar, and a pair left out is a uniform branch.
+__device__ __forceinline__ int wave_token() {
+  return blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
+// ---------------------------------------------------------------------------
+// Rows of x to their sorted places: a wavefront takes one token and U * 1 KB of its row,
+// reads it once and writes it k times.
+template <int EB, int U>  // bytes of an element, 16-byte loads per lane
+struct RowPiece {
+  static constexpr int FMT = EB == 2 ? MOE_AFMT_BF16 : MOE_AFMT_F32, N = 16 / EB;
+  Chunk<FMT, N> q[U];
+  __device__ __forceinline__ static Piece<N> at(int u, int H) {
+    return Piece<N>((blockIdx.y * U + u) * 64 + (threadIdx.x & 63), H);
+  }
+  __device__ __forceinline__ void load(const uint8_t* row, int H) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at(u, H).on) q[u].load(row, at(u, H));
+  }
+  __device__ __forceinline__ void store(uint8_t* row, int H) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at(u, H).on) q[u].store(row, at(u, H));
+  }
+};
+constexpr int kMoveLoads = 4;
+
+template <int EB>
 __global__ __launch_bounds__(256) void dispatch_move(const uint8_t* __restrict__ x, int64_t pitch, int T, int k, int H,
                                                      const int32_t* __restrict__ inv, uint8_t* __restrict__ xs) {
-  constexpr int FMT = EB == 2 ? MOE_AFMT_BF16 : MOE_AFMT_F32, N = 16 / EB;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int t = wave_token();
   if (t >= T) return;
-  const int c0 = blockIdx.y * kSegLoads * 64 + lane;  // chunk of the lane's first load
-  const uint8_t* row = x + (int64_t)t * pitch;
-  Chunk<FMT, N> q[kSegLoads];
-#pragma unroll
-  for (int u = 0; u < kSegLoads; ++u) {
-    const int i = (c0 + 64 * u) * N;
-    if (i < H) q[u].load(row + (int64_t)i * EB, H - i);
-  }
+  RowPiece<EB, kMoveLoads> r;
+  r.load(x + (int64_t)t * pitch, H);
   const int64_t P = (int64_t)T * k;
   for (int j = 0; j < k; ++j) {
     const int pos = inv[(int64_t)t * k + j];
-    if ((unsigned)pos >= (uint64_t)P) continue;
-    uint8_t* dst = xs + (int64_t)pos * H * EB;
+    if ((unsigned)pos < (uint64_t)P) r.store(xs + (int64_t)pos * H * EB, H);
+  }
+}
+
+// The sort and the move of at most kTinyPairs pairs in one launch.  A pair's key is
+// (expert, pair) in one word; its place is the number of smaller keys.  The last workgroup
+// (of blockIdx.y = 0) writes the offsets.
+template <int EB, int U>
+__global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__ idx, int T, int k, int E,
+                                                     const uint8_t* __restrict__ x, int64_t pitch, int H,
+                                                     uint8_t* __restrict__ xs, int32_t* __restrict__ perm,
+                                                     int32_t* __restrict__ inv, int32_t* __restrict__ offsets) {
+  const int P = T * k, lane = threadIdx.x & 63;
+  if (blockIdx.x == gridDim.x - 1) {
+    __shared__ int s_n[kMaxExperts], s_wave[4];
+    if (blockIdx.y != 0) return;
+    for (int e = threadIdx.x; e < kMaxExperts; e += 256) s_n[e] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < P; p += 256) {
+      const int e = idx[p];
+      if ((unsigned)e < (unsigned)E) atomicAdd(&s_n[e], 1);
+    }
+    __syncthreads();
+    // four neighbouring experts per thread
+    int n[4], total;
 #pragma unroll
-    for (int u = 0; u < kSegLoads; ++u) {
-      const int i = (c0 + 64 * u) * N;
-      if (i < H) q[u].store(dst + (int64_t)i * EB, H - i);
+    for (int i = 0; i < 4; ++i) n[i] = s_n[4 * threadIdx.x + i];
+    int at = group_prefix(n[0] + n[1] + n[2] + n[3], s_wave, &total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * threadIdx.x + i;
+      if (e < E) offsets[e] = at;
+      at += n[i];
+    }
+    if (threadIdx.x == 0) offsets[E] = total;
+    return;
+  }
+  const int t = wave_token();
+  if (t >= T) return;
+  RowPiece<EB, U> r;
+  if (x) r.load(x + (int64_t)t * pitch, H);
+  constexpr int kRegs = kTinyPairs / 64;
+  uint32_t key[kRegs];
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) {
+    const int p = 64 * i + lane;
+    const int e = p < P ? idx[p] : -1;
+    key[i] = (unsigned)e < (unsigned)E ? (uint32_t)e << 10 | p : 0xffffffffu;
+  }
+  int mine = -1, ids = 0;
+  for (int j = 0; j < k; ++j) {
+    if ((j & 63) == 0) ids = j + lane < k ? idx[t * k + j + lane] : -1;
+    const int p = t * k + j, e = __builtin_amdgcn_readlane(ids, j & 63);
+    int pos = -1;
+    if ((unsigned)e < (unsigned)E) {
+      const uint32_t own = (uint32_t)e << 10 | p;
+      pos = 0;
+#pragma unroll
+      for (int i = 0; i < kRegs; ++i)
+        if (64 * i < P) pos += __popcll(__ballot(key[i] < own));
+      if (x) r.store(xs + (int64_t)pos * H * EB, H);
+    }
+    if (lane == (j & 63)) mine = pos;
+    if (blockIdx.y == 0 && ((j & 63) == 63 || j == k - 1)) {
+      const int q = t * k + (j & ~63) + lane;
+      if ((j & ~63) + lane <= j) {
+        inv[q] = mine;
+        if (mine >= 0) perm[mine] = q;
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
 // y[t] = sum_j w[t,j] rows[inv[t,j]] in rank order (w = nullptr: a plain sum, the gradient
-// of the move).  A wavefront takes one token and 64 chunks of its row; kRanks rows are in
-// flight per lane.
+// of the move).  A workgroup takes one token and 2048 elements of its row, so that the
+// scattered rows are read in pieces of 4 KB and more; kRanks rows are in flight per lane.
 constexpr int kRanks = 8;
 
-template <int RF, int YF, bool WEIGHTED>
+template <int RF, int YF, bool WEIGHTED, bool NT>
 __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ rows, const int32_t* __restrict__ inv,
                                                     const float* __restrict__ w, int T, int k, int H,
                                                     uint8_t* __restrict__ y, int64_t pitch) {
-  constexpr int N = 8, RB = kElemBytes<RF>, YB = kElemBytes<YF>;
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (t >= T) return;
-  const int i = (blockIdx.y * 64 + lane) * N;
-  if (i >= H) return;
+  constexpr int N = 8, RB = kElemBytes<RF>;
+  const int t = blockIdx.x;
+  const Piece<N> at(blockIdx.y * 256 + threadIdx.x, H);
+  if (!at.on) return;
   const int64_t P = (int64_t)T * k, p0 = (int64_t)t * k;
   float acc[N];
 #pragma unroll
@@ -185,7 +330,7 @@ __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ 
       g[j] = 1.f;
       if (kept[j]) {
         if (WEIGHTED) g[j] = w[p0 + j0 + j];
-        q[j].load(rows + ((int64_t)pos * H + i) * RB, H - i);
+        q[j].template load<NT>(rows + (int64_t)pos * H * RB, at);
       }
     }
 #pragma unroll
@@ -197,7 +342,7 @@ __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ 
   }
   Chunk<YF, N> o;
   o.set(acc);
-  o.store(y + (int64_t)t * pitch + (int64_t)i * YB, H - i);
+  o.template store<true>(y + (int64_t)t * pitch, at);
 }
 
 // ---------------------------------------------------------------------------
@@ -206,13 +351,13 @@ __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ 
 // pieces of the row; the dot products meet in LDS in wavefront order.
 constexpr int kCbWaves = 4;
 
-template <int DF, int RF>
+template <int DF, int RF, bool NT>
 __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uint8_t* __restrict__ dy, int64_t pitch,
                                                                        const uint8_t* ys,
                                                                        const int32_t* __restrict__ inv,
                                                                        const float* __restrict__ w, int T, int k, int H,
                                                                        uint8_t* dys, float* __restrict__ dw) {
-  constexpr int N = 8, DB = kElemBytes<DF>, RB = kElemBytes<RF>;
+  constexpr int N = 8, RB = kElemBytes<RF>;
   __shared__ float s_dot[kCbWaves][kRanks];
   const int t = blockIdx.x, j0 = blockIdx.y * kRanks, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t P = (int64_t)T * k, p0 = (int64_t)t * k + j0;
@@ -225,14 +370,20 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
     g[j] = pos[j] >= 0 && dys ? w[p0 + j] : 0.f;
     dot[j] = 0.f;
   }
-  for (int i = threadIdx.x * N; i < H; i += 64 * kCbWaves * N) {
+  for (int c = threadIdx.x; c * N < H; c += 64 * kCbWaves) {
+    const Piece<N> at(c, H);
     Chunk<DF, N> d;
     Chunk<RF, N> q[kRanks];
-    d.load(dy + (int64_t)t * pitch + (int64_t)i * DB, H - i);
+    d.load(dy + (int64_t)t * pitch, at);
     if (dw) {
 #pragma unroll
       for (int j = 0; j < kRanks; ++j)
-        if (pos[j] >= 0) q[j].load(ys + ((int64_t)pos[j] * H + i) * RB, H - i);
+        if (pos[j] >= 0) q[j].template load<NT>(ys + (int64_t)pos[j] * H * RB, at);
+      if (at.skip) {
+        d.drop(at.skip);
+#pragma unroll
+        for (int j = 0; j < kRanks; ++j) q[j].drop(at.skip);
+      }
 #pragma unroll
       for (int j = 0; j < kRanks; ++j)
         if (pos[j] >= 0) {
@@ -248,7 +399,7 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
 #pragma unroll
           for (int n = 0; n < N; ++n) v[n] = g[j] * d.get(n);
           q[j].set(v);
-          q[j].store(dys + ((int64_t)pos[j] * H + i) * RB, H - i);
+          q[j].template store_own<true>(dys + (int64_t)pos[j] * H * RB, at);
         }
     }
   }
@@ -268,60 +419,90 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
 }
 
 // ---------------------------------------------------------------------------
-// The gradient of the gates: one wavefront per token, E / 64 logits per lane.  A token's
-// logits are all read before any of its gradients is written (dlogits may be logits).
-template <int PL>
+// The gradient of the gates: one wavefront per token, four neighbouring logits per lane and
+// load.  The gates' gradients are first gathered by expert: lane j adds up, in rank order,
+// every rank that chose its expert, and the first of them puts the sum and the number of
+// ranks into the wavefront's table in LDS.  A token's logits are all read before any of its
+// gradients is written (dlogits may be logits).
+template <int C>  // loads of 256 logits
 __global__ __launch_bounds__(256) void topk_backward_kernel(const float* logits, int T, int E, int k,
                                                             const int32_t* __restrict__ idx,
                                                             const float* __restrict__ dw, int renorm,
                                                             float* dlogits) {
-  const int t = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  __shared__ __attribute__((aligned(16))) float2 s_tab[4][256 * C];
+  const int t = wave_token(), lane = threadIdx.x & 63;
   if (t >= T) return;
-  const float* z = logits + (int64_t)t * E;
-  const int32_t* id = idx + (int64_t)t * k;
-  const float* dg = dw + (int64_t)t * k;
-  // per logit: how often it was chosen and the gates' gradients that fell on it
-  float v[PL], n[PL], d[PL];
+  float2* tab = s_tab[threadIdx.x >> 6];
+  const uint8_t* z = reinterpret_cast<const uint8_t*>(logits + (int64_t)t * E);
+  Chunk<MOE_AFMT_F32, 4> q[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const Piece<4> at(64 * c + lane, E);
+    if (at.on) q[c].load(z, at);
+    // by lane, a stride of 64 entries: neighbours in neighbouring banks
+#pragma unroll
+    for (int n = 0; n < 4; ++n) tab[256 * c + 64 * n + lane] = make_float2(0.f, 0.f);
+  }
+  wave_lds_order();
+  for (int j0 = 0; j0 < k; j0 += 64) {
+    const int j = j0 + lane, nj = min(64, k - j0);
+    const int e = j < k ? idx[(int64_t)t * k + j] : -1;
+    const float g = j < k ? dw[(int64_t)t * k + j] : 0.f;
+    float sum = 0.f, cnt = 0.f;
+    bool first = (unsigned)e < (unsigned)E;
+    for (int i = 0; i < nj; ++i) {
+      const int ei = __builtin_amdgcn_readlane(e, i);
+      const float gi = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), i));
+      const bool same = ei == e;
+      sum += same ? gi : 0.f;
+      cnt += same ? 1.f : 0.f;
+      first = first && !(same && i < lane);
+    }
+    if (first) {
+      const float2 was = tab[e];
+      tab[e] = make_float2(was.x + sum, was.y + cnt);
+    }
+    wave_lds_order();
+  }
+  float v[C][4], n[C][4], d[C][4];
   float mx = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + 64 * i;
-    v[i] = e < E ? z[e] : -INFINITY;
-    n[i] = 0.f;
-    d[i] = 0.f;
-  }
-  for (int j = 0; j < k; ++j) {
-    const int e = id[j];
-    if ((unsigned)e >= (unsigned)E) continue;
-    const float g = dg[j];
+  for (int c = 0; c < C; ++c) {
+    const Piece<4> at(64 * c + lane, E);
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
-      if (e == lane + 64 * i) {
-        n[i] += 1.f;
-        d[i] += g;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const bool own = at.on && i >= at.skip && i < at.n;
+      const float2 a = tab[own ? at.i + i : 0];
+      d[c][i] = own ? a.x : 0.f;
+      n[c][i] = own ? a.y : 0.f;
+      // the softmax runs over all experts, or over the chosen ones (each as often as it was)
+      v[c][i] = own && (!renorm || a.y > 0.f) ? q[c].get(i) : -INFINITY;
+      mx = fmaxf(mx, v[c][i]);
+    }
   }
-  // the softmax runs over all experts, or over the chosen ones (each as often as it was)
-#pragma unroll
-  for (int i = 0; i < PL; ++i) mx = fmaxf(mx, !renorm || n[i] > 0.f ? v[i] : -INFINITY);
   mx = wave_max(mx);
   float sum = 0.f, mean = 0.f;
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const bool in = lane + 64 * i < E && (!renorm || n[i] > 0.f);
-    // a masked logit (-inf) has no share, also where every logit is masked
-    v[i] = in && v[i] != -INFINITY ? __expf(v[i] - mx) : 0.f;
-    sum += renorm ? n[i] * v[i] : v[i];
-    mean += d[i] * v[i];
-  }
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // a masked logit (-inf) has no share, also where every logit is masked
+      v[c][i] = v[c][i] != -INFINITY ? __expf(v[c][i] - mx) : 0.f;
+      sum += renorm ? n[c][i] * v[c][i] : v[c][i];
+      mean += d[c][i] * v[c][i];
+    }
   sum = wave_sum(sum);
   mean = wave_sum(mean);
   const float r = sum == 0.f ? 0.f : 1.f / sum;
   mean *= r;
 #pragma unroll
-  for (int i = 0; i < PL; ++i) {
-    const int e = lane + 64 * i;
-    if (e < E) dlogits[(int64_t)t * E + e] = v[i] * r * (d[i] - (renorm ? n[i] * mean : mean));
+  for (int c = 0; c < C; ++c) {
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = v[c][i] * r * (d[c][i] - (renorm ? n[c][i] * mean : mean));
+    Chunk<MOE_AFMT_F32, 4> out;
+    out.set(o);
+    out.store_own(reinterpret_cast<uint8_t*>(dlogits + (int64_t)t * E), Piece<4>(64 * c + lane, E));
   }
 }
 
@@ -339,18 +520,24 @@ Span rows_of(const void* p, int64_t rows, int32_t H, int fmt, int64_t ld) {
   return {p, rows, H * fmt_bytes(fmt), ld * fmt_bytes(fmt)};
 }
 
+// One instantiation of `f` by two formats and a truth value.
+template <typename F>
+moe_status by_formats(int a, int b, bool nt, F f) {
+  constexpr auto B = std::integral_constant<int, MOE_AFMT_BF16>{};
+  constexpr auto S = std::integral_constant<int, MOE_AFMT_F32>{};
+  const auto with = [&](auto x, auto y) { return nt ? f(x, y, std::true_type{}) : f(x, y, std::false_type{}); };
+  if (a == MOE_AFMT_BF16) return b == MOE_AFMT_BF16 ? with(B, B) : with(B, S);
+  return b == MOE_AFMT_BF16 ? with(S, B) : with(S, S);
+}
+
 template <bool WEIGHTED>
 moe_status run_combine(const void* rows, int fmt, const int32_t* inv, const float* w, int T, int k, int H, void* y,
                        int y_fmt, int64_t ld, hipStream_t s) {
-  const dim3 grid((T + 3) / 4, (H + 64 * 8 - 1) / (64 * 8)), block(256);
-  const uint8_t* r = static_cast<const uint8_t*>(rows);
-  uint8_t* o = static_cast<uint8_t*>(y);
-  const int64_t pitch = ld * fmt_bytes(y_fmt);
-  constexpr int B = MOE_AFMT_BF16, F = MOE_AFMT_F32;
-  if (fmt == B && y_fmt == B) return launch(combine_rows<B, B, WEIGHTED>, grid, block, s, r, inv, w, T, k, H, o, pitch);
-  if (fmt == B) return launch(combine_rows<B, F, WEIGHTED>, grid, block, s, r, inv, w, T, k, H, o, pitch);
-  if (y_fmt == B) return launch(combine_rows<F, B, WEIGHTED>, grid, block, s, r, inv, w, T, k, H, o, pitch);
-  return launch(combine_rows<F, F, WEIGHTED>, grid, block, s, r, inv, w, T, k, H, o, pitch);
+  const bool nt = stream_rows((int64_t)T * k * H * fmt_bytes(fmt));
+  return by_formats(fmt, y_fmt, nt, [&](auto rf, auto yf, auto n) {
+    return launch(combine_rows<rf(), yf(), WEIGHTED, n()>, dim3(T, (H + 256 * 8 - 1) / (256 * 8)), dim3(256), s,
+                  static_cast<const uint8_t*>(rows), inv, w, T, k, H, static_cast<uint8_t*>(y), ld * fmt_bytes(y_fmt));
+  });
 }
 
 }  // namespace
@@ -360,7 +547,8 @@ using namespace rmoe;
 
 extern "C" MOE_API int64_t moe_dispatch_workspace(int32_t T, int32_t k, int32_t n_experts) {
   if (!move_shape_ok(T, k, 1) || n_experts < 1 || n_experts > kMaxExperts) return -1;
-  return (int64_t)sort_plan((int64_t)T * k).blocks * n_experts * 4;
+  const int64_t P = (int64_t)T * k;
+  return P <= kSolePairs ? 0 : (int64_t)sort_plan(P).blocks * n_experts * 4;
 }
 
 extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, int32_t k, int32_t n_experts,
@@ -388,22 +576,40 @@ extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, i
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   const StreamDevice on(s);
+  const uint8_t* src = static_cast<const uint8_t*>(x);
+  uint8_t* dst = static_cast<uint8_t*>(xs);
+  const int64_t eb = x ? fmt_bytes(fmt) : 4, pitch = ld * eb, row_bytes = x ? H * eb : 1;
+  if (P <= kTinyPairs) {
+    // few tokens: 1 KB per wavefront, so that one row is spread over more of them
+    const bool thin = (int64_t)T * ((row_bytes + 4095) / 4096) < 1024;
+    const int piece = thin ? 1024 : 1024 * kMoveLoads;
+    const dim3 grid((T + 3) / 4 + 1, (unsigned)((row_bytes + piece - 1) / piece)), block(256);
+    if (eb == 2)
+      return launch(thin ? dispatch_tiny<2, 1> : dispatch_tiny<2, kMoveLoads>, grid, block, s, topk_idx, T, k, n_experts,
+                    src, pitch, H, dst, perm, inv, offsets);
+    return launch(thin ? dispatch_tiny<4, 1> : dispatch_tiny<4, kMoveLoads>, grid, block, s, topk_idx, T, k, n_experts, src,
+                  pitch, H, dst, perm, inv, offsets);
+  }
   const SortPlan sp = sort_plan(P);
   int bits = 0;
   while ((1 << bits) < n_experts) ++bits;
   int32_t* hist = static_cast<int32_t*>(ws);
-  moe_status st = launch(dispatch_count, dim3(sp.blocks), dim3(kSortThreads), s, topk_idx, (int)P, n_experts, sp.chunk, hist);
-  if (st == MOE_OK)
-    st = launch(dispatch_place, dim3(sp.blocks), dim3(kSortThreads), s, topk_idx, (int)P, n_experts, bits, sp.chunk,
-                hist, perm, inv, offsets);
+  const dim3 chunks(sp.blocks), threads(kSortThreads);
+  moe_status st;
+  if (P <= kSolePairs) {
+    st = launch(dispatch_place<true>, chunks, threads, s, topk_idx, (int)P, n_experts, bits, sp.chunk,
+                static_cast<const int32_t*>(nullptr), perm, inv, offsets);
+  } else {
+    st = launch(dispatch_count, chunks, threads, s, topk_idx, (int)P, n_experts, sp.chunk, hist);
+    if (st == MOE_OK)
+      st = launch(dispatch_place<false>, chunks, threads, s, topk_idx, (int)P, n_experts, bits, sp.chunk,
+                  static_cast<const int32_t*>(hist), perm, inv, offsets);
+  }
   if (st != MOE_OK || !x) return st;
-  const int64_t eb = fmt_bytes(fmt);
-  const int seg = kSegLoads * 64 * (int)(16 / eb);
-  const dim3 grid((T + 3) / 4, (H + seg - 1) / seg);
-  const uint8_t* src = static_cast<const uint8_t*>(x);
-  uint8_t* dst = static_cast<uint8_t*>(xs);
-  if (eb == 2) return launch(dispatch_move<2>, grid, dim3(256), s, src, ld * eb, T, k, H, inv, dst);
-  return launch(dispatch_move<4>, grid, dim3(256), s, src, ld * eb, T, k, H, inv, dst);
+  const int piece = 1024 * kMoveLoads;
+  const dim3 grid((T + 3) / 4, (unsigned)((row_bytes + piece - 1) / piece)), block(256);
+  return launch(eb == 2 ? dispatch_move<2> : dispatch_move<4>, grid, block, s, src, pitch, T, k, H,
+                static_cast<const int32_t*>(inv), dst);
 }
 
 extern "C" MOE_API moe_status moe_dispatch_backward(const void* dxs, int32_t dxs_fmt, const int32_t* inv, int32_t T,
@@ -451,17 +657,12 @@ extern "C" MOE_API moe_status moe_combine_backward(const void* dy, int32_t dy_fm
   if (overlap(out[0], out[1])) return MOE_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const StreamDevice on(s);
-  const dim3 grid(T, (k + kRanks - 1) / kRanks), block(64 * kCbWaves);
-  const uint8_t* d = static_cast<const uint8_t*>(dy);
-  const uint8_t* r = static_cast<const uint8_t*>(ys);
-  uint8_t* o = static_cast<uint8_t*>(dys);
-  const int64_t pitch = ld * fmt_bytes(dy_fmt);
-  constexpr int B = MOE_AFMT_BF16, F = MOE_AFMT_F32;
-  if (dy_fmt == B && ys_fmt == B)
-    return launch(combine_rows_backward<B, B>, grid, block, s, d, pitch, r, inv, w, T, k, H, o, dw);
-  if (dy_fmt == B) return launch(combine_rows_backward<B, F>, grid, block, s, d, pitch, r, inv, w, T, k, H, o, dw);
-  if (ys_fmt == B) return launch(combine_rows_backward<F, B>, grid, block, s, d, pitch, r, inv, w, T, k, H, o, dw);
-  return launch(combine_rows_backward<F, F>, grid, block, s, d, pitch, r, inv, w, T, k, H, o, dw);
+  const bool nt = stream_rows(P * H * fmt_bytes(ys_fmt));
+  return by_formats(dy_fmt, ys_fmt, nt, [&](auto df, auto rf, auto n) {
+    return launch(combine_rows_backward<df(), rf(), n()>, dim3(T, (k + kRanks - 1) / kRanks), dim3(64 * kCbWaves), s,
+                  static_cast<const uint8_t*>(dy), ld * fmt_bytes(dy_fmt), static_cast<const uint8_t*>(ys), inv, w, T, k, H,
+                  static_cast<uint8_t*>(dys), dw);
+  });
 }
 
 extern "C" MOE_API moe_status moe_topk_backward(const float* logits, int32_t T, int32_t n_experts,
@@ -478,6 +679,7 @@ extern "C" MOE_API moe_status moe_topk_backward(const float* logits, int32_t T, 
   const StreamDevice on(s);
   const dim3 grid((T + 3) / 4), block(256);
   const int E = n_experts;
-  if (E <= 256) return launch(topk_backward_kernel<4>, grid, block, s, logits, T, E, k, topk_idx, dw, renorm, dlogits);
-  return launch(topk_backward_kernel<16>, grid, block, s, logits, T, E, k, topk_idx, dw, renorm, dlogits);
+  const auto kernel = E <= 256 ? topk_backward_kernel<1> : E <= 512 ? topk_backward_kernel<2>
+                      : E <= 768 ? topk_backward_kernel<3> : topk_backward_kernel<4>;
+  return launch(kernel, grid, block, s, logits, T, E, k, topk_idx, dw, renorm, dlogits);
 }

@@ -20,13 +20,16 @@ def dispatch(**kw):
     return L.moe_dispatch(*a.values(), None)
 
 
+LONG = dict(T=1 << 15, k=4)   # a sort that needs a workspace
+
+
 @pytest.mark.parametrize("bad", [
-    dict(idx=None), dict(perm=None), dict(inv=None), dict(off=None), dict(ws=None), dict(x=None), dict(xs=None),
+    dict(idx=None), dict(perm=None), dict(inv=None), dict(off=None), dict(LONG, ws=None), dict(x=None), dict(xs=None),
     dict(T=0), dict(T=-1), dict(T=(1 << 22) + 1), dict(k=0), dict(k=1025), dict(T=1 << 20, k=128), dict(E=0), dict(E=1025),
-    dict(fmt=2), dict(fmt=-1), dict(H=0), dict(H=65537), dict(ld=63), dict(ld=-64), dict(n=3), dict(x=A[1] + 1),
-    dict(xs=A[2] + 1), dict(ws=A[6] + 2),
+    dict(fmt=2), dict(fmt=-1), dict(H=0), dict(H=65537), dict(ld=63), dict(ld=-64), dict(LONG, n=3), dict(x=A[1] + 1),
+    dict(xs=A[2] + 1), dict(LONG, ws=A[6] + 2),
     dict(xs=A[1]), dict(xs=A[1] + 8 * 128 - 2), dict(perm=A[4]), dict(inv=A[5]), dict(inv=A[0]), dict(off=A[2]),
-    dict(ws=A[3]), dict(perm=A[2] + 16 * 128 - 4)])
+    dict(LONG, ws=A[3]), dict(perm=A[2] + 16 * 128 - 4)])
 def test_dispatch_refuses(bad):
     assert dispatch(**bad) == R.MOE_EINVAL
 
@@ -140,7 +143,8 @@ def test_workspace_sizes():
         assert L.moe_dispatch_workspace(*bad) == -1
         with pytest.raises(R.MoeError):
             R.moe_dispatch_workspace(*bad)
-    assert 0 <= R.moe_dispatch_workspace(1 << 20, 64, 1024) <= 1 << 21     # bounded however long the prompt
+    assert 0 < R.moe_dispatch_workspace(1 << 20, 64, 1024) <= 1 << 21      # bounded however long the prompt
+    assert R.moe_dispatch_workspace(LONG["T"], LONG["k"], 4) > 3
     for bad in ((0, 1), (1, 0), (1, 16385)):
         with pytest.raises(R.MoeError):
             R.moe_block_norm_workspace(*bad)
@@ -172,27 +176,29 @@ def test_binding_refuses_what_the_library_would_misread():
             ("x", torch.zeros(H, T).t(), {}, "contiguous rows"), ("x", torch.zeros(T, 2 * H)[:, ::2], {}, "contiguous rows"),
             ("x", torch.zeros(1, H).expand(T, H), {}, "contiguous rows"), ("x", x, dict(n_rows=5), "shape"),
             ("xs", torch.zeros(T, 2 * H)[:, :H], dict(dense=True), "without gaps"), ("x", x, dict(width=9), "shape"),
-            ("x", torch.zeros(0, H), {}, "shape"), ("h_out", x, dict(like=x.bfloat16()), "belongs to"),
-            ("h_out", torch.zeros(T, 2 * H)[:, :H], dict(like=x), "belongs to"), ("x", None, {}, "two-dimensional")]:
+            ("x", torch.zeros(0, H), {}, "shape"), ("h_out", x, dict(like=(BF16, H)), "belongs to"),
+            ("h_out", torch.zeros(T, 2 * H)[:, :H], dict(like=(F32, H)), "belongs to"), ("x", None, {}, "two-dimensional")]:
         assert msg in refused(a.rows, name, t, **kw), (name, msg)
     for t, msg in [(torch.zeros(T, k, dtype=torch.float64), "float32"), (torch.zeros(k, T).t(), "contiguous"),
                    (torch.zeros(T, k + 1), "shape"), (None, "contiguous")]:
         assert msg in refused(a.flat, "w", t, torch.float32, T, k)
     assert "go together" in refused(R._norm_inputs, a, T, H, None, None, None, R.MOE_GATE_TOKEN)
-    assert "out of range" in refused(a.workspace, None, -1)
+    assert "contiguous" in refused(a.workspace, x.t())
+    assert a.workspace(None) == a.workspace(x[:0]) == (None, 0)
 
 
 class _On:
     """A stand-in for a tensor on a GPU."""
 
-    def __init__(self, device):
-        self.is_cuda, self.device = True, torch.device(device)
+    def __init__(self, dev):
+        self.get_device = lambda: dev
 
 
 def test_binding_refuses_mixed_devices():
     a = R._Args("moe_combine")
-    a._place("ys", _On("cuda:1"))
-    assert "cuda:0" in refused(a._place, "inv", _On("cuda:0"))
+    a.place("ys", _On(1))
+    assert "cuda:0" in refused(a.place, "inv", _On(0))
+    assert "on the GPU" in refused(a.place, "inv", _On(-1))
 
 
 def test_side_by_side_blocks_of_one_buffer_are_told_apart():
