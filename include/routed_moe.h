@@ -608,7 +608,7 @@ MOE_API moe_status moe_pool_load(moe_ctx* ctx, const char* path, int32_t threads
  *  - An output shares no byte with an input or another output unless the call says so (blocks side
  *    by side in the rows of one buffer are told apart when their strides in bytes are equal).
  *  - Limits: 1 <= T <= 2^22, 1 <= k <= 1024, T*k <= 2^26, n_experts <= 1024, H <= 65536 (moves) or
- *    16384 (norms).
+ *    8192 (norms).
  *  - MOE_EINVAL for a null pointer, shape, format, stride, alignment, overlap or short workspace
  *    (nothing is enqueued); MOE_EHIP if a launch fails.
  */
@@ -679,7 +679,7 @@ typedef struct {
   int32_t h_fmt, y_fmt, x_fmt; /* moe_afmt of the residual stream, the block's output, the norm's output */
   int32_t gate_kind;           /* moe_gate_kind */
   float alpha;                 /* residual scale, finite */
-  float eps;                   /* added to the mean square, in (0, 1] */
+  float eps;                   /* added to the mean square, in [2^-126, 1] */
   int64_t ld_h, ld_y, ld_x;    /* row strides (0 = H) of h, h_out and their gradients; y and dy; x_out and dx */
 } moe_norm_config;
 

@@ -519,23 +519,32 @@ class _Args:
             self.refuse(f"{name} needs contiguous rows" + (" without gaps" if dense else ""))
         if like is not None and (fmt, ld) != like:
             self.refuse(f"{name} must have the type and row stride of the tensor it belongs to")
-        self.place(name, t)
+        if t.get_device() != self.dev:
+            self.place(name, t)
         return t.data_ptr(), fmt, ld, n, h
 
     def flat(self, name, t, dtype, *shape):
         """Pointer of a dense tensor of this type and shape (one number: that many elements)."""
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous():
+        try:
+            ok = t.dtype is dtype and t.is_contiguous()
+        except AttributeError:
+            ok = False
+        if not ok:
             self.refuse(f"{name} must be a contiguous {dtype} tensor")
         if t.shape != shape and not (len(shape) == 1 and t.numel() == shape[0]):
             self.refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
-        self.place(name, t)
+        if t.get_device() != self.dev:
+            self.place(name, t)
         return t.data_ptr()
 
     def pairs(self, name, t):
         """(T, k, pointer) of an int32 [T, k] table."""
-        if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.numel() < 1:
+        try:
+            T, k = t.shape
+        except (AttributeError, ValueError):
+            T = k = 0
+        if not T or not k:
             self.refuse(f"{name} must be an int32 tensor [T, k]")
-        T, k = t.shape
         return T, k, self.flat(name, t, torch.int32, T, k)
 
     def workspace(self, t):

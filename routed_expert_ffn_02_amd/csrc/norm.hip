@@ -11,15 +11,18 @@
 
 namespace rmoe {
 
-constexpr int kNormMaxH = kDecodeMaxTH;  // a row fits one workgroup's registers
+constexpr int kNormN = 8;          // elements of a lane's chunk
+constexpr int kNormMaxWaves = 16;  // of a workgroup
+// A row is one chunk per thread of one workgroup.  (With two, the gradient's rows and sums did
+// not fit the 128 registers of a 1024-thread workgroup: 165 us at 1000 rows of 16384, bf16,
+// against 28 at 8192.)
+constexpr int kNormMaxH = 64 * kNormMaxWaves * kNormN;
 constexpr int kNormMaxT = 1 << 22;
-constexpr int kNormN = 8;                // elements of a lane's chunk
-constexpr int kNormMaxWaves = 16;
 
 struct NormArgs {
   int T, H, gate_kind;
   int64_t h_pitch, y_pitch, x_pitch;  // bytes between rows
-  float alpha, eps;
+  float alpha, eps, per_h;            // per_h = 1 / H
   const uint8_t *h, *y;
   const float *w_post, *gate, *w_pre;
   uint8_t *h_out, *x_out;             // forward
@@ -27,27 +30,43 @@ struct NormArgs {
   uint8_t *dh, *dy;
   float* dgate_token;                 // [T]
   float* part;                        // partial sums of the weights' gradients [kinds][G][H]
-  int part_pre, part_post, part_gate; // index of each kind in part, or -1
+  int part_pre, part_post;            // index of each kind in part, or -1
 };
 
-// The sum over the workgroup's wavefronts of NV values per thread, in wavefront order.
-template <int NV>
-__device__ __forceinline__ void block_sum(float (&v)[NV], float (*s_red)[NV]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
-  if (nw == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) s_red[wave][i] = v[i];
+// The sum over the workgroup's wavefronts (at most W) of NV values per thread, in wavefront
+// order.
+template <int NV, int W>
+struct BlockSum {
+  float v[NV][W];
+  __device__ __forceinline__ void init() {
+    for (int i = threadIdx.x; i < NV * W; i += blockDim.x) (&v[0][0])[i] = 0.f;
+    __syncthreads();
   }
-  __syncthreads();
+  __device__ __forceinline__ void sum(float (&s)[NV]) {
+    const int wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    v[i] = 0.f;
-    for (int w = 0; w < nw; ++w) v[i] += s_red[w][i];
+    for (int i = 0; i < NV; ++i) s[i] = wave_sum(s[i]);
+    if (blockDim.x == 64) return;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i][wave] = s[i];
+    }
+    __syncthreads();
+    // all entries are read at once; those without a wavefront add nothing
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float all[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) all[w] = v[i][w];
+      s[i] = all[0];
+#pragma unroll
+      for (int w = 1; w < W; ++w) s[i] += all[w];
+    }
   }
-}
+};
+
+// 1 / sqrt of a normal number (v_rsq_f32: within one unit in the last place).
+__device__ __forceinline__ float inv_sqrt(float v) { return __builtin_amdgcn_rsqf(v); }
 
 // fp32 weights of a chunk, 1 where there are none.
 __device__ __forceinline__ void load_w(const float* w, const Piece<kNormN>& at, float (&v)[kNormN]) {
@@ -57,94 +76,92 @@ __device__ __forceinline__ void load_w(const float* w, const Piece<kNormN>& at, 
   for (int n = 0; n < kNormN; ++n) v[n] = w && at.on ? q.get(n) : 1.f;
 }
 
-// One workgroup per row, C chunks of 8 elements per thread.  h_out may be h: a thread writes
-// only elements that it alone has read for sums and sums, and no other thread's reads of
-// them count.
-template <int HF, int YF, int XF, int C>
-__global__ __launch_bounds__(64 * kNormMaxWaves) void block_norm_kernel(NormArgs a) {
+// One workgroup per row.  Stores are non-temporal: at 4096 rows of 2048 (h, y fp32, x bf16) 20.4
+// us against 25.9, and a kernel that reads x next takes as long as after ordinary stores, at 1 row
+// and at 4096.  h_out may be h: a thread writes the elements that it alone sums, and what
+// other threads read of them is dropped.
+template <int HF, int YF, int XF, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void block_norm_kernel(NormArgs a) {
   constexpr int N = kNormN;
-  __shared__ float s_y[kNormMaxWaves][1], s_h[kNormMaxWaves][1];
+  __shared__ __attribute__((aligned(16))) BlockSum<1, WAVES> s_y, s_h;
   const int64_t t = blockIdx.x;
-  const int H = a.H;
-  Chunk<HF, N> qh[C];
-  Chunk<YF, N> qy[C];
-  float wq[C][N], g[C][N], wp[C][N];
+  const Piece<N> at(threadIdx.x, a.H);
+  Chunk<HF, N> qh;
+  Chunk<YF, N> qy;
+  float wq[N], g[N], wp[N];
+  if (a.y) qy.load_own(a.y + t * a.y_pitch, at);
+  qh.load_own(a.h + t * a.h_pitch, at);
+  load_w(a.w_post, at, wq);
+  load_w(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, at, g);
+  load_w(a.w_pre, at, wp);
+  s_y.init();  // the loads are on their way
+  s_h.init();
+  float h[N];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const Piece<N> at(threadIdx.x + c * blockDim.x, H);
-    if (a.y) qy[c].load_own(a.y + t * a.y_pitch, at);
-    qh[c].load_own(a.h + t * a.h_pitch, at);
-    load_w(a.w_post, at, wq[c]);
-    load_w(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, at, g[c]);
-    load_w(a.w_pre, at, wp[c]);
-  }
-  float h[C][N];
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int n = 0; n < N; ++n) h[c][n] = qh[c].get(n);
+  for (int n = 0; n < N; ++n) h[n] = qh.get(n);
   if (a.y) {
     float scale = a.alpha;
     if (a.gate_kind == MOE_GATE_TOKEN) scale *= a.gate[t];
     if (a.w_post) {
       float s[1] = {0.f};
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int n = 0; n < N; ++n) s[0] = fmaf(qy[c].get(n), qy[c].get(n), s[0]);
-      block_sum(s, s_y);
-      scale *= 1.f / sqrtf(s[0] / H + a.eps);
+      for (int n = 0; n < N; ++n) s[0] = fmaf(qy.get(n), qy.get(n), s[0]);
+      s_y.sum(s);
+      scale *= inv_sqrt(s[0] * a.per_h + a.eps);
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const Piece<N> at(threadIdx.x + c * blockDim.x, H);
-#pragma unroll
-      for (int n = 0; n < N; ++n) h[c][n] = fmaf(scale * qy[c].get(n), wq[c][n] * g[c][n], h[c][n]);
-      Chunk<HF, N> o;
-      o.set(h[c]);
-      o.template store_own<true>(a.h_out + t * a.h_pitch, at);
-    }
+    for (int n = 0; n < N; ++n) h[n] = fmaf(scale * qy.get(n), wq[n] * g[n], h[n]);
+    Chunk<HF, N> o;
+    o.set(h);
+    o.template store_own<true>(a.h_out + t * a.h_pitch, at);
   }
   if (!a.x_out) return;
   float s[1] = {0.f};
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int n = 0; n < N; ++n) s[0] = fmaf(h[n], h[n], s[0]);
+  s_h.sum(s);
+  const float r = inv_sqrt(s[0] * a.per_h + a.eps);
 #pragma unroll
-    for (int n = 0; n < N; ++n) s[0] = fmaf(h[c][n], h[c][n], s[0]);
-  block_sum(s, s_h);
-  const float r = 1.f / sqrtf(s[0] / H + a.eps);
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const Piece<N> at(threadIdx.x + c * blockDim.x, H);
-#pragma unroll
-    for (int n = 0; n < N; ++n) wp[c][n] = h[c][n] * r * wp[c][n];
-    Chunk<XF, N> o;
-    o.set(wp[c]);
-    o.template store_own<true>(a.x_out + t * a.x_pitch, at);
-  }
+  for (int n = 0; n < N; ++n) wp[n] = h[n] * r * wp[n];
+  Chunk<XF, N> o;
+  o.set(wp);
+  o.template store_own<true>(a.x_out + t * a.x_pitch, at);
 }
 
-// The rows of one token in the gradient, as stored; zeros for a gradient that does not come in.
-template <int HF, int YF, int XF, int C>
+// A chunk of one token's rows in the gradient, as stored.
+template <int HF, int YF, int XF>
 struct NormRows {
-  Chunk<HF, kNormN> h[C], d[C];
-  Chunk<YF, kNormN> y[C];
-  Chunk<XF, kNormN> x[C];
-  __device__ __forceinline__ void load(const NormArgs& a, int64_t t) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const Piece<kNormN> at(threadIdx.x + c * blockDim.x, a.H);
-      h[c].zero();
-      x[c].zero();
-      d[c].zero();
-      y[c].zero();
-      if (a.dx) {
-        h[c].load_own(a.h + t * a.h_pitch, at);
-        x[c].load_own(a.dx + t * a.x_pitch, at);
-      }
-      if (a.dh_in) d[c].load_own(a.dh_in + t * a.h_pitch, at);
-      if (a.y) y[c].load_own(a.y + t * a.y_pitch, at);
+  Chunk<HF, kNormN> h, d;
+  Chunk<YF, kNormN> y;
+  Chunk<XF, kNormN> x;
+  // Zeros for a gradient that does not come in.
+  __device__ __forceinline__ void load(const NormArgs& a, int64_t t, const Piece<kNormN>& at) {
+    h.zero();
+    x.zero();
+    d.zero();
+    y.zero();
+    if (a.dx) {
+      h.load_own(a.h + t * a.h_pitch, at);
+      x.load_own(a.dx + t * a.x_pitch, at);
     }
+    if (a.dh_in) d.load_own(a.dh_in + t * a.h_pitch, at);
+    if (a.y) y.load_own(a.y + t * a.y_pitch, at);
+  }
+  // All four come in and a row has 8 elements or more: loads without a branch, so that the
+  // wait for one row does not become a wait for all that is under way.  keep_own follows.
+  __device__ __forceinline__ void load_all(const NormArgs& a, int64_t t, const Piece<kNormN>& at) {
+    const int64_t i = at.i;  // 0 in a lane behind the row
+    h.load_at(a.h + t * a.h_pitch + i * kElemBytes<HF>);
+    x.load_at(a.dx + t * a.x_pitch + i * kElemBytes<XF>);
+    d.load_at(a.dh_in + t * a.h_pitch + i * kElemBytes<HF>);
+    y.load_at(a.y + t * a.y_pitch + i * kElemBytes<YF>);
+  }
+  __device__ __forceinline__ void keep_own(const Piece<kNormN>& at) {
+    const int skip = at.on ? at.skip : kNormN;
+    h.keep_from(skip);
+    x.keep_from(skip);
+    d.keep_from(skip);
+    y.keep_from(skip);
   }
 };
 
@@ -154,142 +171,146 @@ struct NormRows {
 //   dw_pre = sum_t dx h' r,  dw_post = sum_t du y ry,  dgate = alpha sum dh u
 // A workgroup walks rows b, b + G, ...; its threads keep the weights' gradients of their
 // own channels in registers over those rows and write one partial row at the end, which
-// norm_reduce adds in workgroup order: no atomics, the same bits every time.  AHEAD: the
-// next row is loaded before the current one's sums.
-template <int HF, int YF, int XF, int C, int WAVES, bool AHEAD>
+// norm_reduce adds in workgroup order: no atomics, the same bits every time.  A channel gate g_c
+// and w_post share one sum, S = sum_t alpha dh y ry: dw_post = g_c S, dgate = w_post S.
+// REGULAR: every row comes in (load_all).  With up to eight wavefronts, whose threads have 256
+// registers, the next row is then loaded before the current one's sums (AHEAD): 19.9 us
+// against 27.2 at 2048 rows of 4096 in bf16.
+template <int HF, int YF, int XF, int WAVES, bool REGULAR>
 __global__ __launch_bounds__(64 * WAVES) void block_norm_backward_kernel(NormArgs a) {
   constexpr int N = kNormN;
-  __shared__ float s_a[WAVES][3], s_b[WAVES][1];
-  const int H = a.H;
-  float wp[C][N], wq[C][N], gc[C][N], acc_pre[C][N], acc_post[C][N], acc_gate[C][N];
-  NormRows<HF, YF, XF, C> next;
-  if (AHEAD) next.load(a, blockIdx.x);
+  constexpr bool AHEAD = REGULAR && WAVES <= 8;
+  __shared__ __attribute__((aligned(16))) BlockSum<3, WAVES> s_a;
+  __shared__ __attribute__((aligned(16))) BlockSum<1, WAVES> s_b;
+  const Piece<N> at(threadIdx.x, a.H);
+  NormRows<HF, YF, XF> next;
+  if (AHEAD) next.load_all(a, blockIdx.x, at);
+  // wg = w_post g_c: du w_post = alpha g_t dh (g_c w_post), only the product is needed
+  float wp[N], wg[N], gc[N], acc_pre[N], acc_post[N];
+  load_w(a.w_pre, at, wp);
+  load_w(a.w_post, at, wg);
+  load_w(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, at, gc);
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const Piece<N> at(threadIdx.x + c * blockDim.x, H);
-    load_w(a.w_pre, at, wp[c]);
-    load_w(a.w_post, at, wq[c]);
-    load_w(a.gate_kind == MOE_GATE_CHANNEL ? a.gate : nullptr, at, gc[c]);
-#pragma unroll
-    for (int n = 0; n < N; ++n) acc_pre[c][n] = acc_post[c][n] = acc_gate[c][n] = 0.f;
+  for (int n = 0; n < N; ++n) {
+    wg[n] *= gc[n];
+    acc_pre[n] = acc_post[n] = 0.f;
   }
+  s_a.init();
+  s_b.init();
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    NormRows<HF, YF, XF, C> q;
-    if (AHEAD) {
+    NormRows<HF, YF, XF> q;
+    if constexpr (AHEAD) {
       q = next;
-      if (t + gridDim.x < a.T) next.load(a, t + gridDim.x);
+      next.load_all(a, min(t + gridDim.x, (int64_t)a.T - 1), at);
+      q.keep_own(at);
+    } else if constexpr (REGULAR) {
+      q.load_all(a, t, at);
+      q.keep_own(at);
     } else {
-      q.load(a, t);
+      q.load(a, t, at);
     }
     float s[3] = {0.f, 0.f, 0.f};  // sums of h'^2, d h', y^2
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int n = 0; n < N; ++n) {
+      const float hv = q.h.get(n), yv = q.y.get(n);
+      s[0] = fmaf(hv, hv, s[0]);
+      s[1] = fmaf(wp[n] * q.x.get(n), hv, s[1]);
+      s[2] = fmaf(yv, yv, s[2]);
+    }
+    s_a.sum(s);
+    const float r = inv_sqrt(s[0] * a.per_h + a.eps), hm = r * r * (s[1] * a.per_h);
+    const float ry = a.w_post ? inv_sqrt(s[2] * a.per_h + a.eps) : 1.f;
+    float dh[N], dot[1] = {0.f};
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float hv = q.h[c].get(n), yv = q.y[c].get(n);
-        s[0] = fmaf(hv, hv, s[0]);
-        s[1] = fmaf(wp[c][n] * q.x[c].get(n), hv, s[1]);
-        s[2] = fmaf(yv, yv, s[2]);
-      }
-    block_sum(s, s_a);
-    const float r = 1.f / sqrtf(s[0] / H + a.eps), hm = r * r * (s[1] / H);
-    const float ry = a.w_post ? 1.f / sqrtf(s[2] / H + a.eps) : 1.f;
-    float dh[C][N], dot[1] = {0.f};
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float hv = q.h[c].get(n), xv = q.x[c].get(n);
-        dh[c][n] = fmaf(r, wp[c][n] * xv - hv * hm, q.d[c].get(n));
-        acc_pre[c][n] = fmaf(xv, hv * r, acc_pre[c][n]);
-        dot[0] = fmaf(dh[c][n] * gc[c][n] * wq[c][n], q.y[c].get(n), dot[0]);
-      }
-      if (a.dh) {
-        Chunk<HF, N> o;
-        o.set(dh[c]);
-        o.template store_own<true>(a.dh + t * a.h_pitch, Piece<N>(threadIdx.x + c * blockDim.x, H));
-      }
+    for (int n = 0; n < N; ++n) {
+      const float hv = q.h.get(n), xv = q.x.get(n);
+      dh[n] = fmaf(r, wp[n] * xv - hv * hm, q.d.get(n));
+      acc_pre[n] = fmaf(xv, hv * r, acc_pre[n]);
+      dot[0] = fmaf(dh[n] * wg[n], q.y.get(n), dot[0]);
+    }
+    if (a.dh) {
+      Chunk<HF, N> o;
+      o.set(dh);
+      o.template store_own<true>(a.dh + t * a.h_pitch, at);
     }
     if (!a.y) continue;
-    block_sum(dot, s_b);
-    const float gt = a.gate_kind == MOE_GATE_TOKEN ? a.gate[t] : 1.f, ag = a.alpha * gt;
-    const float ym = a.w_post ? ag * ry * ry * (dot[0] / H) : 0.f;
+    s_b.sum(dot);
+    const float ag = a.gate_kind == MOE_GATE_TOKEN ? a.alpha * a.gate[t] : a.alpha;
+    const float ym = a.w_post ? ag * ry * ry * (dot[0] * a.per_h) : 0.f;
     if (a.dgate_token && threadIdx.x == 0) a.dgate_token[t] = a.alpha * ry * dot[0];
+    float v[N];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      float v[N];
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const float yv = q.y[c].get(n), du = ag * gc[c][n] * dh[c][n], yr = yv * ry;
-        v[n] = ry * (wq[c][n] * du - yv * ym);
-        acc_post[c][n] = fmaf(du, yr, acc_post[c][n]);
-        acc_gate[c][n] = fmaf(a.alpha * dh[c][n], wq[c][n] * yr, acc_gate[c][n]);
-      }
-      if (a.dy) {
-        Chunk<YF, N> o;
-        o.set(v);
-        o.template store_own<true>(a.dy + t * a.y_pitch, Piece<N>(threadIdx.x + c * blockDim.x, H));
-      }
+    for (int n = 0; n < N; ++n) {
+      const float yv = q.y.get(n), du = ag * dh[n];
+      v[n] = ry * (wg[n] * du - yv * ym);
+      acc_post[n] = fmaf(du, yv * ry, acc_post[n]);
+    }
+    if (a.dy) {
+      Chunk<YF, N> o;
+      o.set(v);
+      o.template store_own<true>(a.dy + t * a.y_pitch, at);
     }
   }
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const Piece<N> at(threadIdx.x + c * blockDim.x, H);
-    const auto put = [&](int kind, const float(&v)[N]) {
-      if (kind < 0) return;
-      Chunk<MOE_AFMT_F32, N> o;
-      o.set(v);
-      o.store_own(reinterpret_cast<uint8_t*>(a.part + ((int64_t)kind * gridDim.x + blockIdx.x) * H), at);
-    };
-    put(a.part_pre, acc_pre[c]);
-    put(a.part_post, acc_post[c]);
-    put(a.part_gate, acc_gate[c]);
-  }
+  const auto put = [&](int kind, const float(&v)[N]) {
+    if (kind < 0) return;
+    Chunk<MOE_AFMT_F32, N> o;
+    o.set(v);
+    o.store_own(reinterpret_cast<uint8_t*>(a.part + ((int64_t)kind * gridDim.x + blockIdx.x) * a.H), at);
+  };
+  put(a.part_pre, acc_pre);
+  put(a.part_post, acc_post);
 }
 
-// out[kind][i] = sum over g of part[kind][g][i]: 64 channels per workgroup, its wavefronts
-// take rows w, w + 16, ... and are added in order.
+// The sum over the workgroups' partial rows, 32 channels per workgroup of this kernel: 32
+// groups of 32 lanes take rows g, g + 32, ... and are added in order.  Each kind goes to up to
+// two outputs, each with a factor per channel or none.
 struct NormOut {
-  float* p[3];
+  float* p[2][2];
+  const float* by[2][2];
 };
 __global__ __launch_bounds__(1024) void norm_reduce(const float* __restrict__ part, int G, int H, NormOut out) {
-  __shared__ float s_v[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = blockIdx.x * 64 + lane;
-  const float* p = part + (int64_t)blockIdx.y * G * H;
+  __shared__ float s_v[32][33];
+  const int lane = threadIdx.x & 31, group = threadIdx.x >> 5, i = blockIdx.x * 32 + lane, kind = blockIdx.y;
+  const float* p = part + (int64_t)kind * G * H;
   float v = 0.f;
   if (i < H) {
-#pragma unroll 16
-    for (int g = wave; g < G; g += 16) v += p[(int64_t)g * H + i];
+#pragma unroll 8
+    for (int g = group; g < G; g += 32) v += p[(int64_t)g * H + i];
   }
-  s_v[wave][lane] = v;
+  s_v[group][lane] = v;
   __syncthreads();
-  if (wave != 0 || i >= H) return;
+  if (group != 0 || i >= H) return;
   v = 0.f;
-  for (int w = 0; w < 16; ++w) v += s_v[w][lane];
-  out.p[blockIdx.y][i] = v;
+#pragma unroll
+  for (int g = 0; g < 32; ++g) v += s_v[g][lane];
+  for (int o = 0; o < 2; ++o)
+    if (out.p[kind][o]) out.p[kind][o][i] = out.by[kind][o] ? v * out.by[kind][o][i] : v;
 }
 
 namespace {
 
-int norm_waves(int H) { return std::min(kNormMaxWaves, (H + 64 * kNormN - 1) / (64 * kNormN)); }
+// Wavefronts of a row of H.
+int norm_waves(int H) { return (H + 64 * kNormN - 1) / (64 * kNormN); }
 
-// Workgroups of the gradient kernel when weights' gradients are wanted: one per CU, so that
-// the partial rows stay small beside the rows themselves.
-constexpr int kNormGroups = 256;
-int norm_groups(int T) { return std::min(T, kNormGroups); }
+// Workgroups of the gradient kernel when weights' gradients are wanted: eight wavefronts per
+// CU (of 256), in workgroups of 1 to 8, or one workgroup of up to 16.  Each leaves a partial row
+// per kind, so their number is kept low: at 2048 rows of 4096, 512 workgroups took 22.1 + 4.7 us,
+// 256 take 19.9 + 3.9.
+int norm_groups(int T, int H) { return std::min(T, 256 * std::clamp(8 / norm_waves(H), 1, 4)); }
 
 template <bool BACK, int HF, int YF, int XF>
 moe_status launch_norm_f(const NormArgs& a, int groups, hipStream_t s) {
   const int waves = norm_waves(a.H);
   const dim3 grid(groups), block(64 * waves);
-  const bool two = a.H > 64 * kNormMaxWaves * kNormN;
   if constexpr (BACK) {
-    if (two) return launch(block_norm_backward_kernel<HF, YF, XF, 2, kNormMaxWaves, false>, grid, block, s, a);
-    if (waves > 8) return launch(block_norm_backward_kernel<HF, YF, XF, 1, kNormMaxWaves, false>, grid, block, s, a);
-    return launch(block_norm_backward_kernel<HF, YF, XF, 1, 8, true>, grid, block, s, a);
+    const bool regular = a.H >= kNormN && a.dx && a.dh_in && a.y;
+    const auto kernel = !regular    ? block_norm_backward_kernel<HF, YF, XF, kNormMaxWaves, false>
+                        : waves > 8 ? block_norm_backward_kernel<HF, YF, XF, kNormMaxWaves, true>
+                                    : block_norm_backward_kernel<HF, YF, XF, 8, true>;
+    return launch(kernel, grid, block, s, a);
   } else {
-    if (two) return launch(block_norm_kernel<HF, YF, XF, 2>, grid, block, s, a);
-    return launch(block_norm_kernel<HF, YF, XF, 1>, grid, block, s, a);
+    const auto kernel = waves > 4 ? block_norm_kernel<HF, YF, XF, kNormMaxWaves> : block_norm_kernel<HF, YF, XF, 4>;
+    return launch(kernel, grid, block, s, a);
   }
 }
 
@@ -314,7 +335,7 @@ bool norm_config_ok(const moe_norm_config* c, NormArgs* a) {
   if (!c || c->T < 1 || c->T > kNormMaxT || c->H < 1 || c->H > kNormMaxH) return false;
   if (!fmt_ok(c->h_fmt) || !fmt_ok(c->y_fmt) || !fmt_ok(c->x_fmt)) return false;
   if (c->gate_kind < MOE_GATE_NONE || c->gate_kind > MOE_GATE_CHANNEL) return false;
-  if (!(c->eps > 0.f) || !(c->eps <= 1.f) || !(c->alpha - c->alpha == 0.f)) return false;
+  if (!(c->eps >= 0x1p-126f) || !(c->eps <= 1.f) || !(c->alpha - c->alpha == 0.f)) return false;
   const int64_t ld[3] = {c->ld_h ? c->ld_h : c->H, c->ld_y ? c->ld_y : c->H, c->ld_x ? c->ld_x : c->H};
   for (int64_t v : ld)
     if (v < c->H || v > (1ll << 40)) return false;
@@ -323,6 +344,7 @@ bool norm_config_ok(const moe_norm_config* c, NormArgs* a) {
   a->gate_kind = c->gate_kind;
   a->alpha = c->alpha;
   a->eps = c->eps;
+  a->per_h = 1.f / (float)c->H;
   a->h_pitch = ld[0] * fmt_bytes(c->h_fmt);
   a->y_pitch = ld[1] * fmt_bytes(c->y_fmt);
   a->x_pitch = ld[2] * fmt_bytes(c->x_fmt);
@@ -395,7 +417,7 @@ extern "C" MOE_API moe_status moe_block_norm(const moe_norm_config* cfg, const v
 
 extern "C" MOE_API int64_t moe_block_norm_workspace(int32_t T, int32_t H) {
   if (T < 1 || T > kNormMaxT || H < 1 || H > kNormMaxH) return -1;
-  return 3ll * norm_groups(T) * H * 4;
+  return 2ll * norm_groups(T, H) * H * 4;
 }
 
 extern "C" MOE_API moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* h_out, const void* y,
@@ -435,21 +457,28 @@ extern "C" MOE_API moe_status moe_block_norm_backward(const moe_norm_config* cfg
   a.dy = static_cast<uint8_t*>(dy);
   a.dgate_token = cfg->gate_kind == MOE_GATE_TOKEN ? dgate : nullptr;
   a.part = static_cast<float*>(ws);
+  // the kinds of partial sums and where each goes: dx h' r to dw_pre, alpha dh y ry to dw_post
+  // (by the channel gate) and the channel gate's gradient (by w_post)
   NormOut out_w{};
   int kinds = 0;
-  const auto want = [&](float* p) {
-    if (!p) return -1;
-    out_w.p[kinds] = p;
-    return kinds++;
-  };
-  a.part_pre = want(dw_pre);
-  a.part_post = want(dw_post);
-  a.part_gate = want(cfg->gate_kind == MOE_GATE_CHANNEL ? dgate : nullptr);
+  a.part_pre = a.part_post = -1;
+  if (dw_pre) {
+    out_w.p[kinds][0] = dw_pre;
+    a.part_pre = kinds++;
+  }
+  float* const dgate_c = cfg->gate_kind == MOE_GATE_CHANNEL ? dgate : nullptr;
+  if (dw_post || dgate_c) {
+    out_w.p[kinds][0] = dw_post;
+    out_w.by[kinds][0] = cfg->gate_kind == MOE_GATE_CHANNEL ? gate : nullptr;
+    out_w.p[kinds][1] = dgate_c;
+    out_w.by[kinds][1] = w_post;
+    a.part_post = kinds++;
+  }
   hipStream_t s = static_cast<hipStream_t>(stream);
   const StreamDevice on(s);
-  const int G = partial ? norm_groups(cfg->T) : cfg->T;
+  const int G = partial ? norm_groups(cfg->T, cfg->H) : cfg->T;
   const moe_status st = launch_norm<true>(*cfg, a, G, s);
   if (st != MOE_OK || !partial) return st;
-  return launch(norm_reduce, dim3((cfg->H + 63) / 64, kinds), dim3(1024), s, static_cast<const float*>(ws), G,
+  return launch(norm_reduce, dim3((cfg->H + 31) / 32, kinds), dim3(1024), s, static_cast<const float*>(ws), G,
                 (int)cfg->H, out_w);
 }

@@ -79,6 +79,27 @@ struct Chunk {
     for (int i = 0; i < kWords; ++i) q[i] = 0;
   }
 
+  // N elements at p.
+  __device__ __forceinline__ void load_at(const uint8_t* p) {
+    static_assert(kWords % 4 == 0, "16-byte accesses");
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) {
+      const u32x4 v = load16<false>(p + 4 * i);
+      q[i] = v[0];
+      q[i + 1] = v[1];
+      q[i + 2] = v[2];
+      q[i + 3] = v[3];
+    }
+  }
+  // Zeros for the first `skip` elements, without a branch.
+  __device__ __forceinline__ void keep_from(int skip) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (FMT == MOE_AFMT_BF16) q[i] &= (2 * i >= skip ? 0xffffu : 0u) | (2 * i + 1 >= skip ? 0xffff0000u : 0u);
+      else q[i] = i >= skip ? q[i] : 0;
+    }
+  }
+
   // The piece at its place in `row` (which must be on).  NT: a non-temporal load.
   template <bool NT = false>
   __device__ __forceinline__ void load(const uint8_t* row, const Piece<N>& s) {
@@ -174,10 +195,12 @@ struct Chunk {
 };
 
 // ---------------------------------------------------------------- host side
-// Whether sorted rows of this many bytes are read with non-temporal loads: half of the 256 MB
-// last-level cache and more, where most rows have left it by the time the last is written.
-// combine of 4096 tokens, k = 8, H = 2048 (128 MB of bf16 rows) from memory: 30.8 us against 33.8.
-// Of rows still in the cache it takes longer: 1024 tokens (32 MB) 10.0 us against 7.2.
+// Whether sorted rows of this many bytes pass by the caches (non-temporal loads where they
+// are read, stores where they are written): half of the 256 MB last-level cache and more,
+// where most rows have left it by the time the last is written.  At 4096 tokens, k = 8, H = 2048
+// (128 MB of bf16 rows), from memory: dispatch 27.1 us against 31.5, combine 30.8 against 33.8,
+// its gradient 56.8 against 62.2.  Of smaller rows, still in the cache when they are read, the
+// same loads cost: combine of 1024 tokens (32 MB) 10.0 us against 7.2.
 inline bool stream_rows(int64_t bytes) { return bytes >= (128ll << 20); }
 
 inline bool fmt_ok(int fmt) { return fmt == MOE_AFMT_F32 || fmt == MOE_AFMT_BF16; }

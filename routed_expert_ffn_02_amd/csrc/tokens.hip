@@ -25,12 +25,16 @@ constexpr int64_t kMoveMaxPairs = 1 << 26;
 //                     all keys in registers and a place is one compare and count per 64 pairs
 //   P <= kSolePairs   one launch sorts: each workgroup counts all pairs in LDS, those before
 //                     its own chunk apart from the others
-//   beyond            dispatch_count leaves one histogram per chunk, dispatch_place sums them;
-//                     the chunks grow with P so that there are at most kSortChunks of them
+//   beyond            dispatch_rank leaves each pair's rank within its chunk and one histogram
+//                     per chunk, dispatch_scan turns the histograms into first places, and the
+//                     move adds the two; the chunks grow with P so that there are at most
+//                     kSortChunks of them
 constexpr int kTinyPairs = 1024;
-constexpr int kSolePairs = 1 << 16;
+constexpr int kTinyPieces = 4096;  // and at most this many KB of rows of x: each piece counts again
+constexpr int kSolePairs = 8192;
 constexpr int kSortChunks = 256;
 constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
 
 struct SortPlan {
   int chunk, blocks;  // pairs per workgroup (a multiple of kSortThreads) and workgroups
@@ -41,16 +45,22 @@ inline SortPlan sort_plan(int64_t P) {
   return {chunk, (int)((P + chunk - 1) / chunk)};
 }
 
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int dpp_add(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROW_MASK, 0xf, false);
+}
+
 // Exclusive prefix of one int per thread over the workgroup (a multiple of 64 threads);
 // *total receives the sum.  s_wave: one int per wavefront.
 __device__ __forceinline__ int group_prefix(int v, int* s_wave, int* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
   int x = v;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int y = __shfl_up(x, off);
-    if (lane >= off) x += y;
-  }
+  x += dpp_add<0x111, 0xf>(x);  // row_shr:1, 2, 4, 8: prefixes of each 16-lane row
+  x += dpp_add<0x112, 0xf>(x);
+  x += dpp_add<0x114, 0xf>(x);
+  x += dpp_add<0x118, 0xf>(x);
+  x += dpp_add<0x142, 0xa>(x);  // row_bcast:15 into rows 1 and 3
+  x += dpp_add<0x143, 0xc>(x);  // row_bcast:31 into rows 2 and 3
   if (lane == 63) s_wave[wave] = x;
   __syncthreads();
   int base = 0, sum = 0;
@@ -60,20 +70,6 @@ __device__ __forceinline__ int group_prefix(int v, int* s_wave, int* total) {
   }
   *total = sum;
   return base + x - v;
-}
-
-__global__ __launch_bounds__(kSortThreads) void dispatch_count(const int32_t* __restrict__ idx, int P, int E, int chunk,
-                                                               int32_t* __restrict__ hist) {
-  __shared__ int s_n[kMaxExperts];
-  for (int e = threadIdx.x; e < E; e += kSortThreads) s_n[e] = 0;
-  __syncthreads();
-  const int lo = blockIdx.x * chunk, hi = min(lo + chunk, P);
-  for (int p = lo + threadIdx.x; p < hi; p += kSortThreads) {
-    const int e = idx[p];
-    if ((unsigned)e < (unsigned)E) atomicAdd(&s_n[e], 1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += kSortThreads) hist[(size_t)blockIdx.x * E + e] = s_n[e];
 }
 
 // Lanes of the wavefront whose key equals this lane's (key < 2^bits; a lane with valid =
@@ -87,98 +83,145 @@ __device__ __forceinline__ uint64_t wave_peers(int key, bool valid, int bits) {
   return valid ? m : 0;
 }
 
-// One workgroup per chunk.  SOLE: counts all pairs itself (hist unused); otherwise sums the
-// chunks' histograms.  Within the chunk a pair's place is its expert's base plus its rank
-// among the wavefront's lanes of the same expert plus what earlier wavefronts have of it.
-template <bool SOLE>
-__global__ __launch_bounds__(kSortThreads) void dispatch_place(const int32_t* __restrict__ idx, int P, int E, int bits,
-                                                               int chunk, const int32_t* __restrict__ hist,
-                                                               int32_t* __restrict__ perm, int32_t* __restrict__ inv,
-                                                               int32_t* __restrict__ offsets) {
-  constexpr int kWaves = kSortThreads / 64;
-  __shared__ int s_before[kMaxExperts], s_rest[kMaxExperts];
-  __shared__ uint16_t s_cnt[kWaves][kMaxExperts];
-  __shared__ int s_wave[kWaves];
+// One round of a chunk: kSortThreads pairs in order, e the thread's expert.  Returns the pair's
+// rank among the round's pairs of its expert (lanes of its wavefront before it, then earlier
+// wavefronts), and leaves the wavefronts' counts in s_cnt (zeroed here).
+__device__ __forceinline__ int round_rank(int e, bool kept, int E, int bits, uint16_t (*s_cnt)[kMaxExperts]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int blk = blockIdx.x, lo = blk * chunk, hi = min(lo + chunk, P);
-  int mine = lo + tid < hi ? idx[lo + tid] : -1;  // the first round's pair
-  if (tid < E) s_before[tid] = s_rest[tid] = 0;
-  __syncthreads();
-  if constexpr (SOLE) {
-    // 32 pairs per thread in flight, four to a load (chunks are multiples of four, so four
-    // neighbours lie on one side of lo)
-    constexpr int kLoads = 8;
-    for (int p0 = 4 * tid; p0 < P; p0 += 4 * kLoads * kSortThreads) {
-      u32x4 e[kLoads];
+  if (tid < E) {
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        const int p = p0 + 4 * u * kSortThreads;
-        e[u] = ~(u32x4)0;
-        if (p + 4 <= P) e[u] = load16<false>(reinterpret_cast<const uint8_t*>(idx + p));
-        else
-          for (int i = 0; i < 4; ++i)
-            if (p + i < P) e[u][i] = idx[p + i];
-      }
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        int* side = p0 + 4 * u * kSortThreads < lo ? s_before : s_rest;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (e[u][i] < (unsigned)E) atomicAdd(&side[e[u][i]], 1);
-      }
-    }
-  } else {
-    // the threads of an expert share its column of the histograms
-    const int parts = kSortThreads / E, e = tid % E, part = tid / E, nblk = gridDim.x;
-    if (part < parts) {
-      int before = 0, rest = 0;
-#pragma unroll 16
-      for (int c = part; c < nblk; c += parts) {
-        const int v = hist[(size_t)c * E + e];
-        before += c < blk ? v : 0;
-        rest += c < blk ? 0 : v;
-      }
-      atomicAdd(&s_before[e], before);
-      atomicAdd(&s_rest[e], rest);
-    }
+    for (int w = 0; w < kSortWaves; ++w) s_cnt[w][tid] = 0;
   }
   __syncthreads();
+  const uint64_t peers = wave_peers(e, kept, bits);
+  int rank = __popcll(peers & ((1ull << lane) - 1));
+  if (kept && rank == 0) s_cnt[wave][e] = (uint16_t)__popcll(peers);
+  __syncthreads();
+  if (kept) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) rank += w < wave ? s_cnt[w][e] : 0;
+  }
+  return rank;
+}
+__device__ __forceinline__ int round_total(int e, const uint16_t (*s_cnt)[kMaxExperts]) {
+  int n = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w) n += s_cnt[w][e];
+  return n;
+}
+
+// The whole sort, one workgroup per chunk of kSortThreads pairs.
+__global__ __launch_bounds__(kSortThreads) void dispatch_place(const int32_t* __restrict__ idx, int P, int E, int bits,
+                                                               int32_t* __restrict__ perm, int32_t* __restrict__ inv,
+                                                               int32_t* __restrict__ offsets) {
+  __shared__ int s_before[kMaxExperts], s_rest[kMaxExperts];
+  __shared__ uint16_t s_cnt[kSortWaves][kMaxExperts];
+  __shared__ int s_wave[kSortWaves];
+  const int tid = threadIdx.x, lo = blockIdx.x * kSortThreads, p = lo + tid;
+  const int mine = p < P ? idx[p] : -1;
+  if (tid < E) s_before[tid] = s_rest[tid] = 0;
+  __syncthreads();
+  // four pairs to a load (chunks are multiples of four, so four neighbours lie on one side
+  // of lo), all of them in flight
+  constexpr int kLoads = (kSolePairs + 4 * kSortThreads - 1) / (4 * kSortThreads);
+  u32x4 e[kLoads];
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int p0 = 4 * (u * kSortThreads + tid);
+    e[u] = ~(u32x4)0;
+    if (p0 + 4 <= P) {
+      e[u] = load16<false>(reinterpret_cast<const uint8_t*>(idx + p0));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (p0 + i < P) e[u][i] = idx[p0 + i];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    int* side = 4 * (u * kSortThreads + tid) < lo ? s_before : s_rest;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e[u][i] < (unsigned)E) atomicAdd(&side[e[u][i]], 1);
+  }
+  const bool kept = (unsigned)mine < (unsigned)E;
+  const int rank = round_rank(mine, kept, E, bits, s_cnt);  // its barriers end the counting
   // an expert's first place in this chunk: kept pairs of lower experts, then its own pairs
   // in earlier chunks
   const int before = tid < E ? s_before[tid] : 0;
   int kept_all;
   const int base = group_prefix(before + (tid < E ? s_rest[tid] : 0), s_wave, &kept_all);
-  if (blk == 0) {
+  if (blockIdx.x == 0) {
     if (tid < E) offsets[tid] = base;
     if (tid == 0) offsets[E] = kept_all;
   }
   if (tid < E) s_before[tid] = base + before;
+  __syncthreads();
+  const int pos = kept ? s_before[mine] + rank : -1;
+  if (kept) perm[pos] = p;
+  if (p < P) inv[p] = pos;
+}
+
+__global__ __launch_bounds__(kSortThreads) void dispatch_rank(const int32_t* __restrict__ idx, int P, int E, int bits,
+                                                              int chunk, int32_t* __restrict__ hist,
+                                                              int32_t* __restrict__ ranks) {
+  __shared__ int s_run[kMaxExperts];
+  __shared__ uint16_t s_cnt[kSortWaves][kMaxExperts];
+  const int tid = threadIdx.x, lo = blockIdx.x * chunk, hi = min(lo + chunk, P);
+  if (tid < E) s_run[tid] = 0;
   for (int r0 = lo; r0 < hi; r0 += kSortThreads) {
-    for (int w = 0; w < kWaves; ++w)
-      if (tid < E) s_cnt[w][tid] = 0;
-    __syncthreads();  // also: the bases of the last round
-    const int p = r0 + tid, e = mine;
-    mine = p + kSortThreads < hi ? idx[p + kSortThreads] : -1;
+    const int p = r0 + tid, e = p < hi ? idx[p] : -1;
     const bool kept = (unsigned)e < (unsigned)E;
-    const uint64_t peers = wave_peers(e, kept, bits);
-    const int rank = __popcll(peers & ((1ull << lane) - 1));
-    if (kept && rank == 0) s_cnt[wave][e] = (uint16_t)__popcll(peers);
+    const int rank = round_rank(e, kept, E, bits, s_cnt);
+    if (kept) ranks[p] = s_run[e] + rank;
     __syncthreads();
-    int pos = -1;
-    if (kept) {
-      pos = s_before[e] + rank;
+    if (tid < E) s_run[tid] += round_total(tid, s_cnt);
+  }
+  if (tid < E) hist[(size_t)blockIdx.x * E + tid] = s_run[tid];
+}
+
+// hist[c][e] (pairs of expert e in chunk c) to the first place of those pairs, and the offsets.
+// One workgroup; kParts threads share an expert's column where there are fewer experts.
+__global__ __launch_bounds__(kSortThreads) void dispatch_scan(int32_t* __restrict__ hist, int E, int chunks,
+                                                              int32_t* __restrict__ offsets) {
+  __shared__ int s_part[kSortThreads], s_base[kMaxExperts], s_wave[kSortWaves];
+  const int tid = threadIdx.x, parts = kSortThreads / E, e = tid % E, part = tid / E;
+  const int per = (chunks + parts - 1) / parts, c0 = part * per, c1 = part < parts ? min(c0 + per, chunks) : 0;
+  constexpr int kHold = 16;  // a column's piece stays in registers up to this length
+  int v[kHold], sum = 0;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) pos += w < wave ? s_cnt[w][e] : 0;
-      perm[pos] = p;
-    }
-    if (p < hi) inv[p] = pos;
-    __syncthreads();
-    if (tid < E) {
-      int n = 0;
+  for (int i = 0; i < kHold; ++i) {
+    v[i] = c0 + i < c1 ? hist[(size_t)(c0 + i) * E + e] : 0;
+    sum += v[i];
+  }
+#pragma unroll 8
+  for (int c = c0 + kHold; c < c1; ++c) sum += hist[(size_t)c * E + e];
+  s_part[tid] = sum;
+  __syncthreads();
+  int total = 0;
+  if (tid < E)
+    for (int q = 0; q < parts; ++q) total += s_part[q * E + tid];
+  int kept_all;
+  const int base = group_prefix(total, s_wave, &kept_all);
+  if (tid < E) {
+    offsets[tid] = base;
+    s_base[tid] = base;
+  }
+  if (tid == 0) offsets[E] = kept_all;
+  __syncthreads();
+  if (part >= parts) return;
+  int at = s_base[e];
+  for (int q = 0; q < part; ++q) at += s_part[q * E + e];
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) n += s_cnt[w][tid];
-      s_before[tid] += n;
+  for (int i = 0; i < kHold; ++i)
+    if (c0 + i < c1) {
+      hist[(size_t)(c0 + i) * E + e] = at;
+      at += v[i];
     }
+  for (int c = c0 + kHold; c < c1; ++c) {
+    const int n = hist[(size_t)c * E + e];
+    hist[(size_t)c * E + e] = at;
+    at += n;
   }
 }
 
@@ -196,46 +239,58 @@ __device__ __forceinline__ int wave_token() {
 }
 
 // ---------------------------------------------------------------------------
-// Rows of x to their sorted places: a wavefront takes one token and U * 1 KB of its row,
-// reads it once and writes it k times.
-template <int EB, int U>  // bytes of an element, 16-byte loads per lane
-struct RowPiece {
-  static constexpr int FMT = EB == 2 ? MOE_AFMT_BF16 : MOE_AFMT_F32, N = 16 / EB;
-  Chunk<FMT, N> q[U];
-  __device__ __forceinline__ static Piece<N> at(int u, int H) {
-    return Piece<N>((blockIdx.y * U + u) * 64 + (threadIdx.x & 63), H);
-  }
-  __device__ __forceinline__ void load(const uint8_t* row, int H) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (at(u, H).on) q[u].load(row, at(u, H));
-  }
-  __device__ __forceinline__ void store(uint8_t* row, int H) const {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (at(u, H).on) q[u].store(row, at(u, H));
-  }
+// Rows of x to their sorted places.  A workgroup takes one token and 4 KB of its row, 16 bytes
+// a thread, reads them once and writes them k times.  FIND: the pairs' places come from their
+// ranks and the chunks' first places (lane j finds rank j's), and the tables are written
+// beside the rows (by the workgroup of blockIdx.y = 0); otherwise from inv.  NT: stores that
+// do not stay in the caches, see stream_rows.
+struct MoveArgs {
+  const uint8_t* x;         // nullptr: the tables alone
+  int64_t pitch;
+  int T, k, E, H;
+  uint8_t* xs;
+  int32_t* inv;             // [T,k] read, or written (FIND)
+  const int32_t* idx;       // FIND: [T,k] expert ids,
+  int chunk;                // pairs of a chunk,
+  const int32_t* first;     // [chunks,E] first places,
+  const int32_t* ranks;     // [T,k] ranks within the chunk
+  int32_t* perm;            // and the other table
 };
-constexpr int kMoveLoads = 4;
 
-template <int EB>
-__global__ __launch_bounds__(256) void dispatch_move(const uint8_t* __restrict__ x, int64_t pitch, int T, int k, int H,
-                                                     const int32_t* __restrict__ inv, uint8_t* __restrict__ xs) {
-  const int t = wave_token();
-  if (t >= T) return;
-  RowPiece<EB, kMoveLoads> r;
-  r.load(x + (int64_t)t * pitch, H);
-  const int64_t P = (int64_t)T * k;
-  for (int j = 0; j < k; ++j) {
-    const int pos = inv[(int64_t)t * k + j];
-    if ((unsigned)pos < (uint64_t)P) r.store(xs + (int64_t)pos * H * EB, H);
+template <int EB, bool FIND, bool NT>
+__global__ __launch_bounds__(256) void dispatch_move(MoveArgs a) {
+  constexpr int FMT = EB == 2 ? MOE_AFMT_BF16 : MOE_AFMT_F32, N = 16 / EB;
+  const int t = blockIdx.x, lane = threadIdx.x & 63;
+  const Piece<N> at(blockIdx.y * 256 + threadIdx.x, a.H);
+  Chunk<FMT, N> q;
+  if (a.x && at.on) q.load(a.x + (int64_t)t * a.pitch, at);
+  for (int j0 = 0; j0 < a.k; j0 += 64) {
+    const int p = t * a.k + j0 + lane, n = min(64, a.k - j0);
+    int mine = -1;
+    if (lane < n) {
+      if constexpr (FIND) {
+        const int e = a.idx[p];
+        if ((unsigned)e < (unsigned)a.E) mine = a.first[(size_t)(p / a.chunk) * a.E + e] + a.ranks[p];
+        if (blockIdx.y == 0 && threadIdx.x < 64) {
+          a.inv[p] = mine;
+          if (mine >= 0) a.perm[mine] = p;
+        }
+      } else {
+        mine = a.inv[p];
+      }
+    }
+    if (!a.x) continue;
+    for (int j = 0; j < n; ++j) {
+      const int pos = __builtin_amdgcn_readlane(mine, j);
+      if (pos >= 0 && at.on) q.template store<NT>(a.xs + (int64_t)pos * a.H * EB, at);
+    }
   }
 }
 
 // The sort and the move of at most kTinyPairs pairs in one launch.  A pair's key is
-// (expert, pair) in one word; its place is the number of smaller keys.  The last workgroup
-// (of blockIdx.y = 0) writes the offsets.
-template <int EB, int U>
+// (expert, pair) in one word; its place is the number of smaller keys.  A wavefront takes one
+// token and 1 KB of its row; the last workgroup (of blockIdx.y = 0) writes the offsets.
+template <int EB, int R>  // R: 64-pair registers of keys
 __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__ idx, int T, int k, int E,
                                                      const uint8_t* __restrict__ x, int64_t pitch, int H,
                                                      uint8_t* __restrict__ xs, int32_t* __restrict__ perm,
@@ -267,12 +322,13 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
   }
   const int t = wave_token();
   if (t >= T) return;
-  RowPiece<EB, U> r;
-  if (x) r.load(x + (int64_t)t * pitch, H);
-  constexpr int kRegs = kTinyPairs / 64;
-  uint32_t key[kRegs];
+  constexpr int FMT = EB == 2 ? MOE_AFMT_BF16 : MOE_AFMT_F32, N = 16 / EB;
+  const Piece<N> at(blockIdx.y * 64 + lane, H);
+  Chunk<FMT, N> q;
+  if (x && at.on) q.load(x + (int64_t)t * pitch, at);
+  uint32_t key[R];
 #pragma unroll
-  for (int i = 0; i < kRegs; ++i) {
+  for (int i = 0; i < R; ++i) {
     const int p = 64 * i + lane;
     const int e = p < P ? idx[p] : -1;
     key[i] = (unsigned)e < (unsigned)E ? (uint32_t)e << 10 | p : 0xffffffffu;
@@ -286,9 +342,8 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
       const uint32_t own = (uint32_t)e << 10 | p;
       pos = 0;
 #pragma unroll
-      for (int i = 0; i < kRegs; ++i)
-        if (64 * i < P) pos += __popcll(__ballot(key[i] < own));
-      if (x) r.store(xs + (int64_t)pos * H * EB, H);
+      for (int i = 0; i < R; ++i) pos += __popcll(__ballot(key[i] < own));
+      if (x && at.on) q.store(xs + (int64_t)pos * H * EB, at);
     }
     if (lane == (j & 63)) mine = pos;
     if (blockIdx.y == 0 && ((j & 63) == 63 || j == k - 1)) {
@@ -548,7 +603,7 @@ using namespace rmoe;
 extern "C" MOE_API int64_t moe_dispatch_workspace(int32_t T, int32_t k, int32_t n_experts) {
   if (!move_shape_ok(T, k, 1) || n_experts < 1 || n_experts > kMaxExperts) return -1;
   const int64_t P = (int64_t)T * k;
-  return P <= kSolePairs ? 0 : (int64_t)sort_plan(P).blocks * n_experts * 4;
+  return P <= kSolePairs ? 0 : 4 * ((int64_t)sort_plan(P).blocks * n_experts + P);
 }
 
 extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, int32_t k, int32_t n_experts,
@@ -579,37 +634,43 @@ extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, i
   const uint8_t* src = static_cast<const uint8_t*>(x);
   uint8_t* dst = static_cast<uint8_t*>(xs);
   const int64_t eb = x ? fmt_bytes(fmt) : 4, pitch = ld * eb, row_bytes = x ? H * eb : 1;
-  if (P <= kTinyPairs) {
-    // few tokens: 1 KB per wavefront, so that one row is spread over more of them
-    const bool thin = (int64_t)T * ((row_bytes + 4095) / 4096) < 1024;
-    const int piece = thin ? 1024 : 1024 * kMoveLoads;
-    const dim3 grid((T + 3) / 4 + 1, (unsigned)((row_bytes + piece - 1) / piece)), block(256);
-    if (eb == 2)
-      return launch(thin ? dispatch_tiny<2, 1> : dispatch_tiny<2, kMoveLoads>, grid, block, s, topk_idx, T, k, n_experts,
-                    src, pitch, H, dst, perm, inv, offsets);
-    return launch(thin ? dispatch_tiny<4, 1> : dispatch_tiny<4, kMoveLoads>, grid, block, s, topk_idx, T, k, n_experts, src,
-                  pitch, H, dst, perm, inv, offsets);
+  if (P <= kTinyPairs && T * ((row_bytes + 1023) / 1024) <= kTinyPieces) {
+    const dim3 grid((T + 3) / 4 + 1, (unsigned)((row_bytes + 1023) / 1024)), block(256);
+    const auto go = [&](auto kernel) {
+      return launch(kernel, grid, block, s, topk_idx, T, k, n_experts, src, pitch, H, dst, perm, inv, offsets);
+    };
+    if (P <= 64) return eb == 2 ? go(dispatch_tiny<2, 1>) : go(dispatch_tiny<4, 1>);
+    if (P <= 256) return eb == 2 ? go(dispatch_tiny<2, 4>) : go(dispatch_tiny<4, 4>);
+    return eb == 2 ? go(dispatch_tiny<2, kTinyPairs / 64>) : go(dispatch_tiny<4, kTinyPairs / 64>);
   }
-  const SortPlan sp = sort_plan(P);
   int bits = 0;
   while ((1 << bits) < n_experts) ++bits;
-  int32_t* hist = static_cast<int32_t*>(ws);
-  const dim3 chunks(sp.blocks), threads(kSortThreads);
-  moe_status st;
+  const dim3 threads(kSortThreads);
+  MoveArgs m{src, pitch, T, k, n_experts, H, dst, inv};
+  const auto move = [&](auto find) {
+    constexpr bool F = find();
+    const bool nt = stream_rows(P * row_bytes);
+    const auto kernel = eb == 2 ? (nt ? dispatch_move<2, F, true> : dispatch_move<2, F, false>)
+                                : (nt ? dispatch_move<4, F, true> : dispatch_move<4, F, false>);
+    return launch(kernel, dim3(T, (unsigned)((row_bytes + 4095) / 4096)), dim3(256), s, m);
+  };
   if (P <= kSolePairs) {
-    st = launch(dispatch_place<true>, chunks, threads, s, topk_idx, (int)P, n_experts, bits, sp.chunk,
-                static_cast<const int32_t*>(nullptr), perm, inv, offsets);
-  } else {
-    st = launch(dispatch_count, chunks, threads, s, topk_idx, (int)P, n_experts, sp.chunk, hist);
-    if (st == MOE_OK)
-      st = launch(dispatch_place<false>, chunks, threads, s, topk_idx, (int)P, n_experts, bits, sp.chunk,
-                  static_cast<const int32_t*>(hist), perm, inv, offsets);
+    const dim3 chunks((unsigned)((P + kSortThreads - 1) / kSortThreads));
+    const moe_status st = launch(dispatch_place, chunks, threads, s, topk_idx, (int)P, n_experts, bits, perm, inv, offsets);
+    return st != MOE_OK || !x ? st : move(std::false_type{});
   }
-  if (st != MOE_OK || !x) return st;
-  const int piece = 1024 * kMoveLoads;
-  const dim3 grid((T + 3) / 4, (unsigned)((row_bytes + piece - 1) / piece)), block(256);
-  return launch(eb == 2 ? dispatch_move<2> : dispatch_move<4>, grid, block, s, src, pitch, T, k, H,
-                static_cast<const int32_t*>(inv), dst);
+  const SortPlan sp = sort_plan(P);
+  int32_t* hist = static_cast<int32_t*>(ws);
+  int32_t* ranks = hist + (int64_t)sp.blocks * n_experts;
+  moe_status st = launch(dispatch_rank, dim3(sp.blocks), threads, s, topk_idx, (int)P, n_experts, bits, sp.chunk, hist, ranks);
+  if (st == MOE_OK) st = launch(dispatch_scan, dim3(1), threads, s, hist, n_experts, sp.blocks, offsets);
+  if (st != MOE_OK) return st;
+  m.idx = topk_idx;
+  m.chunk = sp.chunk;
+  m.first = hist;
+  m.ranks = ranks;
+  m.perm = perm;
+  return move(std::true_type{});
 }
 
 extern "C" MOE_API moe_status moe_dispatch_backward(const void* dxs, int32_t dxs_fmt, const int32_t* inv, int32_t T,

@@ -16,9 +16,9 @@ GATES = ("none", "token", "channel")
 
 
 def depth(H):
-    """Additions a term of a row's sum passes through: 8 or 16 in its thread, six between lanes, up to
+    """Additions a term of a row's sum passes through: 8 in its thread, six between lanes, up to
     sixteen between wavefronts."""
-    return 16 + 6 + 16
+    return 8 + 6 + 16
 
 
 def kind(gate):
@@ -85,7 +85,7 @@ def back(v, h_out, gate, alpha, out, dh=True, dx=True, ws=True, stream=None):
                               out.get("dw_pre"), w, gate_kind=kind(gate), alpha=alpha, eps=EPS, stream=stream)
 
 
-SHAPES = [(1, 1), (1, 2048), (2, 7), (3, 64), (5, 513), (4, 4096), (33, 1999), (9, 8192), (3, 8200), (2, 16384), (700, 96),
+SHAPES = [(1, 1), (1, 2048), (2, 7), (3, 64), (5, 513), (4, 4096), (33, 1999), (9, 8192), (3, 8191), (2, 4104), (700, 96),
           (300, 2056)]
 
 
