@@ -113,7 +113,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_kernel(NormArgs a) {
     for (int n = 0; n < N; ++n) h[n] = fmaf(scale * qy.get(n), wq[n] * g[n], h[n]);
     Chunk<HF, N> o;
     o.set(h);
-    o.template store_own<true>(a.h_out + t * a.h_pitch, at);
+    o.template store_wave<true>(a.h_out + t * a.h_pitch, at, a.H);
   }
   if (!a.x_out) return;
   float s[1] = {0.f};
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_kernel(NormArgs a) {
   for (int n = 0; n < N; ++n) wp[n] = h[n] * r * wp[n];
   Chunk<XF, N> o;
   o.set(wp);
-  o.template store_own<true>(a.x_out + t * a.x_pitch, at);
+  o.template store_wave<true>(a.x_out + t * a.x_pitch, at, a.H);
 }
 
 // A chunk of one token's rows in the gradient, as stored.
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_backward_kernel(NormArg
     if (a.dh) {
       Chunk<HF, N> o;
       o.set(dh);
-      o.template store_own<true>(a.dh + t * a.h_pitch, at);
+      o.template store_wave<true>(a.dh + t * a.h_pitch, at, a.H);
     }
     if (!a.y) continue;
     s_b.sum(dot);
@@ -248,14 +248,14 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_backward_kernel(NormArg
     if (a.dy) {
       Chunk<YF, N> o;
       o.set(v);
-      o.template store_own<true>(a.dy + t * a.y_pitch, at);
+      o.template store_wave<true>(a.dy + t * a.y_pitch, at, a.H);
     }
   }
   const auto put = [&](int kind, const float(&v)[N]) {
     if (kind < 0) return;
     Chunk<MOE_AFMT_F32, N> o;
     o.set(v);
-    o.store_own(reinterpret_cast<uint8_t*>(a.part + ((int64_t)kind * gridDim.x + blockIdx.x) * a.H), at);
+    o.store_wave(reinterpret_cast<uint8_t*>(a.part + ((int64_t)kind * gridDim.x + blockIdx.x) * a.H), at, a.H);
   };
   put(a.part_pre, acc_pre);
   put(a.part_post, acc_post);

@@ -397,7 +397,7 @@ __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ 
   }
   Chunk<YF, N> o;
   o.set(acc);
-  o.template store<true>(y + (int64_t)t * pitch, at);
+  o.template store_wave<true>(y + (int64_t)t * pitch, at, H);
 }
 
 // ---------------------------------------------------------------------------
@@ -454,7 +454,7 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
 #pragma unroll
           for (int n = 0; n < N; ++n) v[n] = g[j] * d.get(n);
           q[j].set(v);
-          q[j].template store_own<true>(dys + (int64_t)pos[j] * H * RB, at);
+          q[j].template store_wave<true>(dys + (int64_t)pos[j] * H * RB, at, H);
         }
     }
   }
