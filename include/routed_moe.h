@@ -607,8 +607,8 @@ MOE_API moe_status moe_pool_load(moe_ctx* ctx, const char* path, int32_t threads
  *    element is rounded once, to nearest even, to its format.
  *  - An output shares no byte with an input or another output unless the call says so (blocks side
  *    by side in the rows of one buffer are told apart when their strides in bytes are equal).
- *  - Limits: 1 <= T <= 2^22, 1 <= k <= 1024, T*k <= 2^26, n_experts <= 1024, H <= 65536 (moves) or
- *    8192 (norms).
+ *  - Limits: 1 <= T <= 2^21, 1 <= k <= 1024, T*k <= 2^26, n_experts <= 1024, H <= 65536 (moves) or
+ *    8192 (norms), ld <= 2^36.
  *  - MOE_EINVAL for a null pointer, shape, format, stride, alignment, overlap or short workspace
  *    (nothing is enqueued); MOE_EHIP if a launch fails.
  */

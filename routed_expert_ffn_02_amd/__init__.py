@@ -475,6 +475,7 @@ def moe_permute_noalloc(slot_idx, P: int, n_slot_range: int, perm, offsets, grou
 # Around the experts.  These take torch tensors only and read shapes, formats and row strides
 # from them; a tensor the library would misread (type, shape, stride, device) is refused here.
 _FMT = {torch.float32: MOE_AFMT_F32, torch.bfloat16: MOE_AFMT_BF16}
+_I32_MAX = 0x7fffffff
 
 
 # the current stream's handle and the current device without the objects around them
@@ -511,7 +512,7 @@ class _Args:
             ld, step = t.stride()
         except (AttributeError, KeyError, ValueError):
             self.refuse(f"{name} must be a two-dimensional fp32 or bf16 tensor")
-        if n < 1 or h < 1 or (n_rows is not None and n != n_rows) or (width is not None and h != width):
+        if n < 1 or h < 1 or n > _I32_MAX or h > _I32_MAX or (n_rows is not None and n != n_rows) or (width is not None and h != width):
             self.refuse(f"{name} has shape {(n, h)}, not {(n_rows or 'T', width or 'H')}")
         if n == 1:
             ld = h
@@ -543,7 +544,7 @@ class _Args:
             T, k = t.shape
         except (AttributeError, ValueError):
             T = k = 0
-        if not T or not k:
+        if not T or not k or T > _I32_MAX or k > _I32_MAX:
             self.refuse(f"{name} must be an int32 tensor [T, k]")
         return T, k, self.flat(name, t, torch.int32, T, k)
 
@@ -702,32 +703,30 @@ def moe_block_norm_backward(h_out, y, w_post, gate, w_pre, dh_out, dx, dh, dy, d
                             stream=None) -> None:
     """The gradient of moe_block_norm from dh_out and dx (either may be None); any output may be None."""
     a = _Args("moe_block_norm_backward")
-    lead = next((t for t in (dh_out, dx) if t is not None), None)
+    lead = dx if dh_out is None else dh_out
     if not isinstance(lead, torch.Tensor) or lead.dim() != 2:
         a.refuse("dh_out or dx must be given")
     T, H = lead.shape
+    # (format, row stride) that h_out, dh_out and dh share, and y and dy
     h_like = y_like = None
     hp = yp = dhp = dxp = o_h = o_y = None
-    x_fmt, ld_x = 0, H
+    h_fmt = y_fmt = x_fmt = 0
+    ld_h = ld_y = ld_x = H
     if dh_out is not None:
-        dhp, *h_like = a.rows("dh_out", dh_out, T, H)[:3]
-        h_like = tuple(h_like)
+        dhp, h_fmt, ld_h, _, _ = a.rows("dh_out", dh_out, T, H)
+        h_like = h_fmt, ld_h
     if h_out is not None:
-        hp, *like = a.rows("h_out", h_out, T, H, False, h_like)[:3]
-        h_like = tuple(like)
+        hp, h_fmt, ld_h, _, _ = a.rows("h_out", h_out, T, H, False, h_like)
+        h_like = h_fmt, ld_h
     if dh is not None:
-        o_h, *like = a.rows("dh", dh, T, H, False, h_like)[:3]
-        h_like = tuple(like)
+        o_h, h_fmt, ld_h, _, _ = a.rows("dh", dh, T, H, False, h_like)
     if y is not None:
-        yp, *like = a.rows("y", y, T, H)[:3]
-        y_like = tuple(like)
+        yp, y_fmt, ld_y, _, _ = a.rows("y", y, T, H)
+        y_like = y_fmt, ld_y
     if dy is not None:
-        o_y, *like = a.rows("dy", dy, T, H, False, y_like)[:3]
-        y_like = tuple(like)
+        o_y, y_fmt, ld_y, _, _ = a.rows("dy", dy, T, H, False, y_like)
     if dx is not None:
         dxp, x_fmt, ld_x, _, _ = a.rows("dx", dx, T, H)
-    h_fmt, ld_h = h_like or (0, H)
-    y_fmt, ld_y = y_like or (0, H)
     q, g, p = _norm_inputs(a, T, H, w_post, gate, w_pre, gate_kind)
     dq = None if dw_post is None else a.flat("dw_post", dw_post, torch.float32, H)
     dp = None if dw_pre is None else a.flat("dw_pre", dw_pre, torch.float32, H)

@@ -17,7 +17,7 @@ constexpr int kNormMaxWaves = 16;  // of a workgroup
 // not fit the 128 registers of a 1024-thread workgroup: 165 us at 1000 rows of 16384, bf16,
 // against 28 at 8192.)
 constexpr int kNormMaxH = 64 * kNormMaxWaves * kNormN;
-constexpr int kNormMaxT = 1 << 22;
+constexpr int kNormMaxT = 1 << 21;  // a launch of T workgroups of 1024 threads stays below 2^32
 
 struct NormArgs {
   int T, H, gate_kind;
@@ -338,7 +338,7 @@ bool norm_config_ok(const moe_norm_config* c, NormArgs* a) {
   if (!(c->eps >= 0x1p-126f) || !(c->eps <= 1.f) || !(c->alpha - c->alpha == 0.f)) return false;
   const int64_t ld[3] = {c->ld_h ? c->ld_h : c->H, c->ld_y ? c->ld_y : c->H, c->ld_x ? c->ld_x : c->H};
   for (int64_t v : ld)
-    if (v < c->H || v > (1ll << 40)) return false;
+    if (v < c->H || v > kMaxStride) return false;
   a->T = c->T;
   a->H = c->H;
   a->gate_kind = c->gate_kind;

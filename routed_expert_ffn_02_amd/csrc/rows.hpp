@@ -228,6 +228,7 @@ struct Chunk {
 // same loads cost: combine of 1024 tokens (32 MB) 10.0 us against 7.2.
 inline bool stream_rows(int64_t bytes) { return bytes >= (128ll << 20); }
 
+constexpr int64_t kMaxStride = 1ll << 36;  // elements between rows: byte offsets of 2^21 rows stay in 64 bits
 inline bool fmt_ok(int fmt) { return fmt == MOE_AFMT_F32 || fmt == MOE_AFMT_BF16; }
 inline int64_t fmt_bytes(int fmt) { return fmt == MOE_AFMT_BF16 ? 2 : 4; }
 inline bool aligned_to(const void* p, int64_t a) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(a - 1)) == 0; }

@@ -14,7 +14,7 @@
 namespace rmoe {
 
 constexpr int kMoveMaxH = 1 << 16;       // elements of a row
-constexpr int kMoveMaxT = 1 << 22;       // tokens
+constexpr int kMoveMaxT = 1 << 21;       // tokens
 constexpr int kMoveMaxK = 1024;          // ranks
 constexpr int64_t kMoveMaxPairs = 1 << 26;
 
@@ -50,10 +50,11 @@ __device__ __forceinline__ int dpp_add(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, ROW_MASK, 0xf, false);
 }
 
-// Exclusive prefix of one int per thread over the workgroup (a multiple of 64 threads);
-// *total receives the sum.  s_wave: one int per wavefront.
+// Exclusive prefix of one int per thread over a workgroup of W wavefronts; *total receives the
+// sum.  s_wave: one int per wavefront.
+template <int W>
 __device__ __forceinline__ int group_prefix(int v, int* s_wave, int* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int x = v;
   x += dpp_add<0x111, 0xf>(x);  // row_shr:1, 2, 4, 8: prefixes of each 16-lane row
   x += dpp_add<0x112, 0xf>(x);
@@ -64,9 +65,11 @@ __device__ __forceinline__ int group_prefix(int v, int* s_wave, int* total) {
   if (lane == 63) s_wave[wave] = x;
   __syncthreads();
   int base = 0, sum = 0;
-  for (int w = 0; w < nw; ++w) {
-    base += w < wave ? s_wave[w] : 0;
-    sum += s_wave[w];
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const int n = s_wave[w];
+    base += w < wave ? n : 0;
+    sum += n;
   }
   *total = sum;
   return base + x - v;
@@ -150,15 +153,16 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_place(const int32_t* __
   // in earlier chunks
   const int before = tid < E ? s_before[tid] : 0;
   int kept_all;
-  const int base = group_prefix(before + (tid < E ? s_rest[tid] : 0), s_wave, &kept_all);
+  const int base = group_prefix<kSortWaves>(before + (tid < E ? s_rest[tid] : 0), s_wave, &kept_all);
   if (blockIdx.x == 0) {
     if (tid < E) offsets[tid] = base;
     if (tid == 0) offsets[E] = kept_all;
   }
   if (tid < E) s_before[tid] = base + before;
   __syncthreads();
-  const int pos = kept ? s_before[mine] + rank : -1;
-  if (kept) perm[pos] = p;
+  int pos = kept ? s_before[mine] + rank : -1;
+  if (pos >= P) pos = -1;  // only if the ids changed under the kernel
+  if (pos >= 0) perm[pos] = p;
   if (p < P) inv[p] = pos;
 }
 
@@ -181,11 +185,12 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_rank(const int32_t* __r
 }
 
 // hist[c][e] (pairs of expert e in chunk c) to the first place of those pairs, and the offsets.
-// One workgroup; kParts threads share an expert's column where there are fewer experts.
+// One workgroup; where there are fewer experts than threads, up to kScanParts share a column.
+constexpr int kScanParts = 16;
 __global__ __launch_bounds__(kSortThreads) void dispatch_scan(int32_t* __restrict__ hist, int E, int chunks,
                                                               int32_t* __restrict__ offsets) {
   __shared__ int s_part[kSortThreads], s_base[kMaxExperts], s_wave[kSortWaves];
-  const int tid = threadIdx.x, parts = kSortThreads / E, e = tid % E, part = tid / E;
+  const int tid = threadIdx.x, parts = min(kSortThreads / E, kScanParts), e = tid % E, part = tid / E;
   const int per = (chunks + parts - 1) / parts, c0 = part * per, c1 = part < parts ? min(c0 + per, chunks) : 0;
   constexpr int kHold = 16;  // a column's piece stays in registers up to this length
   int v[kHold], sum = 0;
@@ -202,7 +207,7 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_scan(int32_t* __restric
   if (tid < E)
     for (int q = 0; q < parts; ++q) total += s_part[q * E + tid];
   int kept_all;
-  const int base = group_prefix(total, s_wave, &kept_all);
+  const int base = group_prefix<kSortWaves>(total, s_wave, &kept_all);
   if (tid < E) {
     offsets[tid] = base;
     s_base[tid] = base;
@@ -271,12 +276,14 @@ __global__ __launch_bounds__(256) void dispatch_move(MoveArgs a) {
       if constexpr (FIND) {
         const int e = a.idx[p];
         if ((unsigned)e < (unsigned)a.E) mine = a.first[(size_t)(p / a.chunk) * a.E + e] + a.ranks[p];
+        if ((unsigned)mine >= (unsigned)(a.T * a.k)) mine = -1;  // none, or the ids changed under the call
         if (blockIdx.y == 0 && threadIdx.x < 64) {
           a.inv[p] = mine;
           if (mine >= 0) a.perm[mine] = p;
         }
       } else {
         mine = a.inv[p];
+        if ((unsigned)mine >= (unsigned)(a.T * a.k)) mine = -1;
       }
     }
     if (!a.x) continue;
@@ -310,7 +317,7 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
     int n[4], total;
 #pragma unroll
     for (int i = 0; i < 4; ++i) n[i] = s_n[4 * threadIdx.x + i];
-    int at = group_prefix(n[0] + n[1] + n[2] + n[3], s_wave, &total);
+    int at = group_prefix<4>(n[0] + n[1] + n[2] + n[3], s_wave, &total);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = 4 * threadIdx.x + i;
@@ -343,6 +350,7 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
       pos = 0;
 #pragma unroll
       for (int i = 0; i < R; ++i) pos += __popcll(__ballot(key[i] < own));
+      pos = min(pos, P - 1);  // P only if the ids changed under the kernel
       if (x && at.on) q.store(xs + (int64_t)pos * H * EB, at);
     }
     if (lane == (j & 63)) mine = pos;
@@ -569,7 +577,7 @@ bool move_shape_ok(int32_t T, int32_t k, int32_t H) {
 }
 
 // A caller's row stride in elements (0: dense rows), or -1.
-int64_t row_stride(int64_t ld, int32_t H) { return ld == 0 ? H : (ld >= H && ld <= (1ll << 40) ? ld : -1); }
+int64_t row_stride(int64_t ld, int32_t H) { return ld == 0 ? H : (ld >= H && ld <= kMaxStride ? ld : -1); }
 
 Span rows_of(const void* p, int64_t rows, int32_t H, int fmt, int64_t ld) {
   return {p, rows, H * fmt_bytes(fmt), ld * fmt_bytes(fmt)};

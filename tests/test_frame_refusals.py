@@ -25,8 +25,8 @@ LONG = dict(T=1 << 15, k=4)   # a sort that needs a workspace
 
 @pytest.mark.parametrize("bad", [
     dict(idx=None), dict(perm=None), dict(inv=None), dict(off=None), dict(LONG, ws=None), dict(x=None), dict(xs=None),
-    dict(T=0), dict(T=-1), dict(T=(1 << 22) + 1), dict(k=0), dict(k=1025), dict(T=1 << 20, k=128), dict(E=0), dict(E=1025),
-    dict(fmt=2), dict(fmt=-1), dict(H=0), dict(H=65537), dict(ld=63), dict(ld=-64), dict(LONG, n=3), dict(x=A[1] + 1),
+    dict(T=0), dict(T=-1), dict(T=(1 << 21) + 1), dict(k=0), dict(k=1025), dict(T=1 << 20, k=128), dict(E=0), dict(E=1025),
+    dict(fmt=2), dict(fmt=-1), dict(H=0), dict(H=65537), dict(ld=63), dict(ld=-64), dict(ld=(1 << 36) + 1), dict(LONG, n=3), dict(x=A[1] + 1),
     dict(xs=A[2] + 1), dict(LONG, ws=A[6] + 2),
     dict(xs=A[1]), dict(xs=A[1] + 8 * 128 - 2), dict(perm=A[4]), dict(inv=A[5]), dict(inv=A[0]), dict(off=A[2]),
     dict(LONG, ws=A[3]), dict(perm=A[2] + 16 * 128 - 4)])
@@ -91,9 +91,9 @@ def norm_cfg(**kw):
     return R.moe_norm_config(*a.values())
 
 
-BAD_CONFIG = [dict(T=0), dict(T=(1 << 22) + 1), dict(H=0), dict(H=8193), dict(h=2), dict(y=-1), dict(x=9),
+BAD_CONFIG = [dict(T=0), dict(T=(1 << 21) + 1), dict(H=0), dict(H=8193), dict(h=2), dict(y=-1), dict(x=9),
               dict(gate_kind=3), dict(gate_kind=-1), dict(alpha=float("inf")), dict(alpha=float("nan")), dict(eps=0.0), dict(eps=1e-40),
-              dict(eps=-1e-6), dict(eps=float("nan")), dict(eps=2.0), dict(ld_h=63), dict(ld_y=-1), dict(ld_x=1)]
+              dict(eps=-1e-6), dict(eps=float("nan")), dict(eps=2.0), dict(ld_h=63), dict(ld_h=(1 << 36) + 1), dict(ld_y=-1), dict(ld_x=1)]
 
 
 def norm(cfg=None, **kw):
@@ -139,7 +139,7 @@ def test_norm_backward_refuses(bad):
 
 
 def test_workspace_sizes():
-    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 1025), (1 << 22, 1024, 8)):
+    for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (1, 1, 1025), (1 << 21, 1024, 8)):
         assert L.moe_dispatch_workspace(*bad) == -1
         with pytest.raises(R.MoeError):
             R.moe_dispatch_workspace(*bad)
@@ -148,7 +148,7 @@ def test_workspace_sizes():
     for bad in ((0, 1), (1, 0), (1, 8193)):
         with pytest.raises(R.MoeError):
             R.moe_block_norm_workspace(*bad)
-    assert R.moe_block_norm_workspace(4096, 2048) == R.moe_block_norm_workspace(1 << 22, 2048)   # bounded
+    assert R.moe_block_norm_workspace(4096, 2048) == R.moe_block_norm_workspace(1 << 21, 2048)   # bounded
 
 
 # --- the binding's own checks ------------------------------------------------

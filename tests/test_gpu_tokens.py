@@ -82,7 +82,8 @@ def check_dispatch(idx, E, x, got):
 SORTS = [(1, 1, 1, 0.0), (1, 2, 8, 0.0), (1, 8, 256, 0.0), (3, 5, 7, 0.3), (4, 8, 256, 0.0), (64, 8, 256, 0.1),
          (127, 1, 2, 0.0), (130, 6, 1000, 0.02), (97, 16, 1024, 0.0), (300, 7, 33, 0.5), (1024, 8, 256, 0.0),
          (2049, 3, 255, 0.01), (4096, 8, 256, 0.02), (9001, 16, 512, 0.0), (5000, 30, 64, 0.1), (700, 100, 1000, 0.1),
-         (11, 1024, 1024, 0.2)]
+         (11, 1024, 1024, 0.2), (1024, 1, 16, 0.0), (341, 3, 8, 0.1), (2048, 4, 100, 0.0), (8193, 1, 5, 0.0), (70001, 8, 3, 0.1),
+         (300007, 2, 1024, 0.02), (20000, 4, 1, 0.3)]
 
 
 @pytest.mark.parametrize("T,k,E,drop", SORTS)
