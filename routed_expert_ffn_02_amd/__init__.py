@@ -509,15 +509,19 @@ class _Args:
         try:
             fmt = _FMT[t.dtype]
             n, h = t.shape
-            ld, step = t.stride()
         except (AttributeError, KeyError, ValueError):
             self.refuse(f"{name} must be a two-dimensional fp32 or bf16 tensor")
-        if n < 1 or h < 1 or n > _I32_MAX or h > _I32_MAX or (n_rows is not None and n != n_rows) or (width is not None and h != width):
+        if n < 1 or h < 1 or n > _I32_MAX or h > _I32_MAX or (n_rows is not None and n != n_rows) or (
+                width is not None and h != width):
             self.refuse(f"{name} has shape {(n, h)}, not {(n_rows or 'T', width or 'H')}")
-        if n == 1:
+        if t.is_contiguous():
             ld = h
-        if (step != 1 and h > 1) or ld < h or (dense and ld != h):
-            self.refuse(f"{name} needs contiguous rows" + (" without gaps" if dense else ""))
+        else:
+            ld, step = t.stride()
+            if n == 1:
+                ld = h
+            if (step != 1 and h > 1) or ld < h or dense:
+                self.refuse(f"{name} needs contiguous rows" + (" without gaps" if dense else ""))
         if like is not None and (fmt, ld) != like:
             self.refuse(f"{name} must have the type and row stride of the tensor it belongs to")
         if t.get_device() != self.dev:

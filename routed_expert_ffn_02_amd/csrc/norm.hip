@@ -3,8 +3,9 @@
 //   h' = h + alpha * g * u        (g: none, one per token, or one per channel)
 //   x  = w_pre * h' / rms(h')     rms(v) = sqrt(mean(v^2) + eps)
 // and its gradient.  Memory-bound: a row is read once, kept in registers across its
-// reductions, and written once.  Statistics and all arithmetic are fp32; x is formed from
-// h' before h' is rounded to its own type, so each output is rounded once.
+// reductions, and written once (117 MB at 4096 rows of 2048, h and y fp32, x bf16: 18.2 us, 6.5
+// TB/s; one row: 2.4 us, a launch and one round trip).  Statistics and all arithmetic are fp32;
+// x is formed from h' before h' is rounded to its own type, so each output is rounded once.
 #include <algorithm>
 
 #include "rows.hpp"
@@ -263,7 +264,8 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_backward_kernel(NormArg
 
 // The sum over the workgroups' partial rows, 32 channels per workgroup of this kernel: 32
 // groups of 32 lanes take rows g, g + 32, ... and are added in order.  Each kind goes to up to
-// two outputs, each with a factor per channel or none.
+// two outputs, each with a factor per channel or none.  4.0 us for 8.4 MB of partial rows (256
+// of 4096, two kinds): a launch and one read.
 struct NormOut {
   float* p[2][2];
   const float* by[2][2];

@@ -29,9 +29,14 @@ constexpr int64_t kMoveMaxPairs = 1 << 26;
 //                     per chunk, dispatch_scan turns the histograms into first places, and the
 //                     move adds the two; the chunks grow with P so that there are at most
 //                     kSortChunks of them
+// What bounds all three is latency: launches and dependent reads.  E = 256, k = 8, H = 256, kernel
+// times and, in brackets, calls in a row: 1024 pairs 7.2 us (8.4) in the first form, 4.5 + 3.0 (11.3)
+// in the second; 8192 pairs 5.6 + 3.7 (10.6) in the second, 3.8 + 3.1 + 4.5 (14.0) in the third; 16384
+// pairs 6.6 + 4.9 (11.8) against 3.8 + 3.2 + 5.6 (13.4); at 32768 the second's counting takes 9.4 us
+// (an LDS atomic of 64 lanes about 32 cycles), the third's two launches 7.3.
 constexpr int kTinyPairs = 1024;
 constexpr int kTinyPieces = 4096;  // and at most this many KB of rows of x: each piece counts again
-constexpr int kSolePairs = 8192;
+constexpr int kSolePairs = 1 << 14;
 constexpr int kSortChunks = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -75,11 +80,13 @@ __device__ __forceinline__ int group_prefix(int v, int* s_wave, int* total) {
   return base + x - v;
 }
 
-// Lanes of the wavefront whose key equals this lane's (key < 2^bits; a lane with valid =
-// false gets 0).
-__device__ __forceinline__ uint64_t wave_peers(int key, bool valid, int bits) {
+// Lanes of the wavefront whose key (< kMaxExperts) equals this lane's; a lane with valid = false
+// gets 0.
+__device__ __forceinline__ uint64_t wave_peers(int key, bool valid) {
+  static_assert(kMaxExperts <= 1 << 10, "ten bits");
   uint64_t m = __ballot(valid);
-  for (int b = 0; b < bits; ++b) {
+#pragma unroll
+  for (int b = 0; b < 10; ++b) {
     const uint64_t set = __ballot((key >> b) & 1);
     m &= ((key >> b) & 1) ? set : ~set;
   }
@@ -89,14 +96,14 @@ __device__ __forceinline__ uint64_t wave_peers(int key, bool valid, int bits) {
 // One round of a chunk: kSortThreads pairs in order, e the thread's expert.  Returns the pair's
 // rank among the round's pairs of its expert (lanes of its wavefront before it, then earlier
 // wavefronts), and leaves the wavefronts' counts in s_cnt (zeroed here).
-__device__ __forceinline__ int round_rank(int e, bool kept, int E, int bits, uint16_t (*s_cnt)[kMaxExperts]) {
+__device__ __forceinline__ int round_rank(int e, bool kept, int E, uint16_t (*s_cnt)[kMaxExperts]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (tid < E) {
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) s_cnt[w][tid] = 0;
   }
   __syncthreads();
-  const uint64_t peers = wave_peers(e, kept, bits);
+  const uint64_t peers = wave_peers(e, kept);
   int rank = __popcll(peers & ((1ull << lane) - 1));
   if (kept && rank == 0) s_cnt[wave][e] = (uint16_t)__popcll(peers);
   __syncthreads();
@@ -113,8 +120,10 @@ __device__ __forceinline__ int round_total(int e, const uint16_t (*s_cnt)[kMaxEx
   return n;
 }
 
-// The whole sort, one workgroup per chunk of kSortThreads pairs.
-__global__ __launch_bounds__(kSortThreads) void dispatch_place(const int32_t* __restrict__ idx, int P, int E, int bits,
+// The whole sort, one workgroup per chunk of kSortThreads pairs; LOADS: four-pair loads per
+// thread that cover all pairs.
+template <int LOADS>
+__global__ __launch_bounds__(kSortThreads) void dispatch_place(const int32_t* __restrict__ idx, int P, int E,
                                                                int32_t* __restrict__ perm, int32_t* __restrict__ inv,
                                                                int32_t* __restrict__ offsets) {
   __shared__ int s_before[kMaxExperts], s_rest[kMaxExperts];
@@ -126,10 +135,9 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_place(const int32_t* __
   __syncthreads();
   // four pairs to a load (chunks are multiples of four, so four neighbours lie on one side
   // of lo), all of them in flight
-  constexpr int kLoads = (kSolePairs + 4 * kSortThreads - 1) / (4 * kSortThreads);
-  u32x4 e[kLoads];
+  u32x4 e[LOADS];
 #pragma unroll
-  for (int u = 0; u < kLoads; ++u) {
+  for (int u = 0; u < LOADS; ++u) {
     const int p0 = 4 * (u * kSortThreads + tid);
     e[u] = ~(u32x4)0;
     if (p0 + 4 <= P) {
@@ -141,14 +149,14 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_place(const int32_t* __
     }
   }
 #pragma unroll
-  for (int u = 0; u < kLoads; ++u) {
+  for (int u = 0; u < LOADS; ++u) {
     int* side = 4 * (u * kSortThreads + tid) < lo ? s_before : s_rest;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (e[u][i] < (unsigned)E) atomicAdd(&side[e[u][i]], 1);
   }
   const bool kept = (unsigned)mine < (unsigned)E;
-  const int rank = round_rank(mine, kept, E, bits, s_cnt);  // its barriers end the counting
+  const int rank = round_rank(mine, kept, E, s_cnt);  // its barriers end the counting
   // an expert's first place in this chunk: kept pairs of lower experts, then its own pairs
   // in earlier chunks
   const int before = tid < E ? s_before[tid] : 0;
@@ -166,7 +174,7 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_place(const int32_t* __
   if (p < P) inv[p] = pos;
 }
 
-__global__ __launch_bounds__(kSortThreads) void dispatch_rank(const int32_t* __restrict__ idx, int P, int E, int bits,
+__global__ __launch_bounds__(kSortThreads) void dispatch_rank(const int32_t* __restrict__ idx, int P, int E,
                                                               int chunk, int32_t* __restrict__ hist,
                                                               int32_t* __restrict__ ranks) {
   __shared__ int s_run[kMaxExperts];
@@ -176,7 +184,7 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_rank(const int32_t* __r
   for (int r0 = lo; r0 < hi; r0 += kSortThreads) {
     const int p = r0 + tid, e = p < hi ? idx[p] : -1;
     const bool kept = (unsigned)e < (unsigned)E;
-    const int rank = round_rank(e, kept, E, bits, s_cnt);
+    const int rank = round_rank(e, kept, E, s_cnt);
     if (kept) ranks[p] = s_run[e] + rank;
     __syncthreads();
     if (tid < E) s_run[tid] += round_total(tid, s_cnt);
@@ -245,7 +253,8 @@ __device__ __forceinline__ int wave_token() {
 
 // ---------------------------------------------------------------------------
 // Rows of x to their sorted places.  A workgroup takes one token and 4 KB of its row, 16 bytes
-// a thread, reads them once and writes them k times.  FIND: the pairs' places come from their
+// a thread, reads them once and writes them k times.  Bound by memory: 151 MB at 4096 tokens, k = 8,
+// H = 2048 in bf16 take 27.8 us (5.4 TB/s; a fill of as many bytes writes 6.6).  FIND: the pairs' places come from their
 // ranks and the chunks' first places (lane j finds rank j's), and the tables are written
 // beside the rows (by the workgroup of blockIdx.y = 0); otherwise from inv.  NT: stores that
 // do not stay in the caches, see stream_rows.
@@ -296,7 +305,7 @@ __global__ __launch_bounds__(256) void dispatch_move(MoveArgs a) {
 
 // The sort and the move of at most kTinyPairs pairs in one launch.  A pair's key is
 // (expert, pair) in one word; its place is the number of smaller keys.  A wavefront takes one
-// token and 1 KB of its row; the last workgroup (of blockIdx.y = 0) writes the offsets.
+// token and 1 KB of its row, so that a few tokens' rows spread over the chip (3.1 us at 4 tokens, k = 8); the last workgroup (of blockIdx.y = 0) writes the offsets.
 template <int EB, int R>  // R: 64-pair registers of keys
 __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__ idx, int T, int k, int E,
                                                      const uint8_t* __restrict__ x, int64_t pitch, int H,
@@ -306,12 +315,17 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
   if (blockIdx.x == gridDim.x - 1) {
     __shared__ int s_n[kMaxExperts], s_wave[4];
     if (blockIdx.y != 0) return;
+    int ids[kTinyPairs / 256];
+#pragma unroll
+    for (int i = 0; i < kTinyPairs / 256; ++i) {
+      const int p = 256 * i + threadIdx.x, e = idx[min(p, P - 1)];  // no branch: the loads overlap
+      ids[i] = p < P ? e : -1;
+    }
     for (int e = threadIdx.x; e < kMaxExperts; e += 256) s_n[e] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < P; p += 256) {
-      const int e = idx[p];
-      if ((unsigned)e < (unsigned)E) atomicAdd(&s_n[e], 1);
-    }
+#pragma unroll
+    for (int i = 0; i < kTinyPairs / 256; ++i)
+      if ((unsigned)ids[i] < (unsigned)E) atomicAdd(&s_n[ids[i]], 1);
     __syncthreads();
     // four neighbouring experts per thread
     int n[4], total;
@@ -337,29 +351,42 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int p = 64 * i + lane;
-    const int e = p < P ? idx[p] : -1;
-    key[i] = (unsigned)e < (unsigned)E ? (uint32_t)e << 10 | p : 0xffffffffu;
+    key[i] = idx[min(p, P - 1)];
   }
-  int mine = -1, ids = 0;
-  for (int j = 0; j < k; ++j) {
-    if ((j & 63) == 0) ids = j + lane < k ? idx[t * k + j + lane] : -1;
-    const int p = t * k + j, e = __builtin_amdgcn_readlane(ids, j & 63);
-    int pos = -1;
-    if ((unsigned)e < (unsigned)E) {
-      const uint32_t own = (uint32_t)e << 10 | p;
-      pos = 0;
 #pragma unroll
-      for (int i = 0; i < R; ++i) pos += __popcll(__ballot(key[i] < own));
-      pos = min(pos, P - 1);  // P only if the ids changed under the kernel
-      if (x && at.on) q.store(xs + (int64_t)pos * H * EB, at);
-    }
-    if (lane == (j & 63)) mine = pos;
-    if (blockIdx.y == 0 && ((j & 63) == 63 || j == k - 1)) {
-      const int q = t * k + (j & ~63) + lane;
-      if ((j & ~63) + lane <= j) {
-        inv[q] = mine;
-        if (mine >= 0) perm[mine] = q;
+  for (int i = 0; i < R; ++i) {
+    const int p = 64 * i + lane;
+    key[i] = p < P && key[i] < (unsigned)E ? key[i] << 10 | p : 0xffffffffu;
+  }
+  constexpr int kAtOnce = 8;  // ranks counted together: the counts of one hide the others' waits
+  for (int j0 = 0; j0 < k; j0 += 64) {
+    const int n = min(64, k - j0), p0 = t * k + j0;
+    const int id = lane < n ? idx[p0 + lane] : -1;
+    const uint32_t mine = (unsigned)id < (unsigned)E ? (uint32_t)id << 10 | (p0 + lane) : 0xffffffffu;
+    int place = -1;  // of rank j0 + lane
+    for (int j1 = 0; j1 < n; j1 += kAtOnce) {
+      uint32_t own[kAtOnce];
+      int pos[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        own[j] = __builtin_amdgcn_readlane(mine, j1 + j);  // lanes behind the ranks hold no key
+        pos[j] = 0;
       }
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) pos[j] += __popcll(__ballot(key[i] < own[j]));
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (own[j] == 0xffffffffu) continue;
+        pos[j] = min(pos[j], P - 1);  // P only if the ids changed under the kernel
+        if (lane == j1 + j) place = pos[j];
+        if (x && at.on) q.store(xs + (int64_t)pos[j] * H * EB, at);
+      }
+    }
+    if (blockIdx.y == 0 && lane < n) {
+      inv[p0 + lane] = place;
+      if (place >= 0) perm[place] = p0 + lane;
     }
   }
 }
@@ -367,7 +394,11 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
 // ---------------------------------------------------------------------------
 // y[t] = sum_j w[t,j] rows[inv[t,j]] in rank order (w = nullptr: a plain sum, the gradient
 // of the move).  A workgroup takes one token and 2048 elements of its row, so that the
-// scattered rows are read in pieces of 4 KB and more; kRanks rows are in flight per lane.
+// scattered rows are read in pieces of 4 KB and more (a wavefront per token and 512 elements:
+// 46 us where this takes 28.9, 168 MB at 4096 tokens, k = 8, H = 2048, bf16 to fp32: 5.8 TB/s);
+// kRanks rows are in flight per lane, more ranks go round again.  Outputs go out by
+// non-temporal stores: 33.8 us against 38.2 there with ordinary loads, and a kernel that reads y
+// next takes no longer (1024 tokens: 12.5 us for both against 15.3).
 constexpr int kRanks = 8;
 
 template <int RF, int YF, bool WEIGHTED, bool NT>
@@ -411,7 +442,9 @@ __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ 
 // ---------------------------------------------------------------------------
 // The weighted return's gradient: dys[inv[t,j]] = w[t,j] dy[t], dw[t,j] = <dy[t], ys[inv[t,j]]>.
 // A workgroup takes one token and up to kRanks of its ranks, its wavefronts neighbouring
-// pieces of the row; the dot products meet in LDS in wavefront order.
+// pieces of the row; the dot products meet in LDS in wavefront order.  Bound by memory: 297 MB at
+// 4096 tokens, k = 8, H = 2048 (dy fp32, rows bf16) take 56.6 us (5.2 TB/s); with one wavefront
+// 70.0, with two 74.4.
 constexpr int kCbWaves = 4;
 
 template <int DF, int RF, bool NT>
@@ -486,7 +519,9 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
 // load.  The gates' gradients are first gathered by expert: lane j adds up, in rank order,
 // every rank that chose its expert, and the first of them puts the sum and the number of
 // ranks into the wavefront's table in LDS.  A token's logits are all read before any of its
-// gradients is written (dlogits may be logits).
+// gradients is written (dlogits may be logits).  Bound by one round trip to memory and three
+// wavefront sums: 4.7 us at 4096 tokens of 256 logits, 5.6 at 997 of 1000 with k = 16 (10.5 when every
+// lane compared its logits with every rank).
 template <int C>  // loads of 256 logits
 __global__ __launch_bounds__(256) void topk_backward_kernel(const float* logits, int T, int E, int k,
                                                             const int32_t* __restrict__ idx,
@@ -651,8 +686,6 @@ extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, i
     if (P <= 256) return eb == 2 ? go(dispatch_tiny<2, 4>) : go(dispatch_tiny<4, 4>);
     return eb == 2 ? go(dispatch_tiny<2, kTinyPairs / 64>) : go(dispatch_tiny<4, kTinyPairs / 64>);
   }
-  int bits = 0;
-  while ((1 << bits) < n_experts) ++bits;
   const dim3 threads(kSortThreads);
   MoveArgs m{src, pitch, T, k, n_experts, H, dst, inv};
   const auto move = [&](auto find) {
@@ -664,13 +697,14 @@ extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, i
   };
   if (P <= kSolePairs) {
     const dim3 chunks((unsigned)((P + kSortThreads - 1) / kSortThreads));
-    const moe_status st = launch(dispatch_place, chunks, threads, s, topk_idx, (int)P, n_experts, bits, perm, inv, offsets);
+    static_assert(kSolePairs <= 4 * 4 * kSortThreads, "LOADS");
+    const moe_status st = launch(P <= 2 * 4 * kSortThreads ? dispatch_place<2> : dispatch_place<4>, chunks, threads, s, topk_idx, (int)P, n_experts, perm, inv, offsets);
     return st != MOE_OK || !x ? st : move(std::false_type{});
   }
   const SortPlan sp = sort_plan(P);
   int32_t* hist = static_cast<int32_t*>(ws);
   int32_t* ranks = hist + (int64_t)sp.blocks * n_experts;
-  moe_status st = launch(dispatch_rank, dim3(sp.blocks), threads, s, topk_idx, (int)P, n_experts, bits, sp.chunk, hist, ranks);
+  moe_status st = launch(dispatch_rank, dim3(sp.blocks), threads, s, topk_idx, (int)P, n_experts, sp.chunk, hist, ranks);
   if (st == MOE_OK) st = launch(dispatch_scan, dim3(1), threads, s, hist, n_experts, sp.blocks, offsets);
   if (st != MOE_OK) return st;
   m.idx = topk_idx;
