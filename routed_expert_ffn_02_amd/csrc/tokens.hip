@@ -401,6 +401,27 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
 // next takes no longer (1024 tokens: 12.5 us for both against 15.3).
 constexpr int kRanks = 8;
 
+// A token's ranks j0 .. j0 + kRanks - 1: places (-1: left out) and gates, in scalar registers.  The
+// lanes read them at once and every lane is asked for its own: one load each, where reading
+// them rank by rank is a chain of scalar loads and branches.
+template <bool WEIGHTED>
+struct TokenRanks {
+  int pos[kRanks];
+  float w[kRanks];
+  __device__ __forceinline__ TokenRanks(const int32_t* inv, const float* gates, int j0, int k, int T) {
+    const int lane = threadIdx.x & 63, j = min(j0 + (lane & (kRanks - 1)), k - 1);
+    int p = inv[j];
+    const float g = WEIGHTED ? gates[j] : 1.f;
+    if (j0 + (lane & (kRanks - 1)) >= k || (unsigned)p >= (unsigned)(T * k)) p = -1;
+#pragma unroll
+    for (int i = 0; i < kRanks; ++i) {
+      pos[i] = __builtin_amdgcn_readlane(p, i);
+      w[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), i));
+    }
+  }
+  __device__ __forceinline__ bool kept(int j) const { return pos[j] >= 0; }
+};
+
 template <int RF, int YF, bool WEIGHTED, bool NT>
 __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ rows, const int32_t* __restrict__ inv,
                                                     const float* __restrict__ w, int T, int k, int H,
@@ -408,32 +429,24 @@ __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ 
   constexpr int N = 8, RB = kElemBytes<RF>;
   const int t = blockIdx.x;
   const Piece<N> at(blockIdx.y * 256 + threadIdx.x, H);
-  if (!at.on) return;
-  const int64_t P = (int64_t)T * k, p0 = (int64_t)t * k;
+  const int64_t p0 = (int64_t)t * k;
   float acc[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) acc[n] = 0.f;
   for (int j0 = 0; j0 < k; j0 += kRanks) {
+    const TokenRanks<WEIGHTED> ranks(inv + p0, w + p0, j0, k, T);
     Chunk<RF, N> q[kRanks];
-    float g[kRanks];
-    bool kept[kRanks];
-#pragma unroll
-    for (int j = 0; j < kRanks; ++j) {
-      const int pos = j0 + j < k ? inv[p0 + j0 + j] : -1;
-      kept[j] = (unsigned)pos < (uint64_t)P;
-      g[j] = 1.f;
-      if (kept[j]) {
-        if (WEIGHTED) g[j] = w[p0 + j0 + j];
-        q[j].template load<NT>(rows + (int64_t)pos * H * RB, at);
-      }
-    }
 #pragma unroll
     for (int j = 0; j < kRanks; ++j)
-      if (kept[j]) {
+      if (at.on && ranks.kept(j)) q[j].template load<NT>(rows + (int64_t)ranks.pos[j] * H * RB, at);
 #pragma unroll
-        for (int n = 0; n < N; ++n) acc[n] = WEIGHTED ? fmaf(g[j], q[j].get(n), acc[n]) : acc[n] + q[j].get(n);
+    for (int j = 0; j < kRanks; ++j)
+      if (ranks.kept(j)) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) acc[n] = WEIGHTED ? fmaf(ranks.w[j], q[j].get(n), acc[n]) : acc[n] + q[j].get(n);
       }
   }
+  if (!at.on) return;
   Chunk<YF, N> o;
   o.set(acc);
   o.template store_wave<true>(y + (int64_t)t * pitch, at, H);
@@ -456,16 +469,12 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
   constexpr int N = 8, RB = kElemBytes<RF>;
   __shared__ float s_dot[kCbWaves][kRanks];
   const int t = blockIdx.x, j0 = blockIdx.y * kRanks, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t P = (int64_t)T * k, p0 = (int64_t)t * k + j0;
-  int pos[kRanks];
-  float g[kRanks], dot[kRanks];
+  const int64_t p0 = (int64_t)t * k;
+  // the gates only for dys; read as inv otherwise, and not used
+  const TokenRanks<true> ranks(inv + p0, dys ? w + p0 : reinterpret_cast<const float*>(inv + p0), j0, k, T);
+  float dot[kRanks];
 #pragma unroll
-  for (int j = 0; j < kRanks; ++j) {
-    pos[j] = j0 + j < k ? inv[p0 + j] : -1;
-    if ((unsigned)pos[j] >= (uint64_t)P) pos[j] = -1;
-    g[j] = pos[j] >= 0 && dys ? w[p0 + j] : 0.f;
-    dot[j] = 0.f;
-  }
+  for (int j = 0; j < kRanks; ++j) dot[j] = 0.f;
   for (int c = threadIdx.x; c * N < H; c += 64 * kCbWaves) {
     const Piece<N> at(c, H);
     Chunk<DF, N> d;
@@ -474,7 +483,7 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
     if (dw) {
 #pragma unroll
       for (int j = 0; j < kRanks; ++j)
-        if (pos[j] >= 0) q[j].template load<NT>(ys + (int64_t)pos[j] * H * RB, at);
+        if (ranks.kept(j)) q[j].template load<NT>(ys + (int64_t)ranks.pos[j] * H * RB, at);
       if (at.skip) {
         d.drop(at.skip);
 #pragma unroll
@@ -482,7 +491,7 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
       }
 #pragma unroll
       for (int j = 0; j < kRanks; ++j)
-        if (pos[j] >= 0) {
+        if (ranks.kept(j)) {
 #pragma unroll
           for (int n = 0; n < N; ++n) dot[j] = fmaf(d.get(n), q[j].get(n), dot[j]);
         }
@@ -490,12 +499,12 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
     if (dys) {
 #pragma unroll
       for (int j = 0; j < kRanks; ++j)
-        if (pos[j] >= 0) {
+        if (ranks.kept(j)) {
           float v[N];
 #pragma unroll
-          for (int n = 0; n < N; ++n) v[n] = g[j] * d.get(n);
+          for (int n = 0; n < N; ++n) v[n] = ranks.w[j] * d.get(n);
           q[j].set(v);
-          q[j].template store_wave<true>(dys + (int64_t)pos[j] * H * RB, at, H);
+          q[j].template store_wave<true>(dys + (int64_t)ranks.pos[j] * H * RB, at, H);
         }
     }
   }
@@ -510,7 +519,7 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
     float v = 0.f;
 #pragma unroll
     for (int x = 0; x < kCbWaves; ++x) v += s_dot[x][threadIdx.x];
-    dw[p0 + threadIdx.x] = v;
+    dw[p0 + j0 + threadIdx.x] = v;
   }
 }
 
