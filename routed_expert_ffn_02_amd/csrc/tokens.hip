@@ -30,10 +30,12 @@ constexpr int64_t kMoveMaxPairs = 1 << 26;
 //                     move adds the two; the chunks grow with P so that there are at most
 //                     kSortChunks of them
 // What bounds all three is latency: launches and dependent reads.  E = 256, k = 8, H = 256, kernel
-// times and, in brackets, calls in a row: 1024 pairs 7.2 us (8.4) in the first form, 4.5 + 3.0 (11.3)
-// in the second; 8192 pairs 5.6 + 3.7 (10.6) in the second, 3.8 + 3.1 + 4.5 (14.0) in the third; 16384
-// pairs 6.6 + 4.9 (11.8) against 3.8 + 3.2 + 5.6 (13.4); at 32768 the second's counting takes 9.4 us
-// (an LDS atomic of 64 lanes about 32 cycles), the third's two launches 7.3.
+// times and, in brackets, calls in a row:
+//    1024 pairs   5.2 us (8.4) in the first form, 4.5 + 3.0 (11.3) in the second
+//    8192 pairs   5.2 + 3.7 (10.6) in the second, 3.8 + 3.1 + 4.5 (14.0) in the third
+//   16384 pairs   6.2 + 4.9 (11.5) against 3.8 + 3.2 + 5.6 (13.4)
+//   32768 pairs   the second's counting alone takes 9.4 us (an LDS atomic of 64 lanes about 32
+//                 cycles), the third's two launches 7.4
 constexpr int kTinyPairs = 1024;
 constexpr int kTinyPieces = 4096;  // and at most this many KB of rows of x: each piece counts again
 constexpr int kSolePairs = 1 << 14;
@@ -253,11 +255,11 @@ __device__ __forceinline__ int wave_token() {
 
 // ---------------------------------------------------------------------------
 // Rows of x to their sorted places.  A workgroup takes one token and 4 KB of its row, 16 bytes
-// a thread, reads them once and writes them k times.  Bound by memory: 151 MB at 4096 tokens, k = 8,
-// H = 2048 in bf16 take 27.8 us (5.4 TB/s; a fill of as many bytes writes 6.6).  FIND: the pairs' places come from their
-// ranks and the chunks' first places (lane j finds rank j's), and the tables are written
-// beside the rows (by the workgroup of blockIdx.y = 0); otherwise from inv.  NT: stores that
-// do not stay in the caches, see stream_rows.
+// a thread, reads them once and writes them k times.  Bound by memory: 151 MB at 4096 tokens,
+// k = 8, H = 2048 in bf16 take 27.6 us (5.5 TB/s; a fill of as many bytes writes 6.6).
+// FIND: the pairs' places come from their ranks and the chunks' first places (lane j finds rank
+// j's), and the tables are written beside the rows (by the workgroup of blockIdx.y = 0);
+// otherwise from inv.  NT: stores that do not stay in the caches, see stream_rows.
 struct MoveArgs {
   const uint8_t* x;         // nullptr: the tables alone
   int64_t pitch;
@@ -305,7 +307,8 @@ __global__ __launch_bounds__(256) void dispatch_move(MoveArgs a) {
 
 // The sort and the move of at most kTinyPairs pairs in one launch.  A pair's key is
 // (expert, pair) in one word; its place is the number of smaller keys.  A wavefront takes one
-// token and 1 KB of its row, so that a few tokens' rows spread over the chip (3.1 us at 4 tokens, k = 8); the last workgroup (of blockIdx.y = 0) writes the offsets.
+// token and 1 KB of its row, so that a few tokens' rows spread over the chip (3.1 us at 4 tokens,
+// k = 8, H = 2048); the last workgroup (of blockIdx.y = 0) writes the offsets.
 template <int EB, int R>  // R: 64-pair registers of keys
 __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__ idx, int T, int k, int E,
                                                      const uint8_t* __restrict__ x, int64_t pitch, int H,
@@ -395,7 +398,7 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
 // y[t] = sum_j w[t,j] rows[inv[t,j]] in rank order (w = nullptr: a plain sum, the gradient
 // of the move).  A workgroup takes one token and 2048 elements of its row, so that the
 // scattered rows are read in pieces of 4 KB and more (a wavefront per token and 512 elements:
-// 46 us where this takes 28.9, 168 MB at 4096 tokens, k = 8, H = 2048, bf16 to fp32: 5.8 TB/s);
+// 46 us where this takes 28.6, 168 MB at 4096 tokens, k = 8, H = 2048, bf16 to fp32: 5.9 TB/s);
 // kRanks rows are in flight per lane, more ranks go round again.  Outputs go out by
 // non-temporal stores: 33.8 us against 38.2 there with ordinary loads, and a kernel that reads y
 // next takes no longer (1024 tokens: 12.5 us for both against 15.3).
@@ -434,7 +437,7 @@ __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ 
 #pragma unroll
   for (int n = 0; n < N; ++n) acc[n] = 0.f;
   for (int j0 = 0; j0 < k; j0 += kRanks) {
-    const TokenRanks<WEIGHTED> ranks(inv + p0, w + p0, j0, k, T);
+    const TokenRanks<WEIGHTED> ranks(inv + p0, WEIGHTED ? w + p0 : nullptr, j0, k, T);
     Chunk<RF, N> q[kRanks];
 #pragma unroll
     for (int j = 0; j < kRanks; ++j)
@@ -456,7 +459,7 @@ __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ 
 // The weighted return's gradient: dys[inv[t,j]] = w[t,j] dy[t], dw[t,j] = <dy[t], ys[inv[t,j]]>.
 // A workgroup takes one token and up to kRanks of its ranks, its wavefronts neighbouring
 // pieces of the row; the dot products meet in LDS in wavefront order.  Bound by memory: 297 MB at
-// 4096 tokens, k = 8, H = 2048 (dy fp32, rows bf16) take 56.6 us (5.2 TB/s); with one wavefront
+// 4096 tokens, k = 8, H = 2048 (dy fp32, rows bf16) take 56.0 us (5.3 TB/s); with one wavefront
 // 70.0, with two 74.4.
 constexpr int kCbWaves = 4;
 
@@ -707,7 +710,8 @@ extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, i
   if (P <= kSolePairs) {
     const dim3 chunks((unsigned)((P + kSortThreads - 1) / kSortThreads));
     static_assert(kSolePairs <= 4 * 4 * kSortThreads, "LOADS");
-    const moe_status st = launch(P <= 2 * 4 * kSortThreads ? dispatch_place<2> : dispatch_place<4>, chunks, threads, s, topk_idx, (int)P, n_experts, perm, inv, offsets);
+    const moe_status st = launch(P <= 2 * 4 * kSortThreads ? dispatch_place<2> : dispatch_place<4>, chunks, threads, s,
+                                 topk_idx, (int)P, n_experts, perm, inv, offsets);
     return st != MOE_OK || !x ? st : move(std::false_type{});
   }
   const SortPlan sp = sort_plan(P);

@@ -284,6 +284,9 @@ def test_topk_backward(T, k, E, renorm):
         z[4] = -np.inf                            # every logit masked
         z[0, idx[0, 0]] = -np.inf
         z[2, ::2] = -np.inf
+    if T > 6:
+        z[5, 1::2] = np.finfo(np.float32).min     # masks of the lowest finite value: no share either
+        z[6] = np.finfo(np.float32).min           # all alike: every logit the same share
     dw = rng.standard_normal((T, k)).astype(np.float32)
     dw[(idx < 0) | (idx >= E)] = np.nan           # not read into anything
     got = torch.full((T, E), 9.0, device="cuda")
