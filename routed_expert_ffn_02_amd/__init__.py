@@ -3,13 +3,14 @@
 Argument marshalling only: every function here has the name of a C entry point
 declared in include/routed_moe.h and forwards to it.  Device tensors are passed
 as raw pointers (torch supplies device memory and the HIP stream); every step of
-the hot path runs in the library's kernels.  There is no fallback: importing
-this package fails when the compiled library is missing.
+the hot path runs in the library's kernels.  Calls on a context go through ctypes;
+those around the experts, which check every tensor they are given, through a small
+extension module (_marshal).  There is no fallback: importing this package fails
+when the compiled library or the module is missing.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch  # noqa: F401  (loads the HIP runtime the library links against)
@@ -169,6 +170,8 @@ def _load():
 
 
 lib = _load()
+
+from . import _marshal  # noqa: E402  (built with the library, linked against it)
 
 
 # ---------------------------------------------------------------------------
@@ -473,114 +476,10 @@ def moe_permute_noalloc(slot_idx, P: int, n_slot_range: int, perm, offsets, grou
 
 # ---------------------------------------------------------------------------
 # Around the experts.  These take torch tensors only and read shapes, formats and row strides
-# from them; a tensor the library would misread (type, shape, stride, device) is refused here.
-_FMT = {torch.float32: MOE_AFMT_F32, torch.bfloat16: MOE_AFMT_BF16}
-_I32_MAX = 0x7fffffff
-
-
-# the current stream's handle and the current device without the objects around them
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-
-
-class _Args:
-    """Checks the tensors of one call and holds the device they share.  A decode step makes these
-    calls once a layer, so a check reads each property of a tensor once."""
-    __slots__ = ("where", "dev")
-
-    def __init__(self, where: str):
-        self.where = where
-        self.dev = None
-
-    def refuse(self, msg: str):
-        raise MoeError(MOE_EINVAL, self.where, msg)
-
-    def place(self, name, t):
-        d = t.get_device()
-        if d != self.dev:
-            if d < 0:
-                self.refuse(f"{name} must be on the GPU")
-            if self.dev is not None:
-                self.refuse(f"{name} is on cuda:{d}, other tensors on cuda:{self.dev}")
-            self.dev = d
-
-    def rows(self, name, t, n_rows=None, width=None, dense=False, like=None):
-        """(pointer, format, row stride, rows, H) of a [rows, H] matrix with contiguous rows."""
-        try:
-            fmt = _FMT[t.dtype]
-            n, h = t.shape
-        except (AttributeError, KeyError, ValueError):
-            self.refuse(f"{name} must be a two-dimensional fp32 or bf16 tensor")
-        if n < 1 or h < 1 or n > _I32_MAX or h > _I32_MAX or (n_rows is not None and n != n_rows) or (
-                width is not None and h != width):
-            self.refuse(f"{name} has shape {(n, h)}, not {(n_rows or 'T', width or 'H')}")
-        if t.is_contiguous():
-            ld = h
-        else:
-            ld, step = t.stride()
-            if n == 1:
-                ld = h
-            if (step != 1 and h > 1) or ld < h or dense:
-                self.refuse(f"{name} needs contiguous rows" + (" without gaps" if dense else ""))
-        if like is not None and (fmt, ld) != like:
-            self.refuse(f"{name} must have the type and row stride of the tensor it belongs to")
-        if t.get_device() != self.dev:
-            self.place(name, t)
-        return t.data_ptr(), fmt, ld, n, h
-
-    def flat(self, name, t, dtype, *shape):
-        """Pointer of a dense tensor of this type and shape (one number: that many elements)."""
-        try:
-            ok = t.dtype is dtype and t.is_contiguous()
-        except AttributeError:
-            ok = False
-        if not ok:
-            self.refuse(f"{name} must be a contiguous {dtype} tensor")
-        if t.shape != shape and not (len(shape) == 1 and t.numel() == shape[0]):
-            self.refuse(f"{name} has shape {tuple(t.shape)}, not {shape}")
-        if t.get_device() != self.dev:
-            self.place(name, t)
-        return t.data_ptr()
-
-    def pairs(self, name, t):
-        """(T, k, pointer) of an int32 [T, k] table."""
-        try:
-            T, k = t.shape
-        except (AttributeError, ValueError):
-            T = k = 0
-        if not T or not k or T > _I32_MAX or k > _I32_MAX:
-            self.refuse(f"{name} must be an int32 tensor [T, k]")
-        return T, k, self.flat(name, t, torch.int32, T, k)
-
-    def workspace(self, t):
-        """(pointer, bytes) of the caller's workspace."""
-        if t is None:
-            return None, 0
-        if not isinstance(t, torch.Tensor) or not t.is_contiguous():
-            self.refuse("ws must be a contiguous tensor")
-        n = t.numel() * t.element_size()
-        if not n:
-            return None, 0
-        self.place("ws", t)
-        return t.data_ptr(), n
-
-    def call(self, fn, stream, *args):
-        """Forward to the C entry point on `stream` (default: the current stream of the tensors' device)."""
-        dev = self.dev
-        if stream is None:
-            s = _raw_stream(dev)
-        else:
-            if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
-                self.refuse(f"stream is on {stream.device}, tensors on cuda:{dev}")
-            s = _stream(stream)
-        if _current_device() == dev:
-            st = fn(*args, s)
-        else:
-            with torch.cuda.device(dev):
-                st = fn(*args, s)
-        if st:
-            raise MoeError(st, self.where, "launch failure" if st == MOE_EHIP else
-                           "shape out of range, overlapping tensors, missing argument or short workspace")
+# from them; a tensor the library would misread (type, shape, stride, device) is refused with
+# MOE_EINVAL before anything is enqueued.  Checks and calls are in csrc/marshal.cpp.  `stream` is a
+# torch stream or a handle, by default the current stream of the tensors' device.
+_marshal.set_error(MoeError)
 
 
 def moe_dispatch_workspace(T: int, k: int, n_experts: int) -> int:
@@ -593,105 +492,34 @@ def moe_dispatch_workspace(T: int, k: int, n_experts: int) -> int:
 
 def moe_dispatch(topk_idx, n_experts: int, x, xs, perm, inv, offsets, ws=None, stream=None) -> None:
     """Sort the pairs of topk_idx [T,k] by expert into perm [T*k], inv [T,k] and offsets [n_experts+1], and
-    move the rows of x [T,H] to xs [T*k,H] (both None: sort only).  ws: uint8 workspace."""
-    a = _Args("moe_dispatch")
-    T, k, idx = a.pairs("topk_idx", topk_idx)
-    P = T * k
-    xp = xsp = None
-    fmt = H = ld = 0
-    if x is not None or xs is not None:
-        xp, fmt, ld, _, H = a.rows("x", x, T)
-        xsp, xs_fmt, _, _, _ = a.rows("xs", xs, P, H, True)
-        if xs_fmt != fmt:
-            a.refuse("xs must have x's type")
-    p = a.flat("perm", perm, torch.int32, P)
-    i = a.flat("inv", inv, torch.int32, T, k)
-    o = a.flat("offsets", offsets, torch.int32, n_experts + 1)
-    w, wn = a.workspace(ws)
-    a.call(lib.moe_dispatch, stream, idx, T, k, n_experts, xp, fmt, H, ld, xsp, p, i, o, w, wn)
+    move the rows of x [T,H] to xs [T*k,H] (both None: sort only).  ws: workspace tensor."""
+    _marshal.dispatch(topk_idx, n_experts, x, xs, perm, inv, offsets, ws, stream)
 
 
 def moe_dispatch_backward(dxs, inv, dx, stream=None) -> None:
     """dx [T,H] = the sum of each token's rows of dxs [T*k,H]."""
-    a = _Args("moe_dispatch_backward")
-    T, k, i = a.pairs("inv", inv)
-    g, fmt, _, _, H = a.rows("dxs", dxs, T * k, None, True)
-    o, o_fmt, ld, _, _ = a.rows("dx", dx, T, H)
-    a.call(lib.moe_dispatch_backward, stream, g, fmt, i, T, k, H, o, o_fmt, ld)
+    _marshal.dispatch_backward(dxs, inv, dx, stream)
 
 
 def moe_combine(ys, inv, w, y, stream=None) -> None:
     """y [T,H] = the sum of each token's rows of ys [T*k,H] weighted by w [T,k] (fp32)."""
-    a = _Args("moe_combine")
-    T, k, i = a.pairs("inv", inv)
-    r, fmt, _, _, H = a.rows("ys", ys, T * k, None, True)
-    wp = a.flat("w", w, torch.float32, T, k)
-    o, o_fmt, ld, _, _ = a.rows("y", y, T, H)
-    a.call(lib.moe_combine, stream, r, fmt, i, wp, T, k, H, o, o_fmt, ld)
+    _marshal.combine(ys, inv, w, y, stream)
 
 
 def moe_combine_backward(dy, ys, inv, w, dys, dw, stream=None) -> None:
-    """From dy [T,H]: dys [T*k,H] (or None; may be ys) and dw [T,k] (or None, then ys may be None)."""
-    a = _Args("moe_combine_backward")
-    T, k, i = a.pairs("inv", inv)
-    d, d_fmt, ld, _, H = a.rows("dy", dy, T)
-    r = o = wp = g = None
-    fmt = d_fmt
-    if dys is not None:
-        o, fmt, _, _, _ = a.rows("dys", dys, T * k, H, True)
-        wp = a.flat("w", w, torch.float32, T, k)
-    if dw is not None:
-        r, r_fmt, _, _, _ = a.rows("ys", ys, T * k, H, True)
-        if dys is not None and r_fmt != fmt:
-            a.refuse("dys must have ys's type")
-        fmt = r_fmt
-        g = a.flat("dw", dw, torch.float32, T, k)
-    a.call(lib.moe_combine_backward, stream, d, d_fmt, ld, r, fmt, i, wp, T, k, H, o, g)
+    """From dy [T,H]: dys [T*k,H] (or None, then w may be; may be ys) and dw [T,k] (or None, then ys may be)."""
+    _marshal.combine_backward(dy, ys, inv, w, dys, dw, stream)
 
 
 def moe_topk_backward(logits, topk_idx, dw, renorm: int, dlogits, stream=None) -> None:
     """dlogits [T,E] from the gates' gradients dw [T,k] at the chosen experts topk_idx [T,k]."""
-    a = _Args("moe_topk_backward")
-    T, k, idx = a.pairs("topk_idx", topk_idx)
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
-        a.refuse("logits must be fp32 [T, E]")
-    E = logits.shape[1]
-    z = a.flat("logits", logits, torch.float32, T, E)
-    g = a.flat("dw", dw, torch.float32, T, k)
-    o = a.flat("dlogits", dlogits, torch.float32, T, E)
-    a.call(lib.moe_topk_backward, stream, z, T, E, idx, k, g, renorm, o)
-
-
-# The configuration of a norm call, by its values (the library reads it during the call only).
-_norm_config = functools.lru_cache(maxsize=1024)(lambda *fields: ctypes.pointer(moe_norm_config(*fields)))
-
-
-def _norm_inputs(a: _Args, T, H, w_post, gate, w_pre, gate_kind):
-    q = None if w_post is None else a.flat("w_post", w_post, torch.float32, H)
-    p = None if w_pre is None else a.flat("w_pre", w_pre, torch.float32, H)
-    if (gate is None) != (gate_kind == MOE_GATE_NONE):
-        a.refuse("gate and gate_kind must go together")
-    g = None if gate is None else a.flat("gate", gate, torch.float32, T if gate_kind == MOE_GATE_TOKEN else H)
-    return q, g, p
+    _marshal.topk_backward(logits, topk_idx, dw, renorm, dlogits, stream)
 
 
 def moe_block_norm(h, y=None, w_post=None, gate=None, w_pre=None, h_out=None, x_out=None,
                    gate_kind: int = MOE_GATE_NONE, alpha: float = 1.0, eps: float = 1e-6, stream=None) -> None:
     """h_out = h + alpha gate norm(y; w_post), x_out = norm(h_out; w_pre): the step between two blocks."""
-    a = _Args("moe_block_norm")
-    hp, h_fmt, ld_h, T, H = a.rows("h", h)
-    yp = ho = xo = None
-    y_fmt = x_fmt = h_fmt
-    ld_y = ld_x = H
-    if y is not None:
-        yp, y_fmt, ld_y, _, _ = a.rows("y", y, T, H)
-    if h_out is not None:
-        ho = hp if h_out is h else a.rows("h_out", h_out, T, H, False, (h_fmt, ld_h))[0]
-    if x_out is not None:
-        xo, x_fmt, ld_x, _, _ = a.rows("x_out", x_out, T, H)
-    q, g, p = _norm_inputs(a, T, H, w_post, gate, w_pre, gate_kind)
-    a.call(lib.moe_block_norm, stream, _norm_config(T, H, h_fmt, y_fmt, x_fmt, gate_kind, alpha, eps, ld_h, ld_y, ld_x),
-           hp, yp, q, g, p, ho, xo)
+    _marshal.block_norm(h, y, w_post, gate, w_pre, h_out, x_out, gate_kind, alpha, eps, stream)
 
 
 def moe_block_norm_workspace(T: int, H: int) -> int:
@@ -706,39 +534,8 @@ def moe_block_norm_backward(h_out, y, w_post, gate, w_pre, dh_out, dx, dh, dy, d
                             gate_kind: int = MOE_GATE_NONE, alpha: float = 1.0, eps: float = 1e-6,
                             stream=None) -> None:
     """The gradient of moe_block_norm from dh_out and dx (either may be None); any output may be None."""
-    a = _Args("moe_block_norm_backward")
-    lead = dx if dh_out is None else dh_out
-    if not isinstance(lead, torch.Tensor) or lead.dim() != 2:
-        a.refuse("dh_out or dx must be given")
-    T, H = lead.shape
-    # (format, row stride) that h_out, dh_out and dh share, and y and dy
-    h_like = y_like = None
-    hp = yp = dhp = dxp = o_h = o_y = None
-    h_fmt = y_fmt = x_fmt = 0
-    ld_h = ld_y = ld_x = H
-    if dh_out is not None:
-        dhp, h_fmt, ld_h, _, _ = a.rows("dh_out", dh_out, T, H)
-        h_like = h_fmt, ld_h
-    if h_out is not None:
-        hp, h_fmt, ld_h, _, _ = a.rows("h_out", h_out, T, H, False, h_like)
-        h_like = h_fmt, ld_h
-    if dh is not None:
-        o_h, h_fmt, ld_h, _, _ = a.rows("dh", dh, T, H, False, h_like)
-    if y is not None:
-        yp, y_fmt, ld_y, _, _ = a.rows("y", y, T, H)
-        y_like = y_fmt, ld_y
-    if dy is not None:
-        o_y, y_fmt, ld_y, _, _ = a.rows("dy", dy, T, H, False, y_like)
-    if dx is not None:
-        dxp, x_fmt, ld_x, _, _ = a.rows("dx", dx, T, H)
-    q, g, p = _norm_inputs(a, T, H, w_post, gate, w_pre, gate_kind)
-    dq = None if dw_post is None else a.flat("dw_post", dw_post, torch.float32, H)
-    dp = None if dw_pre is None else a.flat("dw_pre", dw_pre, torch.float32, H)
-    dg = None if dgate is None else a.flat("dgate", dgate, torch.float32, T if gate_kind == MOE_GATE_TOKEN else H)
-    w, wn = a.workspace(ws)
-    a.call(lib.moe_block_norm_backward, stream,
-           _norm_config(T, H, h_fmt, y_fmt, x_fmt, gate_kind, alpha, eps, ld_h, ld_y, ld_x),
-           hp, yp, q, g, p, dhp, dxp, o_h, o_y, dq, dg, dp, w, wn)
+    _marshal.block_norm_backward(h_out, y, w_post, gate, w_pre, dh_out, dx, dh, dy, dw_post, dgate, dw_pre, ws,
+                                 gate_kind, alpha, eps, stream)
 
 
 def moe_decode_block(ctx: Ctx, layer, x, T, logit_bias, topk_idx, topk_w, slot_idx, y, norm: moe_norm_config, h,

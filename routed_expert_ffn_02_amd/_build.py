@@ -1,6 +1,7 @@
-"""Build the routed-MoE C-ABI library for gfx950 with hipcc (in-tree, no JIT cache).
+"""Build the routed-MoE C-ABI library for gfx950 with hipcc (in-tree, no JIT cache), and the
+Python module that hands torch tensors to the calls around the experts.
 
-    python routed_expert_ffn_02_amd/_build.py        # compile csrc/ -> libroutedmoe.so
+    python routed_expert_ffn_02_amd/_build.py        # compile csrc/ -> libroutedmoe.so, _marshal.so
 """
 from __future__ import annotations
 
@@ -9,15 +10,18 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(os.path.dirname(HERE), "_build")
 LIB = os.path.join(HERE, "libroutedmoe.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 ARCH = os.environ.get("RMOE_OFFLOAD_ARCH", "gfx950")
 
 HIP_SOURCES = ["route.hip", "lookup.hip", "decode.hip", "prefill.hip", "fill.hip", "tokens.hip", "norm.hip"]
 CPP_SOURCES = ["runtime.cpp", "cpu_ffn.cpp", "placement.cpp", "bank.cpp"]
+MARSHAL_SOURCE = "marshal.cpp"
 
 # Packed fp32 VALU ops are disabled for all device code (the host pass warns that it
 # does not know the feature; that is harmless).
@@ -43,6 +47,11 @@ def host_cxx() -> str:
     return cand if os.path.exists(cand) else (shutil.which("clang++") or "g++")
 
 
+def torch_root() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
 def _compile(src: str) -> str:
     path = os.path.join(CSRC, src)
     obj = os.path.join(BUILD, src + ".o")
@@ -50,6 +59,8 @@ def _compile(src: str) -> str:
         cmd = [hipcc()] + HIP_FLAGS + ["-c", path, "-o", obj]
     else:
         cmd = [host_cxx()] + CPP_FLAGS + ["-I", os.path.join(rocm_root(), "include"), "-c", path, "-o", obj]
+    if src == MARSHAL_SOURCE:
+        cmd += ["-DUSE_ROCM", "-I", os.path.join(torch_root(), "include"), "-I", sysconfig.get_paths()["include"]]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
@@ -59,18 +70,25 @@ def _compile(src: str) -> str:
 def build(verbose: bool = True) -> str:
     """Compile every source and link libroutedmoe.so (always rebuilds)."""
     os.makedirs(BUILD, exist_ok=True)
-    srcs = HIP_SOURCES + CPP_SOURCES
+    srcs = HIP_SOURCES + CPP_SOURCES + [MARSHAL_SOURCE]
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        objs = list(ex.map(_compile, srcs))
-    tmp = LIB + ".tmp"
-    cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs + ["-o", tmp, "-lpthread"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        *objs, marshal = ex.map(_compile, srcs)
+    _link([hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs, LIB, ["-lpthread"])
+    torch_lib = os.path.join(torch_root(), "lib")
+    _link([host_cxx(), "-shared", "-fPIC", marshal, "-L", HERE, "-L", torch_lib], MARSHAL,
+          ["-l:libroutedmoe.so", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-lamdhip64", "-Wl,-rpath,$ORIGIN"])
     if verbose:
         print(f"built {LIB}")
     return LIB
+
+
+def _link(cmd, out: str, libs) -> None:
+    tmp = out + ".tmp"
+    cmd = cmd + ["-o", tmp] + libs
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
 
 
 if __name__ == "__main__":

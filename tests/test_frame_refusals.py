@@ -159,46 +159,90 @@ def refused(f, *a, **kw):
     return str(e.value)
 
 
-def test_binding_refuses_what_the_library_would_misread():
-    T, k, H, E = 4, 2, 8, 4
-    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
-    x, xs, idx = torch.zeros(T, H), torch.zeros(T * k, H), i32(T, k)
-    tables = (i32(T * k), i32(T, k), i32(E + 1))
-    # right in every respect but for where it is
-    assert "on the GPU" in refused(R.moe_dispatch, idx, E, x, xs, *tables)
-    assert "int32" in refused(R.moe_dispatch, idx.long(), E, x, xs, *tables)
-    assert "T, k" in refused(R.moe_dispatch, i32(T * k), E, x, xs, *tables)
-    assert "contiguous" in refused(R.moe_dispatch, i32(k, T).t(), E, x, xs, *tables)
-    assert "on the GPU" in refused(R.moe_combine, xs, tables[1], torch.zeros(T, k), x)
-    a = R._Args("moe_dispatch")
-    for name, t, kw, msg in [
-            ("x", x.half(), {}, "fp32 or bf16"), ("x", x.double(), {}, "fp32 or bf16"), ("x", x[0], {}, "two-dimensional"),
-            ("x", torch.zeros(H, T).t(), {}, "contiguous rows"), ("x", torch.zeros(T, 2 * H)[:, ::2], {}, "contiguous rows"),
-            ("x", torch.zeros(1, H).expand(T, H), {}, "contiguous rows"), ("x", x, dict(n_rows=5), "shape"),
-            ("xs", torch.zeros(T, 2 * H)[:, :H], dict(dense=True), "without gaps"), ("x", x, dict(width=9), "shape"),
-            ("x", torch.zeros(0, H), {}, "shape"), ("h_out", x, dict(like=(BF16, H)), "belongs to"),
-            ("h_out", torch.zeros(T, 2 * H)[:, :H], dict(like=(F32, H)), "belongs to"), ("x", None, {}, "two-dimensional")]:
-        assert msg in refused(a.rows, name, t, **kw), (name, msg)
-    for t, msg in [(torch.zeros(T, k, dtype=torch.float64), "float32"), (torch.zeros(k, T).t(), "contiguous"),
-                   (torch.zeros(T, k + 1), "shape"), (None, "contiguous")]:
-        assert msg in refused(a.flat, "w", t, torch.float32, T, k)
-    assert "go together" in refused(R._norm_inputs, a, T, H, None, None, None, R.MOE_GATE_TOKEN)
-    assert "contiguous" in refused(a.workspace, x.t())
-    assert a.workspace(None) == a.workspace(x[:0]) == (None, 0)
+T, k, H, E = 4, 2, 8, 4
 
 
-class _On:
-    """A stand-in for a tensor on a GPU."""
-
-    def __init__(self, dev):
-        self.get_device = lambda: dev
+def i32(*s):
+    return torch.zeros(s, dtype=torch.int32)
 
 
-def test_binding_refuses_mixed_devices():
-    a = R._Args("moe_combine")
-    a.place("ys", _On(1))
-    assert "cuda:0" in refused(a.place, "inv", _On(0))
-    assert "on the GPU" in refused(a.place, "inv", _On(-1))
+def f32(*s):
+    return torch.zeros(s)
+
+
+def tables():
+    return [i32(T * k), i32(T, k), i32(E + 1)]
+
+
+@pytest.mark.parametrize("bad,msg", [
+    (dict(), "topk_idx must be on the GPU"), (dict(topk_idx=i32(T, k).long()), "int32"), (dict(topk_idx=i32(T * k)), "T, k"),
+    (dict(topk_idx=i32(0, k)), "T, k"), (dict(topk_idx=i32(k, T).t()), "contiguous"), (dict(topk_idx=None), "tensor"),
+    (dict(topk_idx=[[0, 1]]), "tensor"), (dict(n_experts=1 << 40), "out of range"), (dict(n_experts="4"), "integer"),
+    (dict(x=f32(T, H).half()), "fp32 or bf16"), (dict(x=f32(T, H).double()), "fp32 or bf16"),
+    (dict(x=f32(H)), "two-dimensional"), (dict(x=f32(H, T).t()), "contiguous rows"),
+    (dict(x=f32(T, 2 * H)[:, ::2]), "contiguous rows"), (dict(x=f32(1, H).expand(T, H)), "contiguous rows"),
+    (dict(x=f32(5, H)), "shape"), (dict(x=f32(T, 0)), "shape"), (dict(x=None), "x must be a tensor"),
+    (dict(xs=None), "xs must be a tensor"), (dict(xs=f32(T * k, 2 * H)[:, :H]), "without gaps"), (dict(xs=f32(T * k, 9)), "shape"),
+    (dict(xs=f32(T * k, H).bfloat16()), "x's type"), (dict(perm=i32(T * k + 1)), "shape"), (dict(perm=f32(T * k)), "int32"),
+    (dict(inv=i32(k, T)), "shape"), (dict(offsets=i32(E)), "shape"), (dict(ws=f32(4, 2).t()), "ws must be a contiguous"),
+    (dict(x=f32(T, H).to_sparse()), "strided"), (dict(topk_idx=i32(T, k).to("meta")), "on the GPU")])
+def test_dispatch_binding_refuses(bad, msg):
+    perm, inv, offsets = tables()
+    a = dict(topk_idx=i32(T, k), n_experts=E, x=f32(T, H), xs=f32(T * k, H), perm=perm, inv=inv, offsets=offsets, ws=None)
+    a.update(bad)
+    assert msg in refused(R.moe_dispatch, **a)
+
+
+@pytest.mark.parametrize("bad,msg", [
+    (dict(), "must be on the GPU"), (dict(inv=i32(T, k).short()), "int32"), (dict(ys=f32(T * k + 1, H)), "shape"),
+    (dict(w=f32(T, k).double()), "float32"), (dict(w=f32(k, T).t()), "contiguous"), (dict(w=f32(T, k + 1)), "shape"),
+    (dict(w=None), "w must be a tensor"), (dict(y=f32(T, H + 1)), "shape"), (dict(y=f32(T, H).half()), "fp32 or bf16")])
+def test_combine_binding_refuses(bad, msg):
+    a = dict(ys=f32(T * k, H), inv=i32(T, k), w=f32(T, k), y=f32(T, H))
+    a.update(bad)
+    assert msg in refused(R.moe_combine, **a)
+    if "w" not in bad:
+        assert msg in refused(R.moe_dispatch_backward, a["ys"], a["inv"], a["y"])
+        b = dict(dy=a["y"], ys=a["ys"], inv=a["inv"], w=a["w"], dys=f32(T * k, a["y"].shape[1]), dw=f32(T, k))
+        if a["y"].shape == (T, H):
+            assert msg in refused(R.moe_combine_backward, **b)
+
+
+def test_combine_backward_binding_refuses():
+    a = dict(dy=f32(T, H), ys=f32(T * k, H), inv=i32(T, k), w=f32(T, k), dys=f32(T * k, H), dw=f32(T, k))
+    for bad, msg in [(dict(dys=f32(T * k, H).bfloat16()), "ys's type"), (dict(w=None), "w must be"), (dict(ys=None), "ys must be"),
+                     (dict(dw=f32(T, k).bfloat16()), "float32"), (dict(dys=None, w=None), "on the GPU"),
+                     (dict(dw=None, ys=None), "on the GPU")]:
+        assert msg in refused(R.moe_combine_backward, **{**a, **bad})
+
+
+def test_topk_backward_binding_refuses():
+    a = dict(logits=f32(T, E), topk_idx=i32(T, k), dw=f32(T, k), renorm=0, dlogits=f32(T, E))
+    for bad, msg in [(dict(), "on the GPU"), (dict(logits=f32(T, E).bfloat16()), "fp32"), (dict(logits=f32(T, 2 * E)[:, :E]), "gaps"),
+                     (dict(logits=f32(T + 1, E)), "shape"), (dict(dlogits=f32(T, E + 1)), "shape"), (dict(renorm=None), "integer"),
+                     (dict(dw=f32(T, k + 1)), "shape"), (dict(topk_idx=f32(T, k)), "int32")]:
+        assert msg in refused(R.moe_topk_backward, **{**a, **bad})
+
+
+def test_block_norm_binding_refuses():
+    a = dict(h=f32(T, H), y=f32(T, H), w_post=f32(H), gate=f32(H), w_pre=f32(H), h_out=f32(T, H), x_out=f32(T, H),
+             gate_kind=R.MOE_GATE_CHANNEL)
+    wide = f32(T, 2 * H)[:, :H]
+    for bad, msg in [(dict(), "on the GPU"), (dict(h_out=f32(T, H).bfloat16()), "belongs to"), (dict(h_out=wide), "belongs to"),
+                     (dict(gate_kind=R.MOE_GATE_NONE), "go together"), (dict(gate=None), "go together"), (dict(y=f32(T + 1, H)), "shape"),
+                     (dict(gate=f32(T), gate_kind=R.MOE_GATE_CHANNEL), "shape"), (dict(w_pre=f32(H + 1)), "shape"),
+                     (dict(w_post=f32(H).bfloat16()), "float32"), (dict(alpha="a"), "number"), (dict(h=None), "h must be"),
+                     (dict(gate_kind=1.5), "integer")]:
+        assert msg in refused(R.moe_block_norm, **{**a, **bad})
+    b = dict(h_out=f32(T, H), y=f32(T, H), w_post=f32(H), gate=f32(H), w_pre=f32(H), dh_out=f32(T, H), dx=f32(T, H), dh=f32(T, H),
+             dy=f32(T, H), dw_post=f32(H), dgate=f32(H), dw_pre=f32(H), gate_kind=R.MOE_GATE_CHANNEL)
+    for bad, msg in [(dict(), "on the GPU"), (dict(dh_out=None, dx=None), "dh_out or dx"), (dict(dx=f32(T, H + 1)), "shape"),
+                     (dict(h_out=wide), "belongs to"), (dict(dh=wide), "belongs to"), (dict(dy=f32(T, H).bfloat16()), "belongs to"),
+                     (dict(dgate=f32(T + 1)), "shape"), (dict(dw_pre=f32(H).double()), "float32"),
+                     (dict(dh_out=None, h_out=None, dh=wide), "on the GPU")]:
+        assert msg in refused(R.moe_block_norm_backward, **{**b, **bad})
+    with pytest.raises(TypeError):
+        R._marshal.combine(1, 2)
 
 
 def test_side_by_side_blocks_of_one_buffer_are_told_apart():

@@ -409,3 +409,27 @@ def test_two_streams_at_once_and_graph_replays():
             p.run()
             torch.cuda.synchronize()
             assert all(torch.equal(u, v) for u, v in zip(got, p.outputs()))
+
+
+def test_streams_and_devices_as_the_binding_takes_them():
+    """A stream object, its handle and the current stream lead to the same call; a tensor on the host
+    among tensors on the GPU is named."""
+    r = R()
+    inv = torch.tensor([[0, 1], [3, 2]], dtype=torch.int32, device="cuda")
+    ys, w = torch.randn(4, 33, device="cuda"), torch.rand(2, 2, device="cuda")
+    ys[2] = float("inf")
+    out = [torch.empty(2, 33, device="cuda") for _ in range(4)]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    r.moe_combine(ys, inv, w, out[0])
+    r.moe_combine(ys, inv, w, out[1], stream=s)
+    r.moe_combine(ys, inv, w, out[2], stream=s.cuda_stream)
+    with torch.cuda.stream(s):
+        r.moe_combine(ys, inv, w, out[3])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, out[0]) for o in out)
+    for bad in (dict(ys=ys.cpu()), dict(inv=inv.cpu()), dict(w=w.cpu()), dict(y=out[0].cpu())):
+        with pytest.raises(r.MoeError, match=f"{list(bad)[0]} must be on the GPU"):
+            r.moe_combine(**{**dict(ys=ys, inv=inv, w=w, y=out[0]), **bad})
+    with pytest.raises(r.MoeError, match="stream"):
+        r.moe_combine(ys, inv, w, out[0], stream="0")
