@@ -139,6 +139,10 @@ class Call {
       s = c10::hip::getCurrentHIPStream((c10::DeviceIndex)device_).stream();
     } else if (PyLong_Check(o)) {
       s = PyLong_AsVoidPtr(o);
+      if (PyErr_Occurred()) {
+        PyErr_Clear();
+        refuse("stream is no handle");
+      }
     } else {
       const int64_t device = attribute(o, "device_index");
       if (device != device_)
