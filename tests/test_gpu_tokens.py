@@ -272,11 +272,12 @@ def test_offsets_past_32_bits():
 # --- the gates' gradient -----------------------------------------------------
 @pytest.mark.parametrize("renorm", [0, 1])
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 256), (5, 2, 8), (6, 3, 65), (37, 8, 100), (64, 6, 256), (9, 16, 257),
-                                   (21, 16, 1000), (8, 64, 1024), (3, 1000, 1024)])
+                                   (21, 16, 1000), (8, 64, 1024), (3, 1000, 1024),
+                                   (5, 150, 40), (70, 12, 5)])
 def test_topk_backward(T, k, E, renorm):
     rng = np.random.default_rng(E + k + renorm)
     z = (3.0 * rng.standard_normal((T, E))).astype(np.float32)
-    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    idx = np.stack([rng.permutation(E)[:k] if k <= E else rng.integers(0, E, k) for _ in range(T)]).astype(np.int32)
     if T > 4:
         idx[1, 0] = idx[1, k - 1]                 # the same expert twice (k >= 2 here)
         idx[2, 0] = -1
