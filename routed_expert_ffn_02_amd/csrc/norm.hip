@@ -275,9 +275,12 @@ __global__ __launch_bounds__(1024) void norm_reduce(const float* __restrict__ pa
   const int lane = threadIdx.x & 31, group = threadIdx.x >> 5, i = blockIdx.x * 32 + lane, kind = blockIdx.y;
   const float* p = part + (int64_t)kind * G * H;
   float v = 0.f;
-  if (i < H) {
-#pragma unroll 8
-    for (int g = group; g < G; g += 32) v += p[(int64_t)g * H + i];
+  for (int g0 = group; g0 < G; g0 += 256) {
+    float r[8];  // eight rows in flight, without a branch
+#pragma unroll
+    for (int u = 0; u < 8; ++u) r[u] = p[(int64_t)min(g0 + 32 * u, G - 1) * H + min(i, H - 1)];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v += g0 + 32 * u < G ? r[u] : 0.f;
   }
   s_v[group][lane] = v;
   __syncthreads();

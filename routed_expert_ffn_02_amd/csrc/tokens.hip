@@ -205,8 +205,10 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_scan(int32_t* __restric
   constexpr int kHold = 16;  // a column's piece stays in registers up to this length
   int v[kHold], sum = 0;
 #pragma unroll
+  for (int i = 0; i < kHold; ++i) v[i] = hist[(size_t)min(c0 + i, chunks - 1) * E + e];  // all in flight
+#pragma unroll
   for (int i = 0; i < kHold; ++i) {
-    v[i] = c0 + i < c1 ? hist[(size_t)(c0 + i) * E + e] : 0;
+    v[i] = c0 + i < c1 ? v[i] : 0;
     sum += v[i];
   }
 #pragma unroll 8
