@@ -35,7 +35,10 @@ struct NormArgs {
 };
 
 // The sum over the workgroup's wavefronts (at most W) of NV values per thread, in wavefront
-// order.
+// order.  Its one barrier stands between the wavefronts' writes and the reads of all of them, none
+// behind the reads: before the next sum of the same object, the caller passes another barrier
+// (that of a second object's sum, or its own), or a fast wavefront overwrites what a slow one has
+// yet to read.
 template <int NV, int W>
 struct BlockSum {
   float v[NV][W];
@@ -234,7 +237,10 @@ __global__ __launch_bounds__(64 * WAVES) void block_norm_backward_kernel(NormArg
       o.set(dh);
       o.template store_wave<true>(a.dh + t * a.h_pitch, at, a.H);
     }
-    if (!a.y) continue;
+    if (!a.y) {
+      __syncthreads();  // behind the reads of s_a, where the second sum's barrier does not come
+      continue;
+    }
     s_b.sum(dot);
     const float ag = a.gate_kind == MOE_GATE_TOKEN ? a.alpha * a.gate[t] : a.alpha;
     const float ym = a.w_post ? ag * ry * ry * (dot[0] * a.per_h) : 0.f;
