@@ -634,6 +634,10 @@ bool move_shape_ok(int32_t T, int32_t k, int32_t H) {
          H <= kMoveMaxH;
 }
 
+// int32 and fp32 tables: aligned to their elements (a null one is).
+template <typename... P>
+bool tables_aligned(const P*... p) { return (aligned_to(p, 4) && ...); }
+
 // A caller's row stride in elements (0: dense rows), or -1.
 int64_t row_stride(int64_t ld, int32_t H) { return ld == 0 ? H : (ld >= H && ld <= kMaxStride ? ld : -1); }
 
@@ -684,6 +688,7 @@ extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, i
   if (!topk_idx || !perm || !inv || !offsets || (x == nullptr) != (xs == nullptr)) return MOE_EINVAL;
   const int64_t need = moe_dispatch_workspace(T, k, n_experts);
   if (need < 0 || (need > 0 && !ws) || ws_bytes < (size_t)need || !aligned_to(ws, 4)) return MOE_EINVAL;
+  if (!tables_aligned(topk_idx, perm, inv, offsets)) return MOE_EINVAL;
   const int64_t P = (int64_t)T * k;
   int64_t ld = 0;
   if (x) {
@@ -749,7 +754,7 @@ extern "C" MOE_API moe_status moe_dispatch_backward(const void* dxs, int32_t dxs
                                                     moe_stream_t stream) {
   const int64_t ld = row_stride(ld_dx, H), P = (int64_t)T * k;
   if (!dxs || !inv || !dx || !fmt_ok(dxs_fmt) || !fmt_ok(dx_fmt) || !move_shape_ok(T, k, H) || ld < 0) return MOE_EINVAL;
-  if (!aligned_to(dxs, fmt_bytes(dxs_fmt)) || !aligned_to(dx, fmt_bytes(dx_fmt))) return MOE_EINVAL;
+  if (!aligned_to(dxs, fmt_bytes(dxs_fmt)) || !aligned_to(dx, fmt_bytes(dx_fmt)) || !tables_aligned(inv)) return MOE_EINVAL;
   const Span out = rows_of(dx, T, H, dx_fmt, ld);
   if (overlap(out, rows_of(dxs, P, H, dxs_fmt, H)) || overlap(out, flat(inv, 4 * P))) return MOE_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -763,7 +768,7 @@ extern "C" MOE_API moe_status moe_combine(const void* ys, int32_t ys_fmt, const 
   const int64_t ld = row_stride(ld_y, H), P = (int64_t)T * k;
   if (!ys || !inv || !w || !y || !fmt_ok(ys_fmt) || !fmt_ok(y_fmt) || !move_shape_ok(T, k, H) || ld < 0)
     return MOE_EINVAL;
-  if (!aligned_to(ys, fmt_bytes(ys_fmt)) || !aligned_to(y, fmt_bytes(y_fmt))) return MOE_EINVAL;
+  if (!aligned_to(ys, fmt_bytes(ys_fmt)) || !aligned_to(y, fmt_bytes(y_fmt)) || !tables_aligned(inv, w)) return MOE_EINVAL;
   const Span out = rows_of(y, T, H, y_fmt, ld);
   if (overlap(out, rows_of(ys, P, H, ys_fmt, H)) || overlap(out, flat(inv, 4 * P)) || overlap(out, flat(w, 4 * P)))
     return MOE_EINVAL;
@@ -778,7 +783,8 @@ extern "C" MOE_API moe_status moe_combine_backward(const void* dy, int32_t dy_fm
   const int64_t ld = row_stride(ld_dy, H), P = (int64_t)T * k;
   if (!dy || !inv || (!dys && !dw) || (dw && !ys) || (dys && !w)) return MOE_EINVAL;
   if (!fmt_ok(dy_fmt) || !fmt_ok(ys_fmt) || !move_shape_ok(T, k, H) || ld < 0) return MOE_EINVAL;
-  if (!aligned_to(dy, fmt_bytes(dy_fmt)) || !aligned_to(ys, fmt_bytes(ys_fmt)) || !aligned_to(dys, fmt_bytes(ys_fmt)))
+  if (!aligned_to(dy, fmt_bytes(dy_fmt)) || !aligned_to(ys, fmt_bytes(ys_fmt)) || !aligned_to(dys, fmt_bytes(ys_fmt)) ||
+      !tables_aligned(inv, w, dw))
     return MOE_EINVAL;
   const Span in[4] = {rows_of(dy, T, H, dy_fmt, ld), dys == ys ? flat(nullptr, 0) : rows_of(ys, P, H, ys_fmt, H),
                       flat(inv, 4 * P), flat(w, 4 * P)};
@@ -802,6 +808,7 @@ extern "C" MOE_API moe_status moe_topk_backward(const float* logits, int32_t T, 
                                                 float* dlogits, moe_stream_t stream) {
   if (!logits || !topk_idx || !dw || !dlogits || !move_shape_ok(T, k, 1)) return MOE_EINVAL;
   if (n_experts < 1 || n_experts > kMaxExperts || (renorm != 0 && renorm != 1)) return MOE_EINVAL;
+  if (!tables_aligned(logits, topk_idx, dw, dlogits)) return MOE_EINVAL;
   const int64_t P = (int64_t)T * k, n = (int64_t)T * n_experts;
   const Span out = flat(dlogits, 4 * n);
   if ((dlogits != logits && overlap(out, flat(logits, 4 * n))) || overlap(out, flat(topk_idx, 4 * P)) ||
