@@ -665,8 +665,9 @@ MOE_API moe_status moe_combine_backward(const void* dy, int32_t dy_fmt, int64_t 
  *   renorm 0: dz[e] = p_e (sum_{j: idx_j = e} dw_j - sum_j p_{idx_j} dw_j),  p = softmax(z)
  *   renorm 1: the same with p the softmax over the chosen logits alone; dz = 0 elsewhere
  * logits, dlogits: device fp32 [T,E] (dlogits may be logits); topk_idx int32 and dw fp32 [T,k]; a pair
- * whose id is outside [0, E) is left out.  Logits of -inf have p = 0; a token with no logit above
- * -inf, or with renorm 1 and no pair kept, gets zeros.
+ * whose id is outside [0, E) is left out.  Logits of -inf have p = 0: their gradient is 0 and their
+ * pairs' dw add nothing, whatever their values; a token with no logit above -inf, or with renorm 1
+ * and no pair kept, gets zeros.
  */
 MOE_API moe_status moe_topk_backward(const float* logits, int32_t T, int32_t n_experts, const int32_t* topk_idx,
                                      int32_t k, const float* dw, int32_t renorm, float* dlogits, moe_stream_t stream);

@@ -603,14 +603,18 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const float* logits,
   }
   mx = wave_max(mx);
   float sum = 0.f, mean = 0.f;
+  uint32_t live = 0;  // a bit for each of the lane's logits that is in the softmax
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // a masked logit (-inf) has no share, also where every logit is masked
-      v[c][i] = v[c][i] != -INFINITY ? __expf(v[c][i] - mx) : 0.f;
+      // a masked logit (-inf) has no share, also where every logit is masked, and no part in
+      // the mean, whatever the gate's gradient there (0 * inf would be NaN)
+      const bool in = v[c][i] != -INFINITY;
+      live |= in ? 1u << (4 * c + i) : 0u;
+      v[c][i] = in ? __expf(v[c][i] - mx) : 0.f;
       sum += renorm ? n[c][i] * v[c][i] : v[c][i];
-      mean += d[c][i] * v[c][i];
+      mean += in ? d[c][i] * v[c][i] : 0.f;
     }
   sum = wave_sum(sum);
   mean = wave_sum(mean);
@@ -620,7 +624,10 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const float* logits,
   for (int c = 0; c < C; ++c) {
     float o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = v[c][i] * r * (d[c][i] - (renorm ? n[c][i] * mean : mean));
+    for (int i = 0; i < 4; ++i) {
+      // 0 where there is no share (masked, or not chosen with renorm), also under a NaN mean
+      o[i] = live >> (4 * c + i) & 1 ? v[c][i] * r * (d[c][i] - (renorm ? n[c][i] * mean : mean)) : 0.f;
+    }
     Chunk<MOE_AFMT_F32, 4> out;
     out.set(o);
     out.store_own(reinterpret_cast<uint8_t*>(dlogits + (int64_t)t * E), Piece<4>(64 * c + lane, E));
