@@ -718,8 +718,11 @@ MOE_API moe_status moe_block_norm_backward(const moe_norm_config* cfg, const voi
 /*
  * One decode layer step with the step to the next block: moe_decode_layer into y, then
  * moe_block_norm of y into the residual stream h (in place) and, unless x_next is NULL, the next
- * block's input.  norm->T must be T and norm->H the context's hidden size, norm->y_fmt
- * MOE_AFMT_F32 with dense rows (y is the [T,H] fp32 output of moe_decode_layer).  x_next may be x.
+ * block's input.  norm->T must be T and norm->H the context's hidden size (up to 8192, as
+ * moe_block_norm takes: wider contexts decode with moe_decode_layer), norm->y_fmt MOE_AFMT_F32
+ * with dense rows (y is the [T,H] fp32 output of moe_decode_layer).  h or x_next may be x itself
+ * (in the context's activation format, with dense rows); apart from that they share no byte with
+ * x, logit_bias, topk_idx, topk_w, slot_idx, y, the arena or the router's weights.
  * Errors and capture as moe_decode_layer; MOE_EINVAL for what moe_block_norm refuses, before
  * anything is enqueued.
  */

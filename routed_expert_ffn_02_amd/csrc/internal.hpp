@@ -246,6 +246,16 @@ void launch_prefill_combine(const PrefillArgs& a, hipStream_t s);
 // moe_block_norm; check_only: its argument checks alone (nothing is enqueued).
 moe_status block_norm(const moe_norm_config* cfg, const void* h, const void* y, const float* w_post, const float* gate,
                       const float* w_pre, void* h_out, void* x_out, hipStream_t s, bool check_only);
+// The checks of moe_block_norm in moe_decode_block's place (y into h, in place, and x_next), and
+// that nothing it writes lies where the layer step reads or writes: h and x_next may each be the
+// step's input x of format afmt, but share no byte with the n blocks of memory in `other`.
+struct Region {
+  const void* p;
+  int64_t bytes;
+};
+moe_status block_step_check(const moe_norm_config* cfg, const void* x, int afmt, const void* h, const float* y,
+                            const float* w_post, const float* gate, const float* w_pre, const void* x_next,
+                            const Region* other, int n);
 
 // ---------------------------------------------------------------- CPU branch
 struct CpuPool {

@@ -420,6 +420,27 @@ moe_status rmoe::block_norm(const moe_norm_config* cfg, const void* h, const voi
   return launch_norm<false>(*cfg, a, cfg->T, s);
 }
 
+moe_status rmoe::block_step_check(const moe_norm_config* cfg, const void* x, int afmt, const void* h, const float* y,
+                                  const float* w_post, const float* gate, const float* w_pre, const void* x_next,
+                                  const Region* other, int n) {
+  NormArgs a{};
+  if (!y || block_norm(cfg, h, y, w_post, gate, w_pre, const_cast<void*>(h), const_cast<void*>(x_next), nullptr, true) != MOE_OK ||
+      !norm_config_ok(cfg, &a))
+    return MOE_EINVAL;
+  const NormSpans sp{*cfg, a};
+  const Span step_x = {x, cfg->T, cfg->H * fmt_bytes(afmt), cfg->H * fmt_bytes(afmt)}, step_y = sp.y(y);
+  if (overlap(step_y, sp.w(w_post)) || overlap(step_y, sp.gate(gate)) || overlap(step_y, sp.w(w_pre))) return MOE_EINVAL;
+  const Span out[2] = {sp.h(h), sp.x(x_next)};
+  const int fmt[2] = {cfg->h_fmt, cfg->x_fmt};
+  for (int o = 0; o < 2; ++o) {
+    const bool is_x = out[o].p == x && fmt[o] == afmt && (cfg->T == 1 || out[o].pitch == step_x.pitch);
+    if (!is_x && overlap(out[o], step_x)) return MOE_EINVAL;
+    for (int i = 0; i < n; ++i)
+      if (overlap(out[o], flat(other[i].p, other[i].bytes))) return MOE_EINVAL;
+  }
+  return MOE_OK;
+}
+
 extern "C" MOE_API moe_status moe_block_norm(const moe_norm_config* cfg, const void* h, const void* y,
                                              const float* w_post, const float* gate, const float* w_pre, void* h_out,
                                              void* x_out, moe_stream_t stream) {

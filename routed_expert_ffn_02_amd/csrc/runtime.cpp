@@ -921,8 +921,13 @@ MOE_API moe_status moe_decode_block(moe_ctx* ctx, int32_t layer, const void* x, 
   CHECK_ARG(norm && norm->T == T && norm->H == ctx->cfg.hidden, "norm: T and H must be the step's");
   CHECK_ARG(norm->y_fmt == MOE_AFMT_F32 && (norm->ld_y == 0 || norm->ld_y == norm->H), "norm: y is fp32 with dense rows");
   hipStream_t s = static_cast<hipStream_t>(stream);
-  CHECK_ARG(y && block_norm(norm, h, y, w_post, gate, w_pre, h, x_next, s, true) == MOE_OK,
-            "norm: bad format, stride, gate, alignment or overlap");
+  const moe_config& c = ctx->cfg;
+  const int64_t pairs = 4ll * T * c.top_k;
+  const Region other[] = {{logit_bias, 4ll * T * c.n_experts}, {topk_idx, pairs}, {topk_w, pairs}, {slot_idx, pairs},
+                          {ctx->arena, (int64_t)ctx->arena_bytes},
+                          {ctx->router_w, 4ll * c.n_layers * c.n_experts * c.hidden}};
+  CHECK_ARG(block_step_check(norm, x, c.afmt, h, y, w_post, gate, w_pre, x_next, other, 6) == MOE_OK,
+            "norm: bad shape, format, stride, gate, alignment or overlap");
   const moe_status st = moe_decode_layer(ctx, layer, x, T, logit_bias, topk_idx, topk_w, slot_idx, y, stream);
   if (st != MOE_OK) return st;
   if (block_norm(norm, h, y, w_post, gate, w_pre, h, x_next, s, false) != MOE_OK)
