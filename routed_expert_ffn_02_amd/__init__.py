@@ -540,7 +540,10 @@ def moe_block_norm_backward(h_out, y, w_post, gate, w_pre, dh_out, dx, dh, dy, d
 
 def moe_decode_block(ctx: Ctx, layer, x, T, logit_bias, topk_idx, topk_w, slot_idx, y, norm: moe_norm_config, h,
                      w_post=None, gate=None, w_pre=None, x_next=None, stream=None) -> None:
-    """One decode layer step (moe_decode_layer into y) and moe_block_norm of y into h, in place, and x_next."""
+    """One decode layer step (moe_decode_layer into y) and moe_block_norm of y into h, in place, and x_next.
+    The step's arguments as in moe_decode_layer; the norm's tensors are checked against `norm`."""
+    _marshal.check_block(norm.T, norm.H, norm.h_fmt, norm.x_fmt, norm.gate_kind, norm.ld_h, norm.ld_x, h, w_post, gate, w_pre,
+                         x_next)
     _check(ctx, lib.moe_decode_block(ctx.handle, layer, _ptr(x), T, _ptr(logit_bias), _ptr(topk_idx), _ptr(topk_w),
                                      _ptr(slot_idx), _ptr(y), ctypes.byref(norm), _ptr(h), _ptr(w_post), _ptr(gate),
                                      _ptr(w_pre), _ptr(x_next), _stream(stream)), "moe_decode_block")

@@ -39,6 +39,14 @@ int32_t int_arg(PyObject* o, const char* name) {
     refuse(std::string(name) + " is out of range");
   return (int32_t)v;
 }
+int64_t long_arg(PyObject* o, const char* name) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be an integer");
+  }
+  return v;
+}
 float float_arg(PyObject* o, const char* name) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) {
@@ -106,6 +114,19 @@ class Call {
     return static_cast<T*>(t.data_ptr());
   }
 
+  // T rows of H elements of format fmt, ld elements apart (0: H); of any shape without gaps where
+  // the rows have none.
+  void block_rows(PyObject* o, const char* name, int32_t T, int32_t H, int32_t fmt, int64_t ld) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.scalar_type() != (fmt == MOE_AFMT_BF16 ? at::kBFloat16 : at::kFloat))
+      refuse(std::string(name) + " must have the type that norm gives it");
+    const bool matrix = t.dim() == 2 && t.size(0) == T && t.size(1) == H && (H == 1 || t.stride(1) == 1) &&
+                        (T == 1 || t.stride(0) == (ld ? ld : H));
+    const bool dense = t.numel() == (int64_t)T * H && t.is_contiguous() && (T == 1 || ld == 0 || ld == H);
+    if (!matrix && !dense)
+      refuse(std::string(name) + " has shape " + shape_text(t.sizes()) + " or strides that are not norm's");
+  }
+
   // An int32 table [T, k].
   int32_t* pairs(PyObject* o, const char* name, int32_t* T, int32_t* k) {
     const at::Tensor& t = tensor(o, name);
@@ -127,13 +148,17 @@ class Call {
     return *bytes ? t.data_ptr() : nullptr;
   }
 
-  // The stream of the call: `o` (a handle, or a torch stream), or the current one of the
-  // tensors' device, which becomes the current device until the call is over.
-  moe_stream_t stream(PyObject* o) {
+  void on_one_gpu() const {
     if (off_gpu_) refuse(std::string(off_gpu_) + " must be on the GPU");
     if (other_)
       refuse(std::string(other_) + " is on cuda:" + std::to_string(other_device_) + ", other tensors on cuda:" +
              std::to_string(device_));
+  }
+
+  // The stream of the call: `o` (a handle, or a torch stream), or the current one of the
+  // tensors' device, which becomes the current device until the call is over.
+  moe_stream_t stream(PyObject* o) {
+    on_one_gpu();
     void* s = nullptr;
     if (o == Py_None) {
       s = c10::hip::getCurrentHIPStream((c10::DeviceIndex)device_).stream();
@@ -380,6 +405,24 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// (T, H, h_fmt, x_fmt, gate_kind, ld_h, ld_x, h, w_post, gate, w_pre, x_next): the norm's tensors of
+// moe_decode_block against its configuration.  That call goes through ctypes with the rest of a context's, so
+// an address (an int) stands for a tensor there and is taken as it is.
+PyObject* check_block(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<12>("moe_decode_block", args, n, [](PyObject* const* a) {
+    Call c;
+    const int32_t T = int_arg(a[0], "T"), H = int_arg(a[1], "H"), kind = int_arg(a[4], "gate_kind");
+    const auto given = [](PyObject* o) { return o != Py_None && !PyLong_Check(o); };
+    if (given(a[7])) c.block_rows(a[7], "h", T, H, int_arg(a[2], "h_fmt"), long_arg(a[5], "ld_h"));
+    if (given(a[11])) c.block_rows(a[11], "x_next", T, H, int_arg(a[3], "x_fmt"), long_arg(a[6], "ld_x"));
+    if (given(a[8])) c.need_flat<float>(a[8], "w_post", kF32, {H});
+    if (given(a[9])) c.need_flat<float>(a[9], "gate", kF32, {kind == MOE_GATE_TOKEN ? T : H});
+    if (given(a[10])) c.need_flat<float>(a[10], "w_pre", kF32, {H});
+    c.on_one_gpu();
+    return MOE_OK;
+  });
+}
+
 // (MoeError)
 PyObject* set_error(PyObject*, PyObject* o) {
   Py_INCREF(o);
@@ -389,7 +432,7 @@ PyObject* set_error(PyObject*, PyObject* o) {
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(dispatch), FAST(dispatch_backward), FAST(combine), FAST(combine_backward),
-                           FAST(topk_backward), FAST(block_norm), FAST(block_norm_backward),
+                           FAST(topk_backward), FAST(block_norm), FAST(block_norm_backward), FAST(check_block),
                            {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "Tensors to the C entry points around the experts", -1,
                         g_methods, nullptr, nullptr, nullptr, nullptr};
