@@ -6,12 +6,14 @@ as raw pointers (torch supplies device memory and the HIP stream); every step of
 the hot path runs in the library's kernels.  Calls on a context go through ctypes;
 those around the experts, which check every tensor they are given, through a small
 extension module (_marshal).  There is no fallback: importing this package fails
-when the compiled library or the module is missing.
+when the compiled library is missing, and the calls around the experts fail when the
+module is missing or was built for another Python or torch (calls on a context need it not).
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import re
 
 import torch  # noqa: F401  (loads the HIP runtime the library links against)
 
@@ -171,7 +173,31 @@ def _load():
 
 lib = _load()
 
-from . import _marshal  # noqa: E402  (built with the library, linked against it)
+
+class _NoMarshal:
+    """In the extension module's place where it cannot be used: each of its calls says why."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the calls around the experts need the package's extension module ({self._why}): build it "
+                          "with `python routed_expert_ffn_02_amd/_build.py`")
+
+
+def _load_marshal():
+    try:
+        from . import _marshal as m  # built with the library, linked against it
+    except ImportError as e:
+        return _NoMarshal(str(e))
+    here = re.match(r"[0-9.]*[0-9]", str(torch.__version__)).group()
+    if m.torch_version != here:
+        return _NoMarshal(f"it was built for torch {m.torch_version}, this is {here}")
+    m.set_error(MoeError)
+    return m
+
+
+_marshal = _load_marshal()
 
 
 # ---------------------------------------------------------------------------
@@ -479,7 +505,6 @@ def moe_permute_noalloc(slot_idx, P: int, n_slot_range: int, perm, offsets, grou
 # from them; a tensor the library would misread (type, shape, stride, device) is refused with
 # MOE_EINVAL before anything is enqueued.  Checks and calls are in csrc/marshal.cpp.  `stream` is a
 # torch stream or a handle, by default the current stream of the tensors' device.
-_marshal.set_error(MoeError)
 
 
 def moe_dispatch_workspace(T: int, k: int, n_experts: int) -> int:

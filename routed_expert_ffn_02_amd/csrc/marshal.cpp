@@ -6,6 +6,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/api/include/torch/version.h>
 
 #include <initializer_list>
 #include <limits>
@@ -439,4 +440,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "Tensors to the C ent
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&g_module); }
+// torch_version: the torch that this was compiled against (its C++ interface has no other tag)
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&g_module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}
