@@ -507,12 +507,17 @@ def moe_permute_noalloc(slot_idx, P: int, n_slot_range: int, perm, offsets, grou
 # torch stream or a handle, by default the current stream of the tensors' device.
 
 
+def _workspace(f, *sizes: int) -> int:
+    """f's bytes for sizes; those past 32 bits are refused here (ctypes would cut them off)."""
+    n = int(f(*sizes)) if all(-2 ** 31 <= v < 2 ** 31 for v in sizes) else -1
+    if n < 0:
+        raise MoeError(MOE_EINVAL, f.__name__, "shape out of range")
+    return n
+
+
 def moe_dispatch_workspace(T: int, k: int, n_experts: int) -> int:
     """Bytes of workspace of moe_dispatch."""
-    n = int(lib.moe_dispatch_workspace(T, k, n_experts))
-    if n < 0:
-        raise MoeError(MOE_EINVAL, "moe_dispatch_workspace", "shape out of range")
-    return n
+    return _workspace(lib.moe_dispatch_workspace, T, k, n_experts)
 
 
 def moe_dispatch(topk_idx, n_experts: int, x, xs, perm, inv, offsets, ws=None, stream=None) -> None:
@@ -549,10 +554,7 @@ def moe_block_norm(h, y=None, w_post=None, gate=None, w_pre=None, h_out=None, x_
 
 def moe_block_norm_workspace(T: int, H: int) -> int:
     """Bytes of workspace of moe_block_norm_backward."""
-    n = int(lib.moe_block_norm_workspace(T, H))
-    if n < 0:
-        raise MoeError(MOE_EINVAL, "moe_block_norm_workspace", "shape out of range")
-    return n
+    return _workspace(lib.moe_block_norm_workspace, T, H)
 
 
 def moe_block_norm_backward(h_out, y, w_post, gate, w_pre, dh_out, dx, dh, dy, dw_post, dgate, dw_pre, ws=None,

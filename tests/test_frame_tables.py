@@ -1,5 +1,5 @@
-"""The int32 and fp32 tables of the token calls are aligned to their elements, or refused (on the CPU;
-pointers here are never followed)."""
+"""The int32 and fp32 tables of the token calls are aligned to their elements, or refused, and so are
+sizes past 32 bits (on the CPU; pointers here are never followed)."""
 import pytest
 
 import routed_expert_ffn_02_amd as R
@@ -28,3 +28,15 @@ def test_topk_backward(off):
     for table in (dict(z=A[0] + off), dict(idx=A[1] + off), dict(dw=A[2] + off), dict(dz=A[3] + off),
                   dict(z=A[0] + off, dz=A[0] + off)):
         assert topk(**table) == R.MOE_EINVAL
+
+
+@pytest.mark.parametrize("past", [1 << 31, 1 << 32, -(1 << 32), 1 << 63])
+def test_workspace_sizes_past_32_bits(past):
+    for f, sizes in ((R.moe_dispatch_workspace, (5000, 8, 16)), (R.moe_block_norm_workspace, (64, 128))):
+        assert f(*sizes) > 0
+        for i in range(len(sizes)):
+            with pytest.raises(R.MoeError) as e:
+                f(*[v + past * (i == j) for j, v in enumerate(sizes)])
+            assert e.value.status == R.MOE_EINVAL and f.__name__ in str(e.value)
+    with pytest.raises(R.MoeError):
+        R.moe_block_norm_workspace(4, 8193)
