@@ -716,24 +716,25 @@ extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, i
   const StreamDevice on(s);
   const uint8_t* src = static_cast<const uint8_t*>(x);
   uint8_t* dst = static_cast<uint8_t*>(xs);
+  const int width = x ? H : 1;  // H says nothing of a sort alone
   const int64_t eb = x ? fmt_bytes(fmt) : 4, pitch = ld * eb, row_bytes = x ? H * eb : 1;
   if (P <= kTinyPairs && T * ((row_bytes + 1023) / 1024) <= kTinyPieces) {
     const dim3 grid((T + 3) / 4 + 1, (unsigned)((row_bytes + 1023) / 1024)), block(256);
     const auto go = [&](auto kernel) {
-      return launch(kernel, grid, block, s, topk_idx, T, k, n_experts, src, pitch, H, dst, perm, inv, offsets);
+      return launch(kernel, grid, block, s, topk_idx, T, k, n_experts, src, pitch, width, dst, perm, inv, offsets);
     };
     if (P <= 64) return eb == 2 ? go(dispatch_tiny<2, 1>) : go(dispatch_tiny<4, 1>);
     if (P <= 256) return eb == 2 ? go(dispatch_tiny<2, 4>) : go(dispatch_tiny<4, 4>);
     return eb == 2 ? go(dispatch_tiny<2, kTinyPairs / 64>) : go(dispatch_tiny<4, kTinyPairs / 64>);
   }
   const dim3 threads(kSortThreads);
-  MoveArgs m{src, pitch, T, k, n_experts, H, dst, inv};
+  MoveArgs m{src, pitch, T, k, n_experts, width, dst, inv};
   const auto move = [&](auto find) {
     constexpr bool F = find();
     const bool nt = stream_rows(P * row_bytes);
     const auto kernel = eb == 2 ? (nt ? dispatch_move<2, F, true> : dispatch_move<2, F, false>)
                                 : (nt ? dispatch_move<4, F, true> : dispatch_move<4, F, false>);
-    return launch(kernel, dim3(T, (unsigned)((row_bytes + 4095) / 4096)), row_block(H, (int)(16 / eb)), s, m);
+    return launch(kernel, dim3(T, (unsigned)((row_bytes + 4095) / 4096)), row_block(width, (int)(16 / eb)), s, m);
   };
   if (P <= kSolePairs) {
     const dim3 chunks((unsigned)((P + kSortThreads - 1) / kSortThreads));
