@@ -221,11 +221,19 @@ struct Chunk {
 
 // ---------------------------------------------------------------- host side
 // Whether sorted rows of this many bytes pass by the caches (non-temporal loads where they
-// are read, stores where they are written): half of the 256 MB last-level cache and more,
-// where most rows have left it by the time the last is written.  At 4096 tokens, k = 8, H = 2048
-// (128 MB of bf16 rows), from memory: dispatch 27.1 us against 31.5, combine 30.8 against 33.8,
-// its gradient 56.8 against 62.2.  Of smaller rows, still in the cache when they are read, the
-// same loads cost: combine of 1024 tokens (32 MB) 10.0 us against 7.2.
+// are read, stores where they are written): half of the 256 MB last-level cache and more.  What
+// it costs and gains, in us with ordinary / non-temporal accesses, k = 8 rows of 2048 in bf16:
+//                                     48 MB         64 MB         96 MB         128 MB        192 MB
+//   rows from memory: dispatch        16.1 / 16.2   19.8 / 20.2   30.6 / 28.1   39.7 / 34.8   53.1 / 47.9
+//     combine                         10.9 / 11.7   14.2 / 15.3   24.4 / 22.1   32.0 / 29.4   46.6 / 43.1
+//     its gradient                    19.1 / 21.8   33.1 / 31.4   48.0 / 44.8   63.7 / 58.4   93.7 / 84.9
+//   rows written, then combine        26.2 / 26.2   34.6 / 33.8   53.5 / 51.3   69.8 / 65.6   103 / 101
+//   dispatch, then its rows read      31.1 / 33.4   39.8 / 42.1   58.0 / 65.6   78.8 / 84.6   118 / 121
+//   combine, then its gradient        30.3 / 33.7   41.6 / 48.0   57.7 / 70.7   77.9 / 90.8   116 / 136
+// (4 rows of 1000 in bf16 and 6 of 4096 in fp32 cross over at the same sizes but for combine, which is
+// even there from 96 MB on.)  Rows from memory gain from about 80 MB on; rows that the next
+// kernel takes from the cache lose up to 256 MB, most around 128.  The call does not know which it is:
+// the rule stands between the two.
 inline bool stream_rows(int64_t bytes) { return bytes >= (128ll << 20); }
 
 constexpr int64_t kMaxStride = 1ll << 36;  // elements between rows: byte offsets of 2^21 rows stay in 64 bits
