@@ -3,7 +3,7 @@
 //   h' = h + alpha * g * u        (g: none, one per token, or one per channel)
 //   x  = w_pre * h' / rms(h')     rms(v) = sqrt(mean(v^2) + eps)
 // and its gradient.  Memory-bound: a row is read once, kept in registers across its
-// reductions, and written once (117 MB at 4096 rows of 2048, h and y fp32, x bf16: 18.2 us, 6.5
+// reductions, and written once (117 MB at 4096 rows of 2048, h and y fp32, x bf16: 18.1 us, 6.5
 // TB/s; one row: 2.4 us, a launch and one round trip).  Statistics and all arithmetic are fp32;
 // x is formed from h' before h' is rounded to its own type, so each output is rounded once.
 #include <algorithm>
@@ -16,7 +16,7 @@ constexpr int kNormN = 8;          // elements of a lane's chunk
 constexpr int kNormMaxWaves = 16;  // of a workgroup
 // A row is one chunk per thread of one workgroup.  (With two, the gradient's rows and sums did
 // not fit the 128 registers of a 1024-thread workgroup: 165 us at 1000 rows of 16384, bf16,
-// against 28 at 8192.)
+// against 27.3 at 8192.)
 constexpr int kNormMaxH = 64 * kNormMaxWaves * kNormN;
 constexpr int kNormMaxT = 1 << 21;  // a launch of T workgroups of 1024 threads stays below 2^32
 
@@ -178,8 +178,10 @@ struct NormRows {
 // norm_reduce adds in workgroup order: no atomics, the same bits every time.  A channel gate g_c
 // and w_post share one sum, S = sum_t alpha dh y ry: dw_post = g_c S, dgate = w_post S.
 // REGULAR: every row comes in (load_all).  With up to eight wavefronts, whose threads have 256
-// registers, the next row is then loaded before the current one's sums (AHEAD): 19.9 us
-// against 27.2 at 2048 rows of 4096 in bf16.
+// registers, the next row is then loaded before the current one's sums (AHEAD): 18.9 us at 2048
+// rows of 4096 in bf16 with a channel gate, against 27.2 without.  A token gate is read behind both sums,
+// a wait per row that AHEAD does not hide: 21.0 us there.  Otherwise (an input left out) loads are
+// conditional: 17.6 us without y at that size, for 67 MB against 101.
 template <int HF, int YF, int XF, int WAVES, bool REGULAR>
 __global__ __launch_bounds__(64 * WAVES) void block_norm_backward_kernel(NormArgs a) {
   constexpr int N = kNormN;
@@ -305,8 +307,8 @@ int norm_waves(int H) { return (H + 64 * kNormN - 1) / (64 * kNormN); }
 
 // Workgroups of the gradient kernel when weights' gradients are wanted: eight wavefronts per
 // CU (of 256), in workgroups of 1 to 8, or one workgroup of up to 16.  Each leaves a partial row
-// per kind, so their number is kept low: at 2048 rows of 4096, 512 workgroups took 22.1 + 4.7 us,
-// 256 take 19.9 + 3.9.
+// per kind, so their number is kept low: at 2048 rows of 4096, 512 workgroups took 22.1 + 4.7 us
+// where 256 took 19.9 + 3.9 (18.9 + 4.0 since).
 int norm_groups(int T, int H) { return std::min(T, 256 * std::clamp(8 / norm_waves(H), 1, 4)); }
 
 template <bool BACK, int HF, int YF, int XF>

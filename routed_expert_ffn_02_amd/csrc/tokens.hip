@@ -202,7 +202,9 @@ __global__ __launch_bounds__(kSortThreads) void dispatch_scan(int32_t* __restric
   __shared__ int s_part[kSortThreads], s_base[kMaxExperts], s_wave[kSortWaves];
   const int tid = threadIdx.x, parts = min(kSortThreads / E, kScanParts), e = tid % E, part = tid / E;
   const int per = (chunks + parts - 1) / parts, c0 = part * per, c1 = part < parts ? min(c0 + per, chunks) : 0;
-  constexpr int kHold = 16;  // a column's piece stays in registers up to this length
+  // a column's piece stays in registers up to this length; beyond it (65 chunks and more of 256
+  // experts, 17 of more than 512) the rest is read twice, entry by entry the second time
+  constexpr int kHold = 16;
   int v[kHold], sum = 0;
 #pragma unroll
   for (int i = 0; i < kHold; ++i) v[i] = hist[(size_t)min(c0 + i, chunks - 1) * E + e];  // all in flight
@@ -258,7 +260,7 @@ __device__ __forceinline__ int wave_token() {
 // ---------------------------------------------------------------------------
 // Rows of x to their sorted places.  A workgroup takes one token and 4 KB of its row, 16 bytes
 // a thread, reads them once and writes them k times.  Bound by memory: 151 MB at 4096 tokens,
-// k = 8, H = 2048 in bf16 take 27.6 us (5.5 TB/s; a fill of as many bytes writes 6.6).
+// k = 8, H = 2048 in bf16 take 27.2 us (5.5 TB/s; a fill of as many bytes writes 6.6).
 // FIND: the pairs' places come from their ranks and the chunks' first places (lane j finds rank
 // j's), and the tables are written beside the rows (by the workgroup of blockIdx.y = 0);
 // otherwise from inv.  NT: stores that do not stay in the caches, see stream_rows.
@@ -400,7 +402,7 @@ __global__ __launch_bounds__(256) void dispatch_tiny(const int32_t* __restrict__
 // y[t] = sum_j w[t,j] rows[inv[t,j]] in rank order (w = nullptr: a plain sum, the gradient
 // of the move).  A workgroup takes one token and 2048 elements of its row, so that the
 // scattered rows are read in pieces of 4 KB and more (a wavefront per token and 512 elements:
-// 46 us where this takes 28.6, 168 MB at 4096 tokens, k = 8, H = 2048, bf16 to fp32: 5.9 TB/s);
+// 46 us where this takes 28.5, 168 MB at 4096 tokens, k = 8, H = 2048, bf16 to fp32: 5.9 TB/s);
 // kRanks rows are in flight per lane, more ranks go round again.  Outputs go out by
 // non-temporal stores: 33.8 us against 38.2 there with ordinary loads, and a kernel that reads y
 // next takes no longer (1024 tokens: 12.5 us for both against 15.3).
@@ -461,7 +463,7 @@ __global__ __launch_bounds__(256) void combine_rows(const uint8_t* __restrict__ 
 // The weighted return's gradient: dys[inv[t,j]] = w[t,j] dy[t], dw[t,j] = <dy[t], ys[inv[t,j]]>.
 // A workgroup takes one token and up to kRanks of its ranks, its wavefronts neighbouring
 // pieces of the row; the dot products meet in LDS in wavefront order.  Bound by memory: 297 MB at
-// 4096 tokens, k = 8, H = 2048 (dy fp32, rows bf16) take 56.0 us (5.3 TB/s); with one wavefront
+// 4096 tokens, k = 8, H = 2048 (dy fp32, rows bf16) take 56.4 us (5.3 TB/s); with one wavefront
 // 70.0, with two 74.4.
 constexpr int kCbWaves = 4;
 
@@ -534,7 +536,7 @@ __global__ __launch_bounds__(64 * kCbWaves) void combine_rows_backward(const uin
 // otherwise the first lane of an expert adds up its ranks in order.  A token's logits are
 // all read before any of its gradients is written (dlogits may be logits).  Bound by one round trip
 // to memory and three wavefront sums: 4.0 us at 4096 tokens of 256 logits, k = 8 (4.6 when every
-// token's ranks were compared one by one), 4.5 at 997 of 1000 with k = 16 (5.4; 10.5 when
+// token's ranks were compared one by one), 4.8 at 997 of 1000 with k = 16 (5.4; 10.5 when
 // every lane compared its logits with every rank).
 template <int C>  // loads of 256 logits
 __global__ __launch_bounds__(256) void topk_backward_kernel(const float* logits, int T, int E, int k,
