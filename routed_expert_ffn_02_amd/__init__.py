@@ -190,9 +190,9 @@ def _load_marshal():
         from . import _marshal as m  # built with the library, linked against it
     except ImportError as e:
         return _NoMarshal(str(e))
-    here = re.match(r"[0-9.]*[0-9]", str(torch.__version__)).group()
-    if m.torch_version != here:
-        return _NoMarshal(f"it was built for torch {m.torch_version}, this is {here}")
+    here, built = re.match(r"[0-9.]*[0-9]", str(torch.__version__)).group(), getattr(m, "torch_version", "of an earlier source")
+    if built != here:
+        return _NoMarshal(f"it was built for torch {built}, this is {here}")
     m.set_error(MoeError)
     return m
 

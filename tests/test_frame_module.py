@@ -13,7 +13,9 @@ PKG = os.path.join(ROOT, "routed_expert_ffn_02_amd")
 
 BROKEN = {"missing": "sys.modules['routed_expert_ffn_02_amd._marshal'] = None",
           "another torch": "import types; m = types.ModuleType('routed_expert_ffn_02_amd._marshal'); m.torch_version = '1.0.0'; "
-                           "sys.modules[m.__name__] = m"}
+                           "sys.modules[m.__name__] = m",
+          "an earlier module": "import types; m = types.ModuleType('routed_expert_ffn_02_amd._marshal'); "
+                               "sys.modules[m.__name__] = m"}
 
 
 @pytest.mark.parametrize("why", BROKEN)
