@@ -418,6 +418,7 @@ moe_status rmoe::block_norm(const moe_norm_config* cfg, const void* h, const voi
   a.w_pre = w_pre;
   a.h_out = static_cast<uint8_t*>(h_out);
   a.x_out = static_cast<uint8_t*>(x_out);
+  s = stream_of(s);
   const StreamDevice on(s);
   return launch_norm<false>(*cfg, a, cfg->T, s);
 }
@@ -508,7 +509,7 @@ extern "C" MOE_API moe_status moe_block_norm_backward(const moe_norm_config* cfg
     out_w.by[kinds][1] = w_post;
     a.part_post = kinds++;
   }
-  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = stream_of(stream);
   const StreamDevice on(s);
   const int G = partial ? norm_groups(cfg->T, cfg->H) : cfg->T;
   const moe_status st = launch_norm<true>(*cfg, a, G, s);

@@ -262,13 +262,21 @@ inline bool overlap(const Span& a, const Span& b) {
   return d < a.width || a.pitch - d < b.width;
 }
 
+// A caller's stream as it is handed on.  The handles that HIP reserves are no stream objects: the
+// legacy default stream's is the null stream's other name, and asking either it or the thread's own
+// for its device is left out: they belong to the current one, and hipStreamGetDevice of such a handle
+// has ended the process with a segmentation fault.
+inline hipStream_t stream_of(moe_stream_t stream) {
+  return stream == hipStreamLegacy ? nullptr : static_cast<hipStream_t>(stream);
+}
+
 // The device of `stream` made current for a launch and the caller's restored after it: a
 // stream of another device than the current one gets its kernels on its own device.
 class StreamDevice {
  public:
   explicit StreamDevice(hipStream_t s) {
     hipDevice_t dev = -1;
-    if (s == nullptr || hipStreamGetDevice(s, &dev) != hipSuccess) return;
+    if (s == nullptr || s == hipStreamPerThread || hipStreamGetDevice(s, &dev) != hipSuccess) return;
     if (hipGetDevice(&before_) != hipSuccess || before_ == dev) {
       before_ = -1;
       return;

@@ -714,7 +714,7 @@ extern "C" MOE_API moe_status moe_dispatch(const int32_t* topk_idx, int32_t T, i
     for (int b = 0; b < a; ++b)
       if (overlap(out[a], out[b])) return MOE_EINVAL;
   }
-  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = stream_of(stream);
   const StreamDevice on(s);
   const uint8_t* src = static_cast<const uint8_t*>(x);
   uint8_t* dst = static_cast<uint8_t*>(xs);
@@ -767,7 +767,7 @@ extern "C" MOE_API moe_status moe_dispatch_backward(const void* dxs, int32_t dxs
   if (!aligned_to(dxs, fmt_bytes(dxs_fmt)) || !aligned_to(dx, fmt_bytes(dx_fmt)) || !tables_aligned(inv)) return MOE_EINVAL;
   const Span out = rows_of(dx, T, H, dx_fmt, ld);
   if (overlap(out, rows_of(dxs, P, H, dxs_fmt, H)) || overlap(out, flat(inv, 4 * P))) return MOE_EINVAL;
-  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = stream_of(stream);
   const StreamDevice on(s);
   return run_combine<false>(dxs, dxs_fmt, inv, nullptr, T, k, H, dx, dx_fmt, ld, s);
 }
@@ -782,7 +782,7 @@ extern "C" MOE_API moe_status moe_combine(const void* ys, int32_t ys_fmt, const 
   const Span out = rows_of(y, T, H, y_fmt, ld);
   if (overlap(out, rows_of(ys, P, H, ys_fmt, H)) || overlap(out, flat(inv, 4 * P)) || overlap(out, flat(w, 4 * P)))
     return MOE_EINVAL;
-  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = stream_of(stream);
   const StreamDevice on(s);
   return run_combine<true>(ys, ys_fmt, inv, w, T, k, H, y, y_fmt, ld, s);
 }
@@ -803,7 +803,7 @@ extern "C" MOE_API moe_status moe_combine_backward(const void* dy, int32_t dy_fm
     for (const Span& i : in)
       if (overlap(o, i)) return MOE_EINVAL;
   if (overlap(out[0], out[1])) return MOE_EINVAL;
-  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = stream_of(stream);
   const StreamDevice on(s);
   const bool nt = stream_rows(P * H * fmt_bytes(ys_fmt));
   return by_formats(dy_fmt, ys_fmt, nt, [&](auto df, auto rf, auto n) {
@@ -824,7 +824,7 @@ extern "C" MOE_API moe_status moe_topk_backward(const float* logits, int32_t T, 
   if ((dlogits != logits && overlap(out, flat(logits, 4 * n))) || overlap(out, flat(topk_idx, 4 * P)) ||
       overlap(out, flat(dw, 4 * P)))
     return MOE_EINVAL;
-  hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipStream_t s = stream_of(stream);
   const StreamDevice on(s);
   const dim3 grid((T + 3) / 4), block(256);
   const int E = n_experts;
