@@ -177,6 +177,12 @@ class Call {
     }
     int now = -1;
     if (hipGetDevice(&now) == hipSuccess && now != device_ && hipSetDevice(device_) == hipSuccess) before_ = now;
+    // a handle's device, but for the reserved ones, which belong to the current device
+    hipDevice_t of = device_;
+    const hipStream_t h = static_cast<hipStream_t>(s);
+    if (PyLong_Check(o) && h && h != hipStreamLegacy && h != hipStreamPerThread && hipStreamGetDevice(h, &of) == hipSuccess &&
+        of != device_)
+      refuse("stream is on cuda:" + std::to_string(of) + ", tensors on cuda:" + std::to_string(device_));
     return s;
   }
 

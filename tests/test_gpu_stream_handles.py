@@ -36,3 +36,20 @@ def test_handles_of_the_tensors_device():
         got = out + tables + [dw, dz, x, dh, dwp]
         want = want or got
         assert all(torch.equal(a, b) for a, b in zip(got, want)), stream
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second device")
+def test_handles_of_another_device():
+    ys, inv, w = buffers()
+    y = torch.zeros(2, 33, device="cuda:0")
+    other = torch.cuda.Stream(device=1)
+    for stream in (other, other.cuda_stream):
+        with pytest.raises(R().MoeError, match="stream is on cuda:1"):
+            R().moe_combine(ys, inv, w, y, stream=stream)
+    want = torch.empty_like(y)
+    R().moe_combine(ys, inv, w, want)
+    with torch.cuda.device(1):              # the tensors' device counts, not the current one
+        R().moe_combine(ys, inv, w, y)
+        assert torch.cuda.current_device() == 1
+    torch.cuda.synchronize(0)
+    assert torch.equal(y, want)
