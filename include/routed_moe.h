@@ -731,6 +731,83 @@ MOE_API moe_status moe_decode_block(moe_ctx* ctx, int32_t layer, const void* x, 
                                     const moe_norm_config* norm, void* h, const float* w_post, const float* gate,
                                     const float* w_pre, void* x_next, moe_stream_t stream);
 
+/* ------------------------------------------------------------------ the experts' products
+ *
+ * The two halves of a feed-forward block over rows sorted by expert (as moe_dispatch leaves
+ * them) or over all rows with one weight (a shared expert, an adapter), and their gradients.
+ * Conventions and errors as in "around the experts" above; beside them:
+ *  - offsets: device int32 [n_experts+1], ascending in [0, rows]: expert e has the rows
+ *    [offsets[e], offsets[e+1]).  Rows that no expert has (moe_dispatch's tail) are not read, and
+ *    outputs are left as they were there.  Entries outside [0, rows] are brought into it; where a
+ *    table does not ascend, the outputs' rows are unspecified (nothing else is read or written).
+ *    NULL: one expert (n_experts = 1) of all rows.
+ *  - Sums are fp32 (matrix cores; products of bf16 are exact in them); each output is rounded once.
+ *    With bf16 operands the gradient before a projection (dgu, dz) is rounded to bf16 where it
+ *    becomes the operand of dx and dw, whatever their formats; dbias sums it unrounded.
+ *  - Limits: 1 <= rows <= 2^26, n_experts <= 1024, K and N <= 65536, strides <= 2^36, fewer than
+ *    2^24 tiles of 128 x 128 (128 x 64 in moe_glu) outputs.
+ *  - Alignment beyond the element's is not needed; operands whose rows all start on 16 bytes are
+ *    read faster.
+ */
+
+/* Activations: none; silu z s(z), s the logistic function; gelu in its tanh form,
+ * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2 } moe_act;
+
+typedef struct {
+  int32_t rows, n_experts;
+  int32_t K, N;        /* moe_glu: H and I; moe_linear: inputs and outputs */
+  int32_t fmt;         /* moe_afmt of x, w, dx, and of a, da, gu (moe_glu) or z (moe_linear) */
+  int32_t y_fmt;       /* moe_linear: of y, residual and dy (moe_glu: any, not used) */
+  int32_t dw_fmt;      /* of dw */
+  int32_t act;         /* moe_act */
+  int64_t ld_x, ld_dx; /* row strides in elements (0: dense) of x and dx */
+  int64_t ld_w, gs_w;  /* of w's rows, and from one expert's w to the next (0: dense) */
+  int64_t ld_y;        /* of a and da; of y and dy */
+  int64_t ld_residual, ld_z; /* of residual; of gu or z */
+} moe_product_config;
+
+/*
+ * The gated half, both projections, the activation and their product in one kernel:
+ *   gu = x w[e]^T,   a = act(gu[:, :I]) * gu[:, I:]      (gu in fp32, not rounded before a)
+ * x device [rows,H]; w [n_experts, 2I, H], the gate's rows then up's (gate | up of an expert record
+ * are such a block: gs_w is then the record's size); a [rows,I]; gu [rows,2I] out, or NULL.
+ */
+MOE_API moe_status moe_glu(const moe_product_config* cfg, const void* x, const void* w, const int32_t* offsets, void* a,
+                           void* gu, moe_stream_t stream);
+
+/* Bytes of workspace of moe_glu_backward; -1 for shapes out of range.  Pure host function. */
+MOE_API int64_t moe_glu_workspace(int32_t rows, int32_t n_experts, int32_t H, int32_t I, int32_t fmt);
+
+/*
+ * Its gradient from da [rows,I] and gu as stored: dgu = [da * up * act'(gate) | da * act(gate)],
+ *   dx = dgu w[e]  [rows,H],   dw[e] = dgu_e^T x_e  [n_experts, 2I, H] dense, zeros for an expert without rows.
+ * Either output may be NULL (without dx, w is not read; without dw, x is not).
+ */
+MOE_API moe_status moe_glu_backward(const moe_product_config* cfg, const void* da, const void* gu, const void* x,
+                                    const void* w, const int32_t* offsets, void* dx, void* dw, void* ws, size_t ws_bytes,
+                                    moe_stream_t stream);
+
+/*
+ * A projection with its epilogue:  z = x w[e]^T + bias[e],   y = act(z) + residual
+ * x device [rows,K]; w [n_experts, N, K]; bias fp32 [n_experts, N] or NULL; residual [rows,N] of y_fmt or
+ * NULL (may be y itself with y's stride); y [rows,N]; z [rows,N] out, or NULL.
+ */
+MOE_API moe_status moe_linear(const moe_product_config* cfg, const void* x, const void* w, const float* bias,
+                              const void* residual, const int32_t* offsets, void* y, void* z, moe_stream_t stream);
+
+/* Bytes of workspace of moe_linear_backward; -1 for shapes out of range.  Pure host function. */
+MOE_API int64_t moe_linear_workspace(int32_t rows, int32_t n_experts, int32_t K, int32_t N, int32_t fmt);
+
+/*
+ * Its gradient from dy [rows,N] and z as stored (z may be NULL without an activation): dz = dy * act'(z),
+ *   dx = dz w[e],   dw[e] = dz_e^T x_e [n_experts, N, K] dense,   dbias[e] = the sum of dz_e's rows, fp32 [n_experts, N]
+ * (zeros for an expert without rows); the residual's gradient is dy.  Any output may be NULL (not all).
+ */
+MOE_API moe_status moe_linear_backward(const moe_product_config* cfg, const void* dy, const void* z, const void* x,
+                                       const void* w, const int32_t* offsets, void* dx, void* dw, float* dbias, void* ws,
+                                       size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -93,6 +93,14 @@ class moe_norm_config(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("ld_h", "ld_y", "ld_x")]
 
 
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU = 0, 1, 2
+
+
+class moe_product_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "n_experts", "K", "N", "fmt", "y_fmt", "dw_fmt", "act")] + [
+        (n, ctypes.c_int64) for n in ("ld_x", "ld_dx", "ld_w", "gs_w", "ld_y", "ld_residual", "ld_z")]
+
+
 class moe_bank_header(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_layers", "n_experts", "hidden", "inter", "wfmt", "pad")] + [
         ("record_bytes", ctypes.c_int64), ("n_records", ctypes.c_int64)]
@@ -162,6 +170,12 @@ def _load():
         "moe_block_norm_backward": (I32, [ctypes.POINTER(moe_norm_config)] + [VP] * 13 + [ctypes.c_size_t, VP]),
         "moe_decode_block": (I32, [P, I32, VP, I32, VP, VP, VP, VP, VP, ctypes.POINTER(moe_norm_config), VP, VP, VP,
                                    VP, VP, VP]),
+        "moe_glu": (I32, [ctypes.POINTER(moe_product_config)] + [VP] * 6),
+        "moe_glu_workspace": (I64, [I32] * 5),
+        "moe_glu_backward": (I32, [ctypes.POINTER(moe_product_config)] + [VP] * 8 + [ctypes.c_size_t, VP]),
+        "moe_linear": (I32, [ctypes.POINTER(moe_product_config)] + [VP] * 8),
+        "moe_linear_workspace": (I64, [I32] * 5),
+        "moe_linear_backward": (I32, [ctypes.POINTER(moe_product_config)] + [VP] * 9 + [ctypes.c_size_t, VP]),
         "moe_pool_load": (I32, [P, ctypes.c_char_p, I32, ctypes.POINTER(VP), ctypes.POINTER(moe_bank_stats)]),
     }
     for name, (res, args) in sig.items():
@@ -574,3 +588,43 @@ def moe_decode_block(ctx: Ctx, layer, x, T, logit_bias, topk_idx, topk_w, slot_i
     _check(ctx, lib.moe_decode_block(ctx.handle, layer, _ptr(x), T, _ptr(logit_bias), _ptr(topk_idx), _ptr(topk_w),
                                      _ptr(slot_idx), _ptr(y), ctypes.byref(norm), _ptr(h), _ptr(w_post), _ptr(gate),
                                      _ptr(w_pre), _ptr(x_next), _stream(stream)), "moe_decode_block")
+
+
+# ---------------------------------------------------------------------------
+# The experts' products: tensors as above.  x [rows, K] and its like may have gaps between rows; w is
+# [n_experts, n, k] (or [n, k]) with contiguous rows at any strides, such as a view of expert records; dw is
+# dense.  offsets is moe_dispatch's [n_experts + 1] table, or None with one expert.
+
+
+def moe_glu(x, w, a, gu=None, offsets=None, act: int = MOE_ACT_SILU, stream=None) -> None:
+    """a [rows, I] = act(gate) * up, gate | up = x w^T of each row's expert, w [n_experts, 2I, H] (gate rows, then
+    up's); gu [rows, 2I] receives gate | up for the gradient."""
+    _marshal.glu(x, w, a, gu, offsets, act, stream)
+
+
+def moe_glu_workspace(rows: int, n_experts: int, H: int, I: int, fmt: int) -> int:
+    """Bytes of workspace of moe_glu_backward (fmt: MOE_AFMT_* of its tensors)."""
+    return _workspace(lib.moe_glu_workspace, rows, n_experts, H, I, fmt)
+
+
+def moe_glu_backward(da, gu, x, w, dx, dw, ws, offsets=None, act: int = MOE_ACT_SILU, stream=None) -> None:
+    """From da [rows, I] and gu as moe_glu stored it: dx [rows, H] (or None, then w may be) and
+    dw [n_experts, 2I, H] (or None, then x may be)."""
+    _marshal.glu_backward(da, gu, x, w, dx, dw, ws, offsets, act, stream)
+
+
+def moe_linear(x, w, y, bias=None, residual=None, z=None, offsets=None, act: int = MOE_ACT_NONE, stream=None) -> None:
+    """y [rows, N] = act(z) + residual, z = x w^T + bias of each row's expert, w [n_experts, N, K], bias fp32
+    [n_experts, N]; z [rows, N] receives z for the gradient.  residual may be y."""
+    _marshal.linear(x, w, y, bias, residual, z, offsets, act, stream)
+
+
+def moe_linear_workspace(rows: int, n_experts: int, K: int, N: int, fmt: int) -> int:
+    """Bytes of workspace of moe_linear_backward (fmt: MOE_AFMT_* of x and w)."""
+    return _workspace(lib.moe_linear_workspace, rows, n_experts, K, N, fmt)
+
+
+def moe_linear_backward(dy, z, x, w, dx, dw, dbias, ws, offsets=None, act: int = MOE_ACT_NONE, stream=None) -> None:
+    """From dy [rows, N] and, with an activation, z as moe_linear stored it: dx [rows, K] (or None, then w may be),
+    dw [n_experts, N, K] (or None, then x may be), dbias fp32 [n_experts, N] (or None)."""
+    _marshal.linear_backward(dy, z, x, w, dx, dw, dbias, ws, offsets, act, stream)

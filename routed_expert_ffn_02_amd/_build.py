@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libroutedmoe.so")
 MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = os.environ.get("RMOE_OFFLOAD_ARCH", "gfx950")
 
-HIP_SOURCES = ["route.hip", "lookup.hip", "decode.hip", "prefill.hip", "fill.hip", "tokens.hip", "norm.hip"]
+HIP_SOURCES = ["route.hip", "lookup.hip", "decode.hip", "prefill.hip", "fill.hip", "tokens.hip", "norm.hip", "experts.hip"]
 CPP_SOURCES = ["runtime.cpp", "cpu_ffn.cpp", "placement.cpp", "bank.cpp"]
 MARSHAL_SOURCE = "marshal.cpp"
 

@@ -1,0 +1,405 @@
+// The experts' products over rows sorted by expert, and their gradients: the gated half of a
+// feed-forward block (both projections, activation and product in one kernel), a projection with
+// bias, activation and residual, for experts and shared experts that run outside a context.
+//
+//   glu      gu = x W^T, a = act(gu_gate) gu_up          dgu = [da u act'(g) | da act(g)], dx = dgu W, dW = dgu^T x
+//   linear   z = x W^T + b, y = act(z) + r               dz = dy act'(z), dx = dz W, dW = dz^T x, db = sum dz
+//
+// The products are tiles on the matrix cores (products.hpp).
+#include "products.hpp"
+
+namespace rmoe {
+
+constexpr int kProductMaxRows = 1 << 26;
+constexpr int kProductMaxSize = 1 << 16;  // of a row of x, of the outputs
+
+// ---------------------------------------------------------------- the gradient before the projection
+// d = dgu (glu) or dz (linear), rounded to the operands' type: the products that follow take it as
+// an operand, as autograd's do.  Eight elements a lane; rows behind the last expert's are left out.
+template <bool GLU>
+__global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
+                                                           const void* __restrict__ z, int fmt, int64_t ld_z,
+                                                           const int32_t* __restrict__ offsets, int rows, int E, int n,
+                                                           int act, void* __restrict__ d, int64_t ld_d) {
+  const int c = 8 * (blockIdx.y * 64 + (threadIdx.x & 63));
+  const int end = offsets ? min(max(offsets[E], 0), rows) : rows;
+  if (c >= n) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = blockIdx.x * 8 + 4 * i + (threadIdx.x >> 6);
+    if (row >= end) return;
+    float g[8], v[8];
+    read8(dy, (int64_t)row * ld_dy + c, dy_fmt, n - c, v);
+    if constexpr (GLU) {
+      float u[8];
+      read8(z, (int64_t)row * ld_z + c, fmt, n - c, g);
+      read8(z, (int64_t)row * ld_z + n + c, fmt, n - c, u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const Act f = act_of(g[e], act);
+        g[e] = v[e] * u[e] * f.grad;
+        v[e] *= f.value;
+      }
+      write8(d, (int64_t)row * ld_d + c, fmt, n - c, g);
+      write8(d, (int64_t)row * ld_d + n + c, fmt, n - c, v);
+    } else {
+      if (act != MOE_ACT_NONE) {
+        read8(z, (int64_t)row * ld_z + c, fmt, n - c, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= act_of(g[e], act).grad;
+      }
+      write8(d, (int64_t)row * ld_d + c, fmt, n - c, v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the bias's gradient
+// Column sums of dz in fp32, from dy and z as given (dz is not rounded here).  A workgroup has 64
+// columns, eight lanes of eight, and 128 rows at once; its rows' sums meet in LDS in a fixed
+// order.  Splits of a long expert write their own sums, which bias_join adds in order.
+constexpr int kBiasRows = 512;  // rows of a split, about
+
+__global__ __launch_bounds__(1024) void bias_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
+                                                             const void* __restrict__ z, int fmt, int64_t ld_z,
+                                                             const int32_t* __restrict__ offsets, int rows, int E, int n,
+                                                             int act, int splits, float* __restrict__ out) {
+  __shared__ float part[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = 64 * blockIdx.x + 8 * (lane & 7);
+  const Range r = expert_rows(offsets, blockIdx.y, rows);
+  const int len = (r.n + splits - 1) / splits, from = min(r.n, (int)blockIdx.z * len), to = min(r.n, from + len);
+  float sum[8] = {};
+  if (c < n) {
+#pragma unroll 2
+    for (int i = from + 8 * wave + (lane >> 3); i < to; i += 128) {
+      float v[8], g[8];
+      read8(dy, (int64_t)(r.first + i) * ld_dy + c, dy_fmt, n - c, v);
+      if (act != MOE_ACT_NONE) {
+        read8(z, (int64_t)(r.first + i) * ld_z + c, fmt, n - c, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= act_of(g[e], act).grad;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += v[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int o = 8; o < 64; o <<= 1) sum[e] += __shfl_xor(sum[e], o);
+    if (lane < 8) part[wave][8 * lane + e] = sum[e];
+  }
+  __syncthreads();
+  const int col = 64 * blockIdx.x + threadIdx.x;
+  if (threadIdx.x >= 64 || col >= n) return;
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += part[w][threadIdx.x];
+  out[((int64_t)blockIdx.z * E + blockIdx.y) * n + col] = s;
+}
+
+__global__ __launch_bounds__(256) void bias_join_kernel(const float* __restrict__ part, int64_t total, int splits,
+                                                        float* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < splits; ++k) s += part[k * total + i];
+  out[i] = s;
+}
+
+namespace {
+
+int bias_splits(int64_t rows, int E) {
+  return (int)std::clamp<int64_t>(rows / ((int64_t)E * kBiasRows), 1, 64);
+}
+
+// ---------------------------------------------------------------- launches
+constexpr int64_t kMaxBlocks = (1ll << 32) / 256 - 1;  // a launch's threads are counted in 32 bits
+
+template <typename E, int OP>
+moe_status product_of(const ProductArgs& p, hipStream_t s) {
+  constexpr int BM = 128, BN = 128;
+  using T = ProductTile<E, OP, BM, BN, 64, 64>;
+  const int64_t nt = (p.N + T::kCols - 1) / T::kCols;
+  // row tiles: every expert with a row may end in a part of one
+  const int64_t mt = OP == OP_DW ? (int64_t)p.E * ((p.M + BM - 1) / BM)
+                                 : ((int64_t)p.rows + (int64_t)std::min(p.E, p.rows) * (BM - 1)) / BM;
+  const int64_t blocks = (mt * nt + 7) / 8 * 8;
+  if (blocks > kMaxBlocks) return MOE_EINVAL;
+  return launch(product_kernel<E, OP, BM, BN, 64, 64>, dim3((unsigned)blocks), dim3(T::kThreads), s, p);
+}
+template <int OP>
+moe_status product(int fmt, const ProductArgs& p, hipStream_t s) {
+  return fmt == MOE_AFMT_BF16 ? product_of<uint16_t, OP>(p, s) : product_of<float, OP>(p, s);
+}
+
+// ---------------------------------------------------------------- checks
+struct Dims {
+  int64_t ld_x, ld_dx, ld_w, gs_w, ld_y, ld_dy, ld_r, ld_z;
+  int wrows, zcols;  // rows of an expert's weights; columns of gu or z
+};
+
+int64_t stride_of(int64_t ld, int64_t n) { return ld == 0 ? n : (ld >= n && ld <= kMaxStride ? ld : -1); }
+
+bool dims_ok(const moe_product_config* c, bool glu, bool offsets, Dims& d) {
+  if (!c || c->rows < 1 || c->rows > kProductMaxRows || c->n_experts < 1 || c->n_experts > kMaxExperts) return false;
+  if (c->K < 1 || c->K > kProductMaxSize || c->N < 1 || c->N > kProductMaxSize) return false;
+  if (!offsets && c->n_experts != 1) return false;
+  if (!fmt_ok(c->fmt) || !fmt_ok(c->y_fmt) || !fmt_ok(c->dw_fmt)) return false;
+  if (c->act < MOE_ACT_NONE || c->act > MOE_ACT_GELU) return false;
+  d.wrows = glu ? 2 * c->N : c->N;
+  d.zcols = d.wrows;
+  d.ld_x = stride_of(c->ld_x, c->K);
+  d.ld_dx = stride_of(c->ld_dx, c->K);
+  d.ld_w = stride_of(c->ld_w, c->K);
+  if (d.ld_w < 0) return false;
+  const int64_t dense = (int64_t)d.wrows * d.ld_w;
+  d.gs_w = c->gs_w == 0 ? dense : c->gs_w;
+  d.ld_y = stride_of(c->ld_y, c->N);
+  d.ld_r = stride_of(c->ld_residual, c->N);
+  d.ld_z = stride_of(c->ld_z, d.zcols);
+  if (d.ld_x < 0 || d.ld_dx < 0 || d.ld_y < 0 || d.ld_r < 0 || d.ld_z < 0) return false;
+  // experts' weights lie apart, and the last one's end is an address of 2^46 elements at most
+  return d.gs_w >= (int64_t)(d.wrows - 1) * d.ld_w + c->K && d.gs_w <= kMaxStride;
+}
+
+Span matrix(const void* p, int64_t rows, int64_t n, int fmt, int64_t ld) {
+  return {p, rows, n * fmt_bytes(fmt), ld * fmt_bytes(fmt)};
+}
+// The experts' weights: one block where their rows are evenly spaced, else from the first to the last.
+Span weights(const void* w, const moe_product_config* c, const Dims& d) {
+  if (c->n_experts == 1 || d.gs_w == (int64_t)d.wrows * d.ld_w)
+    return matrix(w, (int64_t)c->n_experts * d.wrows, c->K, c->fmt, d.ld_w);
+  return flat(w, ((int64_t)(c->n_experts - 1) * d.gs_w + (int64_t)(d.wrows - 1) * d.ld_w + c->K) * fmt_bytes(c->fmt));
+}
+
+template <size_t I, size_t O>
+bool apart(const Span (&in)[I], const Span (&out)[O]) {
+  for (size_t o = 0; o < O; ++o) {
+    for (const Span& i : in)
+      if (overlap(out[o], i)) return false;
+    for (size_t q = 0; q < o; ++q)
+      if (overlap(out[o], out[q])) return false;
+  }
+  return true;
+}
+
+template <typename... P>
+bool all_aligned(int64_t to, const P*... p) { return (aligned_to(p, to) && ...); }
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// The workspace: 15 bytes to reach an alignment of 16, d, the bias's partial sums.
+struct Workspace {
+  int64_t ld_d, d, bias, bytes;  // elements; offsets and size in bytes
+};
+Workspace workspace_of(int64_t rows, int E, int64_t n, int64_t bias_n, int fmt) {
+  Workspace w;
+  w.ld_d = up(n, 8);
+  w.d = 0;
+  w.bias = up(rows * w.ld_d * fmt_bytes(fmt), 16);
+  const int splits = bias_splits(rows, E);
+  w.bytes = 15 + w.bias + (bias_n && splits > 1 ? 4 * (int64_t)splits * E * bias_n : 0);
+  return w;
+}
+bool sizes_ok(int32_t rows, int32_t E, int32_t K, int32_t N, int32_t fmt) {
+  return rows >= 1 && rows <= kProductMaxRows && E >= 1 && E <= kMaxExperts && K >= 1 && K <= kProductMaxSize && N >= 1 &&
+         N <= kProductMaxSize && fmt_ok(fmt);
+}
+uint8_t* base_of(void* ws) { return reinterpret_cast<uint8_t*>(((uintptr_t)ws + 15) & ~(uintptr_t)15); }
+
+// dx = d W and dW = d^T x, each where it is asked for.
+moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz, int64_t ld_dz, const void* x, const void* w,
+                     const int32_t* offsets, void* dx, void* dw, hipStream_t s) {
+  ProductArgs p{};
+  p.a = dz;
+  p.lda = ld_dz;
+  p.offsets = offsets;
+  p.rows = c->rows;
+  p.E = c->n_experts;
+  if (dx) {
+    p.b = w;
+    p.ldb = d.ld_w;
+    p.gsb = d.gs_w;
+    p.K = d.wrows;
+    p.N = c->K;
+    p.out = dx;
+    p.ldo = d.ld_dx;
+    p.out_fmt = c->fmt;
+    const moe_status st = product<OP_DX>(c->fmt, p, s);
+    if (st != MOE_OK) return st;
+  }
+  if (dw) {
+    p.b = x;
+    p.ldb = d.ld_x;
+    p.M = d.wrows;
+    p.N = c->K;
+    p.out = dw;
+    p.out_fmt = c->dw_fmt;
+    return product<OP_DW>(c->fmt, p, s);
+  }
+  return MOE_OK;
+}
+
+template <bool GLU>
+moe_status pre_gradient(const moe_product_config* c, const Dims& d, const void* dy, int dy_fmt, const void* z,
+                        const int32_t* offsets, void* out, int64_t ld_d, hipStream_t s) {
+  const dim3 grid((unsigned)((c->rows + 7) / 8), (unsigned)((c->N + 511) / 512));
+  return launch(pre_gradient_kernel<GLU>, grid, dim3(256), s, dy, dy_fmt, d.ld_y, z, c->fmt, d.ld_z, offsets, c->rows,
+                c->n_experts, c->N, c->act, out, ld_d);
+}
+
+}  // namespace
+}  // namespace rmoe
+
+using namespace rmoe;
+
+extern "C" MOE_API moe_status moe_glu(const moe_product_config* cfg, const void* x, const void* w, const int32_t* offsets,
+                                      void* a, void* gu, moe_stream_t stream) {
+  Dims d;
+  if (!x || !w || !a || !dims_ok(cfg, true, offsets, d)) return MOE_EINVAL;
+  const int64_t eb = fmt_bytes(cfg->fmt), R = cfg->rows;
+  if (!all_aligned(eb, x, w, a, gu) || !aligned_to(offsets, 4)) return MOE_EINVAL;
+  const Span in[3] = {matrix(x, R, cfg->K, cfg->fmt, d.ld_x), weights(w, cfg, d), flat(offsets, 4 * (cfg->n_experts + 1ll))};
+  const Span out[2] = {matrix(a, R, cfg->N, cfg->fmt, d.ld_y), matrix(gu, R, d.zcols, cfg->fmt, d.ld_z)};
+  if (!apart(in, out)) return MOE_EINVAL;
+  ProductArgs p{};
+  p.a = x;
+  p.lda = d.ld_x;
+  p.b = w;
+  p.ldb = d.ld_w;
+  p.gsb = d.gs_w;
+  p.offsets = offsets;
+  p.rows = cfg->rows;
+  p.E = cfg->n_experts;
+  p.K = cfg->K;
+  p.N = cfg->N;
+  p.act = cfg->act;
+  p.out = a;
+  p.ldo = d.ld_y;
+  p.out_fmt = cfg->fmt;
+  p.aux = gu;
+  p.ld_aux = d.ld_z;
+  const hipStream_t s = stream_of(stream);
+  const StreamDevice on(s);
+  return product<OP_GLU>(cfg->fmt, p, s);
+}
+
+extern "C" MOE_API int64_t moe_glu_workspace(int32_t rows, int32_t n_experts, int32_t H, int32_t I, int32_t fmt) {
+  if (!sizes_ok(rows, n_experts, H, I, fmt)) return -1;
+  return workspace_of(rows, n_experts, 2ll * I, 0, fmt).bytes;
+}
+
+extern "C" MOE_API moe_status moe_glu_backward(const moe_product_config* cfg, const void* da, const void* gu, const void* x,
+                                               const void* w, const int32_t* offsets, void* dx, void* dw, void* ws,
+                                               size_t ws_bytes, moe_stream_t stream) {
+  Dims d;
+  if (!da || !gu || (!dx && !dw) || (dx && !w) || (dw && !x) || !ws || !dims_ok(cfg, true, offsets, d)) return MOE_EINVAL;
+  const int64_t eb = fmt_bytes(cfg->fmt), R = cfg->rows;
+  const Workspace k = workspace_of(R, cfg->n_experts, 2ll * cfg->N, 0, cfg->fmt);
+  if (ws_bytes < (size_t)k.bytes) return MOE_EINVAL;
+  if (!all_aligned(eb, da, gu, dx ? w : nullptr, dw ? x : nullptr, dx) || !aligned_to(dw, fmt_bytes(cfg->dw_fmt)) ||
+      !aligned_to(offsets, 4))
+    return MOE_EINVAL;
+  const Span none = flat(nullptr, 0);
+  const Span in[5] = {matrix(da, R, cfg->N, cfg->fmt, d.ld_y), matrix(gu, R, d.zcols, cfg->fmt, d.ld_z),
+                      dw ? matrix(x, R, cfg->K, cfg->fmt, d.ld_x) : none, dx ? weights(w, cfg, d) : none,
+                      flat(offsets, 4 * (cfg->n_experts + 1ll))};
+  const Span out[3] = {matrix(dx, R, cfg->K, cfg->fmt, d.ld_dx),
+                       flat(dw, (int64_t)cfg->n_experts * d.wrows * cfg->K * fmt_bytes(cfg->dw_fmt)), flat(ws, k.bytes)};
+  if (!apart(in, out)) return MOE_EINVAL;
+  const hipStream_t s = stream_of(stream);
+  const StreamDevice on(s);
+  uint8_t* const dgu = base_of(ws) + k.d;
+  const moe_status st = pre_gradient<true>(cfg, d, da, cfg->fmt, gu, offsets, dgu, k.ld_d, s);
+  return st == MOE_OK ? gradients(cfg, d, dgu, k.ld_d, x, w, offsets, dx, dw, s) : st;
+}
+
+extern "C" MOE_API moe_status moe_linear(const moe_product_config* cfg, const void* x, const void* w, const float* bias,
+                                         const void* residual, const int32_t* offsets, void* y, void* z,
+                                         moe_stream_t stream) {
+  Dims d;
+  if (!x || !w || !y || !dims_ok(cfg, false, offsets, d)) return MOE_EINVAL;
+  const int64_t eb = fmt_bytes(cfg->fmt), yb = fmt_bytes(cfg->y_fmt), R = cfg->rows;
+  if (!all_aligned(eb, x, w, z) || !all_aligned(yb, y, residual) || !all_aligned(4, offsets, bias)) return MOE_EINVAL;
+  const Span none = flat(nullptr, 0);
+  // (y may take the residual's place: each element is read by the lane that writes it)
+  const bool in_place = residual == y && d.ld_r == d.ld_y;
+  const Span in[5] = {matrix(x, R, cfg->K, cfg->fmt, d.ld_x), weights(w, cfg, d), flat(offsets, 4 * (cfg->n_experts + 1ll)),
+                      flat(bias, 4ll * cfg->n_experts * cfg->N),
+                      in_place ? none : matrix(residual, R, cfg->N, cfg->y_fmt, d.ld_r)};
+  const Span out[2] = {matrix(y, R, cfg->N, cfg->y_fmt, d.ld_y), matrix(z, R, cfg->N, cfg->fmt, d.ld_z)};
+  if (!apart(in, out)) return MOE_EINVAL;
+  ProductArgs p{};
+  p.a = x;
+  p.lda = d.ld_x;
+  p.b = w;
+  p.ldb = d.ld_w;
+  p.gsb = d.gs_w;
+  p.offsets = offsets;
+  p.rows = cfg->rows;
+  p.E = cfg->n_experts;
+  p.K = cfg->K;
+  p.N = cfg->N;
+  p.act = cfg->act;
+  p.out = y;
+  p.ldo = d.ld_y;
+  p.out_fmt = cfg->y_fmt;
+  p.aux = z;
+  p.ld_aux = d.ld_z;
+  p.residual = residual;
+  p.ld_res = d.ld_r;
+  p.bias = bias;
+  const hipStream_t s = stream_of(stream);
+  const StreamDevice on(s);
+  return product<OP_LINEAR>(cfg->fmt, p, s);
+}
+
+extern "C" MOE_API int64_t moe_linear_workspace(int32_t rows, int32_t n_experts, int32_t K, int32_t N, int32_t fmt) {
+  if (!sizes_ok(rows, n_experts, K, N, fmt)) return -1;
+  return workspace_of(rows, n_experts, N, N, fmt).bytes;
+}
+
+extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg, const void* dy, const void* z, const void* x,
+                                                  const void* w, const int32_t* offsets, void* dx, void* dw, float* dbias,
+                                                  void* ws, size_t ws_bytes, moe_stream_t stream) {
+  Dims d;
+  if (!dy || (!dx && !dw && !dbias) || (dx && !w) || (dw && !x) || !ws || !dims_ok(cfg, false, offsets, d)) return MOE_EINVAL;
+  if (cfg->act != MOE_ACT_NONE && !z) return MOE_EINVAL;
+  const int64_t eb = fmt_bytes(cfg->fmt), R = cfg->rows;
+  const Workspace k = workspace_of(R, cfg->n_experts, cfg->N, cfg->N, cfg->fmt);
+  if (ws_bytes < (size_t)k.bytes) return MOE_EINVAL;
+  const bool zs = cfg->act != MOE_ACT_NONE;
+  if (!all_aligned(eb, zs ? z : nullptr, dx ? w : nullptr, dw ? x : nullptr, dx) || !aligned_to(dy, fmt_bytes(cfg->y_fmt)) ||
+      !aligned_to(dw, fmt_bytes(cfg->dw_fmt)) || !all_aligned(4, offsets, dbias))
+    return MOE_EINVAL;
+  const Span none = flat(nullptr, 0);
+  const Span in[5] = {matrix(dy, R, cfg->N, cfg->y_fmt, d.ld_y), zs ? matrix(z, R, cfg->N, cfg->fmt, d.ld_z) : none,
+                      dw ? matrix(x, R, cfg->K, cfg->fmt, d.ld_x) : none, dx ? weights(w, cfg, d) : none,
+                      flat(offsets, 4 * (cfg->n_experts + 1ll))};
+  const Span out[4] = {matrix(dx, R, cfg->K, cfg->fmt, d.ld_dx),
+                       flat(dw, (int64_t)cfg->n_experts * cfg->N * cfg->K * fmt_bytes(cfg->dw_fmt)),
+                       flat(dbias, 4ll * cfg->n_experts * cfg->N), flat(ws, k.bytes)};
+  if (!apart(in, out)) return MOE_EINVAL;
+  const hipStream_t s = stream_of(stream);
+  const StreamDevice on(s);
+  uint8_t* const base = base_of(ws);
+  moe_status st = MOE_OK;
+  if (dbias) {
+    const int splits = bias_splits(R, cfg->n_experts);
+    float* const part = splits > 1 ? reinterpret_cast<float*>(base + k.bias) : dbias;
+    st = launch(bias_gradient_kernel, dim3((cfg->N + 63) / 64, cfg->n_experts, splits), dim3(1024), s, dy, cfg->y_fmt, d.ld_y,
+                z, cfg->fmt, d.ld_z, offsets, cfg->rows, cfg->n_experts, cfg->N, cfg->act, splits, part);
+    if (st == MOE_OK && splits > 1) {
+      const int64_t total = (int64_t)cfg->n_experts * cfg->N;
+      st = launch(bias_join_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), s, part, total, splits, dbias);
+    }
+    if (st != MOE_OK) return st;
+  }
+  if (!dx && !dw) return st;
+  // dy itself where nothing changes it, else dz in the operands' type
+  if (!zs && cfg->y_fmt == cfg->fmt) return gradients(cfg, d, dy, d.ld_y, x, w, offsets, dx, dw, s);
+  st = pre_gradient<false>(cfg, d, dy, cfg->y_fmt, z, offsets, base + k.d, k.ld_d, s);
+  return st == MOE_OK ? gradients(cfg, d, base + k.d, k.ld_d, x, w, offsets, dx, dw, s) : st;
+}

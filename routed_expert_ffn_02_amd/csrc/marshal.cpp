@@ -1,5 +1,5 @@
-// Torch tensors to the C entry points around the experts (moe_dispatch ... moe_block_norm_backward):
-// checks of type, shape, stride and device, the current stream, and the call.  A Python
+// Torch tensors to the C entry points around the experts (moe_dispatch ... moe_block_norm_backward) and
+// of their products (moe_glu ... moe_linear_backward): checks of type, shape, stride and device, the current stream, and the call.  A Python
 // extension module, since those checks in Python cost more than the launch they precede
 // (0.4 us a tensor, 4 to 14 tensors a call, against 3 us): nothing is computed here.
 #include <hip/hip_runtime_api.h>
@@ -126,6 +126,51 @@ class Call {
     const bool dense = t.numel() == (int64_t)T * H && t.is_contiguous() && (T == 1 || ld == 0 || ld == H);
     if (!matrix && !dense)
       refuse(std::string(name) + " has shape " + shape_text(t.sizes()) + " or strides that are not norm's");
+  }
+
+  // Weights [E, n, k] (or [n, k]: E = 1) whose rows of k are contiguous; all zero for None.
+  struct Weights {
+    void* p = nullptr;
+    int32_t fmt = MOE_AFMT_F32, e = 0, n = 0, k = 0;
+    int64_t ld = 0, gs = 0;
+  };
+  Weights weights(PyObject* o, const char* name) {
+    if (o == Py_None) return {};
+    const at::Tensor& t = tensor(o, name);
+    const auto type = t.scalar_type();
+    if ((t.dim() != 2 && t.dim() != 3) || (type != at::kFloat && type != at::kBFloat16))
+      refuse(std::string(name) + " must be a two- or three-dimensional fp32 or bf16 tensor");
+    const int64_t d = t.dim(), e = d == 3 ? t.size(0) : 1, n = t.size(d - 2), k = t.size(d - 1);
+    constexpr int64_t most = std::numeric_limits<int32_t>::max();
+    if (e < 1 || n < 1 || k < 1 || e > most || n > most || k > most)
+      refuse(std::string(name) + " has shape " + shape_text(t.sizes()) + ": no size may be 0");
+    const int64_t ld = n == 1 ? k : t.stride(d - 2), gs = e == 1 ? 0 : t.stride(0);
+    if ((t.stride(d - 1) != 1 && k > 1) || ld < k || (e > 1 && gs < 1))
+      refuse(std::string(name) + " needs contiguous rows, and experts one after the other");
+    return {t.data_ptr(), type == at::kBFloat16 ? MOE_AFMT_BF16 : MOE_AFMT_F32, (int32_t)e, (int32_t)n, (int32_t)k, ld, gs};
+  }
+  // Their gradient: e * n * k elements without gaps, of either type; nullptr for None.
+  void* weights_gradient(PyObject* o, const char* name, int64_t e, int64_t n, int64_t k, int32_t* fmt) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, name);
+    const auto type = t.scalar_type();
+    const int64_t d = t.dim();
+    if ((type != at::kFloat && type != at::kBFloat16) || !t.is_contiguous())
+      refuse(std::string(name) + " must be a contiguous fp32 or bf16 tensor");
+    if ((d != 3 && !(d == 2 && e == 1)) || (d == 3 && t.size(0) != e) || t.size(d - 2) != n || t.size(d - 1) != k)
+      refuse(std::string(name) + " has shape " + shape_text(t.sizes()) + ", not " + shape_text({e, n, k}));
+    *fmt = type == at::kBFloat16 ? MOE_AFMT_BF16 : MOE_AFMT_F32;
+    return t.data_ptr();
+  }
+  // The experts' table of rows [E + 1] and E; E = 1 for None.
+  const int32_t* offsets(PyObject* o, int32_t* e) {
+    *e = 1;
+    if (o == Py_None) return nullptr;
+    const at::Tensor& t = tensor(o, "offsets");
+    if (t.dim() != 1 || t.size(0) < 2 || t.size(0) > std::numeric_limits<int32_t>::max())
+      refuse("offsets must be an int32 tensor [experts + 1]");
+    *e = (int32_t)(t.size(0) - 1);
+    return need_flat<int32_t>(o, "offsets", at::kInt, {t.size(0)});
   }
 
   // An int32 table [T, k].
@@ -430,6 +475,178 @@ PyObject* check_block(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+void same_type(int32_t a, int32_t b, const char* name) {
+  if (a != b) refuse(std::string(name) + " must have the operands' type");
+}
+void want_weights(const Call::Weights& w, int32_t e, int64_t n, int32_t k) {
+  if (w.e != e || w.n != n || (k && w.k != k))
+    refuse("w has shape " + shape_text({w.e, w.n, w.k}) + ", not " + shape_text({e, n, k ? k : w.k}));
+}
+
+// (x, w, a, gu, offsets, act, stream)
+PyObject* glu(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<7>("moe_glu", args, n, [](PyObject* const* a) {
+    Call c;
+    int32_t E;
+    const Rows x = c.need_rows(a[0], "x", {});
+    const Call::Weights w = c.weights(a[1], "w");
+    if (!w.p) refuse("w must be a tensor");
+    const int32_t* off = c.offsets(a[4], &E);
+    const Rows o = c.need_rows(a[2], "a", {x.n});
+    want_weights(w, E, 2ll * o.h, x.h);
+    const Rows gu = c.rows(a[3], "gu", {x.n, 2ll * o.h});
+    same_type(w.fmt, x.fmt, "w");
+    same_type(o.fmt, x.fmt, "a");
+    if (gu.p) same_type(gu.fmt, x.fmt, "gu");
+    moe_product_config cfg{};
+    cfg.rows = x.n;
+    cfg.n_experts = E;
+    cfg.K = x.h;
+    cfg.N = o.h;
+    cfg.fmt = cfg.y_fmt = cfg.dw_fmt = x.fmt;
+    cfg.act = int_arg(a[5], "act");
+    cfg.ld_x = x.ld;
+    cfg.ld_w = w.ld;
+    cfg.gs_w = w.gs;
+    cfg.ld_y = o.ld;
+    cfg.ld_z = gu.ld;
+    const moe_stream_t s = c.stream(a[6]);
+    return unlocked([&] { return moe_glu(&cfg, x.p, w.p, off, o.p, gu.p, s); });
+  });
+}
+
+// (da, gu, x, w, dx, dw, ws, offsets, act, stream)
+PyObject* glu_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<10>("moe_glu_backward", args, n, [](PyObject* const* a) {
+    Call c;
+    int32_t E;
+    const Rows da = c.need_rows(a[0], "da", {});
+    const Rows gu = c.need_rows(a[1], "gu", {da.n, 2ll * da.h});
+    const int32_t* off = c.offsets(a[7], &E);
+    same_type(gu.fmt, da.fmt, "gu");
+    const Rows dx = c.rows(a[4], "dx", {da.n});
+    Call::Weights w;
+    if (dx.p) {
+      w = c.weights(a[3], "w");
+      if (!w.p) refuse("dx needs w");
+      want_weights(w, E, 2ll * da.h, dx.h);
+      same_type(dx.fmt, da.fmt, "dx");
+      same_type(w.fmt, da.fmt, "w");
+    }
+    Rows x;
+    if (a[5] != Py_None) {
+      x = c.need_rows(a[2], "x", {da.n, dx.h});
+      same_type(x.fmt, da.fmt, "x");
+    }
+    moe_product_config cfg{};
+    cfg.rows = da.n;
+    cfg.n_experts = E;
+    cfg.K = dx.p ? dx.h : x.h;
+    cfg.N = da.h;
+    cfg.fmt = cfg.y_fmt = cfg.dw_fmt = da.fmt;
+    void* dw = c.weights_gradient(a[5], "dw", E, 2ll * da.h, cfg.K, &cfg.dw_fmt);
+    if (!dx.p && !dw) refuse("dx or dw must be given");
+    cfg.act = int_arg(a[8], "act");
+    cfg.ld_x = x.ld;
+    cfg.ld_dx = dx.ld;
+    cfg.ld_w = w.ld;
+    cfg.gs_w = w.gs;
+    cfg.ld_y = da.ld;
+    cfg.ld_z = gu.ld;
+    size_t bytes;
+    void* ws = c.workspace(a[6], &bytes);
+    const moe_stream_t s = c.stream(a[9]);
+    return unlocked([&] { return moe_glu_backward(&cfg, da.p, gu.p, x.p, w.p, off, dx.p, dw, ws, bytes, s); });
+  });
+}
+
+// (x, w, y, bias, residual, z, offsets, act, stream)
+PyObject* linear(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<9>("moe_linear", args, n, [](PyObject* const* a) {
+    Call c;
+    int32_t E;
+    const Rows x = c.need_rows(a[0], "x", {});
+    const Call::Weights w = c.weights(a[1], "w");
+    if (!w.p) refuse("w must be a tensor");
+    const int32_t* off = c.offsets(a[6], &E);
+    want_weights(w, E, w.n, x.h);
+    same_type(w.fmt, x.fmt, "w");
+    const Rows y = c.need_rows(a[2], "y", {x.n, w.n}), r = c.rows(a[4], "residual", {x.n, w.n});
+    const Rows z = c.rows(a[5], "z", {x.n, w.n});
+    if (r.p && r.fmt != y.fmt) refuse("residual must have y's type");
+    if (z.p) same_type(z.fmt, x.fmt, "z");
+    const float* bias = E == 1 ? c.flat<float>(a[3], "bias", kF32, {w.n}) : c.flat<float>(a[3], "bias", kF32, {E, w.n});
+    moe_product_config cfg{};
+    cfg.rows = x.n;
+    cfg.n_experts = E;
+    cfg.K = x.h;
+    cfg.N = w.n;
+    cfg.fmt = cfg.dw_fmt = x.fmt;
+    cfg.y_fmt = y.fmt;
+    cfg.act = int_arg(a[7], "act");
+    cfg.ld_x = x.ld;
+    cfg.ld_w = w.ld;
+    cfg.gs_w = w.gs;
+    cfg.ld_y = y.ld;
+    cfg.ld_residual = r.ld;
+    cfg.ld_z = z.ld;
+    const moe_stream_t s = c.stream(a[8]);
+    return unlocked([&] { return moe_linear(&cfg, x.p, w.p, bias, r.p, off, y.p, z.p, s); });
+  });
+}
+
+// (dy, z, x, w, dx, dw, dbias, ws, offsets, act, stream)
+PyObject* linear_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return entry<11>("moe_linear_backward", args, n, [](PyObject* const* a) {
+    Call c;
+    int32_t E;
+    const int32_t act = int_arg(a[9], "act");
+    const Rows dy = c.need_rows(a[0], "dy", {});
+    const Rows z = act == MOE_ACT_NONE ? Rows{} : c.need_rows(a[1], "z", {dy.n, dy.h});
+    const int32_t* off = c.offsets(a[8], &E);
+    const Rows dx = c.rows(a[4], "dx", {dy.n});
+    int32_t fmt = z.p ? z.fmt : dy.fmt;
+    Call::Weights w;
+    if (dx.p) {
+      w = c.weights(a[3], "w");
+      if (!w.p) refuse("dx needs w");
+      want_weights(w, E, dy.h, dx.h);
+      if (z.p) same_type(w.fmt, fmt, "w");
+      fmt = w.fmt;
+      same_type(dx.fmt, fmt, "dx");
+    }
+    Rows x;
+    if (a[5] != Py_None) {
+      x = c.need_rows(a[2], "x", {dy.n, dx.h});
+      if (z.p || dx.p) same_type(x.fmt, fmt, "x");
+      fmt = x.fmt;
+    }
+    moe_product_config cfg{};
+    cfg.rows = dy.n;
+    cfg.n_experts = E;
+    cfg.K = dx.p ? dx.h : x.p ? x.h : 1;
+    cfg.N = dy.h;
+    cfg.fmt = cfg.dw_fmt = fmt;
+    cfg.y_fmt = dy.fmt;
+    void* dw = c.weights_gradient(a[5], "dw", E, dy.h, cfg.K, &cfg.dw_fmt);
+    float* db = E == 1 ? c.flat<float>(a[6], "dbias", kF32, {dy.h}) : c.flat<float>(a[6], "dbias", kF32, {E, dy.h});
+    if (!dx.p && !dw && !db) refuse("dx, dw or dbias must be given");
+    cfg.act = act;
+    cfg.ld_x = x.ld;
+    cfg.ld_dx = dx.ld;
+    cfg.ld_w = w.ld;
+    cfg.gs_w = w.gs;
+    cfg.ld_y = dy.ld;
+    cfg.ld_z = z.ld;
+    size_t bytes;
+    void* ws = c.workspace(a[7], &bytes);
+    const moe_stream_t s = c.stream(a[10]);
+    return unlocked([&] {
+      return moe_linear_backward(&cfg, dy.p, z.p, x.p, w.p, off, dx.p, dw, db, ws, bytes, s);
+    });
+  });
+}
+
 // (MoeError)
 PyObject* set_error(PyObject*, PyObject* o) {
   Py_INCREF(o);
@@ -439,7 +656,8 @@ PyObject* set_error(PyObject*, PyObject* o) {
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(dispatch), FAST(dispatch_backward), FAST(combine), FAST(combine_backward),
-                           FAST(topk_backward), FAST(block_norm), FAST(block_norm_backward), FAST(check_block),
+                           FAST(topk_backward), FAST(block_norm), FAST(block_norm_backward), FAST(check_block), FAST(glu),
+                           FAST(glu_backward), FAST(linear), FAST(linear_backward),
                            {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", "Tensors to the C entry points around the experts", -1,
                         g_methods, nullptr, nullptr, nullptr, nullptr};
