@@ -6,6 +6,8 @@
 //   linear   z = x W^T + b, y = act(z) + r               dz = dy act'(z), dx = dz W, dW = dz^T x, db = sum dz
 //
 // The products are tiles on the matrix cores (products.hpp).
+#include <cmath>
+
 #include "products.hpp"
 
 namespace rmoe {
@@ -15,7 +17,8 @@ constexpr int kProductMaxSize = 1 << 16;  // of a row of x, of the outputs
 
 // ---------------------------------------------------------------- the gradient before the projection
 // d = dgu (glu) or dz (linear), rounded to the operands' type: the products that follow take it as
-// an operand, as autograd's do.  Eight elements a lane; rows behind the last expert's are left out.
+// an operand, as autograd's do, with zeros up to ld_d behind each row.  Eight elements a lane; rows behind
+// the last expert's are left out.
 template <bool GLU>
 __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
                                                            const void* __restrict__ z, int fmt, int64_t ld_z,
@@ -24,10 +27,16 @@ __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restric
   const int c = 8 * (blockIdx.y * 64 + (threadIdx.x & 63));
   const int end = offsets ? min(max(offsets[E], 0), rows) : rows;
   if (c >= n) return;
+  const int all = GLU ? 2 * n : n;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int row = blockIdx.x * 8 + 4 * i + (threadIdx.x >> 6);
     if (row >= end) return;
+    if (c + 8 >= n)  // the last of the row
+      for (int e = all; e < ld_d; ++e) {
+        if (fmt == MOE_AFMT_BF16) static_cast<uint16_t*>(d)[row * ld_d + e] = 0;
+        else static_cast<float*>(d)[row * ld_d + e] = 0.f;
+      }
     float g[8], v[8];
     read8(dy, (int64_t)row * ld_dy + c, dy_fmt, n - c, v);
     if constexpr (GLU) {
@@ -55,15 +64,17 @@ __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restric
 
 // ---------------------------------------------------------------- the bias's gradient
 // Column sums of dz in fp32, from dy and z as given (dz is not rounded here).  A workgroup has 64
-// columns, eight lanes of eight, and 128 rows at once; its rows' sums meet in LDS in a fixed
-// order.  Splits of a long expert write their own sums, which bias_join adds in order.
-constexpr int kBiasRows = 512;  // rows of a split, about
+// columns, eight lanes of eight, and 32 rows at once; its rows' sums meet in LDS in a fixed order.
+// Splits of a long expert write their own sums, which bias_join adds in order: 128 rows a split and
+// more, up to 64 splits, put about as many loads in flight as there are (777 rows of 1001 in bf16 with
+// gelu: 19 us in one split of sixteen wavefronts).
+constexpr int kBiasRows = 128;  // rows of a split, at least
 
-__global__ __launch_bounds__(1024) void bias_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
-                                                             const void* __restrict__ z, int fmt, int64_t ld_z,
-                                                             const int32_t* __restrict__ offsets, int rows, int E, int n,
-                                                             int act, int splits, float* __restrict__ out) {
-  __shared__ float part[16][64];
+__global__ __launch_bounds__(256) void bias_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
+                                                            const void* __restrict__ z, int fmt, int64_t ld_z,
+                                                            const int32_t* __restrict__ offsets, int rows, int E, int n,
+                                                            int act, int splits, float* __restrict__ out) {
+  __shared__ float part[4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = 64 * blockIdx.x + 8 * (lane & 7);
   const Range r = expert_rows(offsets, blockIdx.y, rows);
@@ -71,7 +82,7 @@ __global__ __launch_bounds__(1024) void bias_gradient_kernel(const void* __restr
   float sum[8] = {};
   if (c < n) {
 #pragma unroll 2
-    for (int i = from + 8 * wave + (lane >> 3); i < to; i += 128) {
+    for (int i = from + 8 * wave + (lane >> 3); i < to; i += 32) {
       float v[8], g[8];
       read8(dy, (int64_t)(r.first + i) * ld_dy + c, dy_fmt, n - c, v);
       if (act != MOE_ACT_NONE) {
@@ -92,10 +103,8 @@ __global__ __launch_bounds__(1024) void bias_gradient_kernel(const void* __restr
   __syncthreads();
   const int col = 64 * blockIdx.x + threadIdx.x;
   if (threadIdx.x >= 64 || col >= n) return;
-  float s = 0.f;
-#pragma unroll
-  for (int w = 0; w < 16; ++w) s += part[w][threadIdx.x];
-  out[((int64_t)blockIdx.z * E + blockIdx.y) * n + col] = s;
+  out[((int64_t)blockIdx.z * E + blockIdx.y) * n + col] =
+      (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
 }
 
 __global__ __launch_bounds__(256) void bias_join_kernel(const float* __restrict__ part, int64_t total, int splits,
@@ -117,17 +126,121 @@ int bias_splits(int64_t rows, int E) {
 // ---------------------------------------------------------------- launches
 constexpr int64_t kMaxBlocks = (1ll << 32) / 256 - 1;  // a launch's threads are counted in 32 bits
 
-template <typename E, int OP>
-moe_status product_of(const ProductArgs& p, hipStream_t s) {
-  constexpr int BM = 128, BN = 128;
-  using T = ProductTile<E, OP, BM, BN, 64, 64>;
-  const int64_t nt = (p.N + T::kCols - 1) / T::kCols;
-  // row tiles: every expert with a row may end in a part of one
+// Row tiles of BM (every expert with a row may end in a part of one) and the grid over them.
+template <int OP, int BM, int COLS>
+int64_t tiles_of(const ProductArgs& p) {
+  const int64_t nt = (p.N + COLS - 1) / COLS;
   const int64_t mt = OP == OP_DW ? (int64_t)p.E * ((p.M + BM - 1) / BM)
                                  : ((int64_t)p.rows + (int64_t)std::min(p.E, p.rows) * (BM - 1)) / BM;
-  const int64_t blocks = (mt * nt + 7) / 8 * 8;
+  return mt * nt;
+}
+template <typename T, int OP, int BM>
+moe_status run_tiles(void (*kernel)(ProductArgs), ProductArgs p, int threads, hipStream_t s) {
+  const int64_t tiles = tiles_of<OP, BM, T::kCols>(p);
+  // whole runs on every XCD
+  const int64_t eight = 8 * (OP == OP_DW ? (int64_t)dealt_run((uint32_t)std::min<int64_t>(tiles / p.E, 1 << 30)) : 1);
+  const int64_t blocks = (tiles + eight - 1) / eight * eight;
   if (blocks > kMaxBlocks) return MOE_EINVAL;
-  return launch(product_kernel<E, OP, BM, BN, 64, 64>, dim3((unsigned)blocks), dim3(T::kThreads), s, p);
+  p.tiles = (uint32_t)tiles;
+  return launch(kernel, dim3((unsigned)blocks), dim3(threads), s, p);
+}
+
+// Whether the operands' rows start on 16 bytes, whole pieces make up every row (a d of the workspace
+// has zeros behind its rows), and a tile's offsets stay below the descriptor's size.
+template <typename E, int OP>
+bool direct_ok(const ProductArgs& p) {
+  constexpr int64_t eb = sizeof(E), el = 16 / eb;
+  if (!aligned_to(p.a, 16) || !aligned_to(p.b, 16) || p.lda % el || p.ldb % el || p.gsb % el) return false;
+  constexpr int64_t most = (1ll << 31) - (1 << 20);
+  if (OP == OP_DW) return (p.M % el == 0 || p.padded) && p.N % el == 0 && std::max(p.lda, p.ldb) * 128 < most;
+  if ((p.K % el && !p.padded) || (256 * p.lda + p.K) * eb >= most) return false;
+  if (OP == OP_DX) return p.N % el == 0 && p.ldb * 128 < most;
+  return ((OP == OP_GLU ? (int64_t)p.N : 0) + 256) * p.ldb * eb + p.K * eb < most;
+}
+
+constexpr int kCus = 256;  // MI355X
+
+template <typename E, int OP, int BM, int BN, int WM, int WN, int KS, int PER_CU>
+moe_status direct(const ProductArgs& p, hipStream_t s) {
+  using T = ProductTile<E, OP, BM, BN, WM, WN>;
+  return run_tiles<T, OP, BM>(product_direct_kernel<E, OP, BM, BN, WM, WN, KS, KS * T::kWaves * PER_CU / 4>, p, KS * T::kThreads, s);
+}
+template <typename E, int OP, int BM, int BN, int WM, int WN>
+moe_status staged(const ProductArgs& p, hipStream_t s) {
+  using T = ProductTile<E, OP, BM, BN, WM, WN>;
+  return run_tiles<T, OP, BM>(product_kernel<E, OP, BM, BN, WM, WN>, p, T::kThreads, s);
+}
+
+// A tile's shape, chosen by its estimated time: rounds of workgroups x what a tile costs beside its
+// stages, and per stage (128 bytes of k) the longer of what it takes alone on a CU and of what the CU's
+// share of all tiles takes.  The figures (us) fit measured times of 45 to 90 shapes a row (1 to 32768
+// rows, up to 256 experts, sizes 512 to 8192), where the choice is within 1 to 3% of the best shape on
+// average and 21% at worst.  In bf16, 4096^3: 256 x 256 107 us, 128 x 256 122, 128 x 128 124, 64 x 128
+// 161, 64 x 64 199; 1024 x 4096 x 4096: 86, 53, 44, 44, 54; one row of 4096 x 4096: 83, 50, 37, 28, 24,
+// and 17 where four groups of wavefronts share the k.
+struct TileCost {
+  int bm, bn, per_cu, parts;
+  float fixed, alone, shared;
+};
+enum { TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS, TILES };
+constexpr TileCost kCosts[2][3][TILES] = {
+    {// fp32: forward, rows' gradient, weights' gradient (the two large shapes have no kernel)
+     {{}, {}, {128, 128, 2, 1, 2.47f, 2.33f, 1.96f}, {64, 128, 3, 1, 2.09f, .90f, 1.f}, {64, 64, 5, 1, 3.51f, .62f, .50f}, {64, 64, 1, 4, 4.71f, 1.77f, 1.87f}},
+     {{}, {}, {128, 128, 2, 1, 2.47f, 2.39f, 1.80f}, {64, 128, 3, 1, 2.74f, 1.06f, .90f}, {64, 64, 5, 1, 2.92f, .88f, .45f}, {64, 64, 1, 4, 4.13f, 1.77f, 1.69f}},
+     {{}, {}, {128, 128, 2, 1, 4.41f, 2.39f, 1.48f}, {64, 128, 3, 1, 2.91f, 1.09f, .74f}, {64, 64, 5, 1, 1.95f, .99f, .42f}, {64, 64, 1, 4, 4.77f, 1.77f, 1.58f}}},
+    {{{256, 256, 1, 1, 4.33f, .90f, 1.64f}, {128, 256, 1, 1, 4.11f, .61f, .94f}, {128, 128, 2, 1, 4.19f, .56f, .47f}, {64, 128, 3, 1, 3.18f, .31f, .29f},
+      {64, 64, 5, 1, 2.77f, .32f, .20f}, {64, 64, 1, 4, 4.46f, .60f, .56f}},
+     {{256, 256, 1, 1, 3.75f, 1.44f, 1.35f}, {128, 256, 1, 1, 5.08f, .68f, .79f}, {128, 128, 2, 1, 2.47f, .43f, .44f}, {64, 128, 3, 1, 3.06f, .57f, .25f},
+      {64, 64, 5, 1, 3.51f, .26f, .21f}, {64, 64, 1, 4, 3.85f, .80f, .92f}},
+     {{256, 256, 1, 1, 3.75f, .94f, 1.54f}, {128, 256, 1, 1, 3.58f, .70f, 1.f}, {128, 128, 2, 1, 3.38f, .67f, .58f}, {64, 128, 3, 1, 3.51f, .45f, .40f},
+      {64, 64, 5, 1, 2.98f, .46f, .20f}, {64, 64, 1, 4, 5.07f, .66f, .81f}}}};
+static_assert(MOE_AFMT_F32 == 0 && MOE_AFMT_BF16 == 1, "kCosts' first index");
+
+template <typename E, int OP>
+int choose_tile(const ProductArgs& p, std::initializer_list<int> from) {
+  constexpr int kCus = 256, kK = 128 / sizeof(E);
+  const TileCost* costs = kCosts[sizeof(E) == 2][OP == OP_DW ? 2 : OP == OP_DX];
+  const float rows = p.rows, used = std::min(p.E, p.rows);  // experts with a row, at most
+  int best = -1;
+  float least = 0;
+  for (const int i : from) {
+    const TileCost& c = costs[i];
+    const int cols = OP == OP_GLU ? c.bn / 2 : c.bn;
+    const float nt = (p.N + cols - 1) / cols;
+    const float mt = OP == OP_DW  ? (float)p.E * ((p.M + c.bm - 1) / c.bm)
+                     : p.E == 1 ? std::ceil(rows / c.bm)
+                                : std::max(rows / c.bm + .5f * used, used);
+    const float k = OP == OP_DW ? rows / p.E : p.K, stages = std::ceil(std::ceil(k / kK) / c.parts);
+    const float tiles = mt * nt, time = std::ceil(tiles / (kCus * c.per_cu)) * c.fixed +
+                                        stages * std::max(c.alone, std::ceil(tiles / kCus) * c.shared);
+    if (best < 0 || time < least) {
+      best = i;
+      least = time;
+    }
+  }
+  return best;
+}
+
+template <typename E, int OP>
+moe_status product_of(const ProductArgs& p, hipStream_t s) {
+  if (direct_ok<E, OP>(p)) {
+    int tile;
+    if constexpr (sizeof(E) == 2) {
+      tile = choose_tile<E, OP>(p, {TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS});
+      if (tile == TILE_256) return direct<E, OP, 256, 256, 128, 64, 1, 1>(p, s);
+      if (tile == TILE_128_256) return direct<E, OP, 128, 256, 64, 64, 1, 1>(p, s);
+    } else {
+      tile = choose_tile<E, OP>(p, {TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS});
+    }
+    if (tile == TILE_128) return direct<E, OP, 128, 128, 64, 64, 1, 2>(p, s);
+    if (tile == TILE_64_128) return direct<E, OP, 64, 128, 32, 64, 1, 3>(p, s);
+    if (tile == TILE_64) return direct<E, OP, 64, 64, 32, 32, 1, 5>(p, s);
+    return direct<E, OP, 64, 64, 32, 32, 4, 1>(p, s);
+  }
+  // rows that start anywhere: 4096 x 2048 x 4096 in bf16 176 us in 128 x 128, 250 in 64 x 64; the gradient of 333 x
+  // 999 x 257 in fp32 74 us and 39
+  if (choose_tile<E, OP>(p, {TILE_128, TILE_64}) == TILE_64) return staged<E, OP, 64, 64, 32, 32>(p, s);
+  return staged<E, OP, 128, 128, 64, 64>(p, s);
 }
 template <int OP>
 moe_status product(int fmt, const ProductArgs& p, hipStream_t s) {
@@ -210,11 +323,12 @@ bool sizes_ok(int32_t rows, int32_t E, int32_t K, int32_t N, int32_t fmt) {
 uint8_t* base_of(void* ws) { return reinterpret_cast<uint8_t*>(((uintptr_t)ws + 15) & ~(uintptr_t)15); }
 
 // dx = d W and dW = d^T x, each where it is asked for.
-moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz, int64_t ld_dz, const void* x, const void* w,
+moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz, int64_t ld_dz, bool padded, const void* x, const void* w,
                      const int32_t* offsets, void* dx, void* dw, hipStream_t s) {
   ProductArgs p{};
   p.a = dz;
   p.lda = ld_dz;
+  p.padded = padded;
   p.offsets = offsets;
   p.rows = c->rows;
   p.E = c->n_experts;
@@ -313,7 +427,7 @@ extern "C" MOE_API moe_status moe_glu_backward(const moe_product_config* cfg, co
   const StreamDevice on(s);
   uint8_t* const dgu = base_of(ws) + k.d;
   const moe_status st = pre_gradient<true>(cfg, d, da, cfg->fmt, gu, offsets, dgu, k.ld_d, s);
-  return st == MOE_OK ? gradients(cfg, d, dgu, k.ld_d, x, w, offsets, dx, dw, s) : st;
+  return st == MOE_OK ? gradients(cfg, d, dgu, k.ld_d, true, x, w, offsets, dx, dw, s) : st;
 }
 
 extern "C" MOE_API moe_status moe_linear(const moe_product_config* cfg, const void* x, const void* w, const float* bias,
@@ -389,7 +503,7 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
   if (dbias) {
     const int splits = bias_splits(R, cfg->n_experts);
     float* const part = splits > 1 ? reinterpret_cast<float*>(base + k.bias) : dbias;
-    st = launch(bias_gradient_kernel, dim3((cfg->N + 63) / 64, cfg->n_experts, splits), dim3(1024), s, dy, cfg->y_fmt, d.ld_y,
+    st = launch(bias_gradient_kernel, dim3((cfg->N + 63) / 64, cfg->n_experts, splits), dim3(256), s, dy, cfg->y_fmt, d.ld_y,
                 z, cfg->fmt, d.ld_z, offsets, cfg->rows, cfg->n_experts, cfg->N, cfg->act, splits, part);
     if (st == MOE_OK && splits > 1) {
       const int64_t total = (int64_t)cfg->n_experts * cfg->N;
@@ -398,8 +512,8 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
     if (st != MOE_OK) return st;
   }
   if (!dx && !dw) return st;
-  // dy itself where nothing changes it, else dz in the operands' type
-  if (!zs && cfg->y_fmt == cfg->fmt) return gradients(cfg, d, dy, d.ld_y, x, w, offsets, dx, dw, s);
+  // dy itself where nothing changes it and its rows start on 16 bytes, else dz in the operands' type
+  if (!zs && cfg->y_fmt == cfg->fmt && aligned_to(dy, 16) && (d.ld_y * eb | cfg->N * eb) % 16 == 0) return gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, s);
   st = pre_gradient<false>(cfg, d, dy, cfg->y_fmt, z, offsets, base + k.d, k.ld_d, s);
-  return st == MOE_OK ? gradients(cfg, d, base + k.d, k.ld_d, x, w, offsets, dx, dw, s) : st;
+  return st == MOE_OK ? gradients(cfg, d, base + k.d, k.ld_d, true, x, w, offsets, dx, dw, s) : st;
 }

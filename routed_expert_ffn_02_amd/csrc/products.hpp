@@ -29,6 +29,8 @@ struct ProductArgs {
   const float* bias;         // [E,N] or null
   int64_t ldo, ld_aux, ld_res;
   int32_t out_fmt;           // of out and residual
+  bool padded;               // a's rows have zeros up to a multiple of 16 bytes
+  uint32_t tiles;            // at most
 };
 
 // ---------------------------------------------------------------- activations
@@ -83,6 +85,7 @@ __device__ __forceinline__ void read8(const void* base, int64_t at, int fmt, int
   }
 }
 // Rounded to fmt (nearest even) at p.
+template <bool NT = false>
 __device__ __forceinline__ void write8(void* base, int64_t at, int fmt, int n, const float (&v)[8]) {
   if (fmt == MOE_AFMT_BF16) {
     uint16_t* p = static_cast<uint16_t*>(base) + at;
@@ -90,7 +93,7 @@ __device__ __forceinline__ void write8(void* base, int64_t at, int fmt, int n, c
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     if (n >= 8) {
-      store16<false>(reinterpret_cast<uint8_t*>(p), q);
+      store16<NT>(reinterpret_cast<uint8_t*>(p), q);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -105,8 +108,8 @@ __device__ __forceinline__ void write8(void* base, int64_t at, int fmt, int n, c
         a[i] = __float_as_uint(v[i]);
         b[i] = __float_as_uint(v[4 + i]);
       }
-      store16<false>(reinterpret_cast<uint8_t*>(p), a);
-      store16<false>(reinterpret_cast<uint8_t*>(p + 4), b);
+      store16<NT>(reinterpret_cast<uint8_t*>(p), a);
+      store16<NT>(reinterpret_cast<uint8_t*>(p + 4), b);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -127,20 +130,31 @@ __device__ __forceinline__ Range expert_rows(const int32_t* offsets, int g, int 
   return {lo, max(hi - lo, 0)};
 }
 
-// Workgroups go round the eight XCDs; XCD x takes the x-th eighth of the tiles' order, so tiles
-// that share operands share an L2.  -1: none.
-__device__ __forceinline__ int64_t tile_of_block(uint32_t total) {
-  const uint32_t per = (total + 7) / 8, i = blockIdx.x >> 3;
+__device__ __forceinline__ Range expert_rows_uniform(const int32_t* offsets, int g, int rows) {
+  // by scalar loads: they wait for no vector memory access, of which many may be on their way
+  if (!offsets) return {0, rows};
+  const auto* o = (const __attribute__((address_space(4))) int32_t*)offsets;
+  const int lo = min(max(o[g], 0), rows), hi = min(max(o[g + 1], 0), rows);
+  return {lo, max(hi - lo, 0)};
+}
+
+// Workgroups go round the eight XCDs; an XCD's i-th takes the i-th entry of its list of tiles.  The
+// list is an eighth of all tiles' order, so that tiles that share operands share an L2; -1: none.
+__device__ __forceinline__ int64_t tile_of_list(uint32_t total, uint32_t i) {
+  const uint32_t per = (total + 7) / 8;
   const uint64_t t = (uint64_t)(blockIdx.x & 7) * per + i;
   return i < per && t < total ? (int64_t)t : -1;
 }
+// The weights' gradient: an expert's tiles (`each` of them) differ in cost from another's, so every
+// expert's are dealt out to all XCDs, in runs of neighbours that share operands.
+__host__ __device__ __forceinline__ uint32_t dealt_run(uint32_t each) { return each < 16 ? 1 : each / 8; }
+__device__ __forceinline__ int64_t dealt_tile(uint32_t total, uint32_t each, uint32_t i) {
+  const uint32_t run = dealt_run(each), x = blockIdx.x & 7;
+  const uint64_t t = ((uint64_t)(i / run) * 8 + x) * run + i % run;
+  return t < total ? (int64_t)t : -1;
+}
 
 __device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return a + b < a ? 0xffffffffu : a + b; }
-
-// A row tile's place: expert, first row, its rows (at most BM), the column tile.
-struct TileAt {
-  int g, row0, rows, n;
-};
 
 // Band order: eight row tiles high, then column by column, so about as many row tiles as
 // column tiles are in flight on an XCD.
@@ -152,102 +166,137 @@ __device__ __forceinline__ void band_order(uint32_t r, int mt, int nt, int& m, i
   m = band * kBand + in % high;
 }
 
-// The workgroup's row tile among all experts'; every wavefront finds it by itself, its lanes
-// counting the tiles of E / 64 experts each.
-template <int BM>
-__device__ __forceinline__ bool find_tile(const int32_t* offsets, int rows, int E, int nt, TileAt& t) {
-  const int lane = threadIdx.x & 63;
-  if (!offsets) {
-    const int mt = (rows + BM - 1) / BM;
-    const int64_t b = tile_of_block((uint32_t)mt * nt);
-    if (b < 0) return false;
-    int m;
-    band_order((uint32_t)b, mt, nt, m, t.n);
-    t.g = 0;
-    t.row0 = m * BM;
-    t.rows = min(BM, rows - m * BM);
-    return true;
-  }
-  const int per = (E + 63) / 64, g0 = lane * per;
-  uint32_t mine = 0;
+// Where a tile of C lies: M x N outputs of K terms from row row0 (or of them) of expert g's; m0: its
+// first row of weights (OP_DW), n0: its first column.
+struct Place {
+  int g, row0, m0, n0, M, N, K;
+};
+
+// The row tiles of all experts, counted: each wavefront's lanes count those of E / 64
+// experts each, up to and with its own.
+template <int OP, int BM>
+__device__ __forceinline__ uint32_t count_tiles(const ProductArgs& p) {
+  if (OP == OP_DW || !p.offsets) return 0;
+  const int lane = threadIdx.x & 63, per = (p.E + 63) / 64, g0 = lane * per;
+  uint32_t incl = 0;
   for (int i = 0; i < per; ++i)
-    if (g0 + i < E) mine += (expert_rows(offsets, g0 + i, rows).n + BM - 1) / BM;
-  uint32_t incl = mine;
+    if (g0 + i < p.E) incl += (expert_rows(p.offsets, g0 + i, p.rows).n + BM - 1) / BM;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const uint32_t v = __shfl_up(incl, o);
     if (lane >= o) incl = add_sat(incl, v);
   }
-  const uint32_t mts = __builtin_amdgcn_readlane(incl, 63);
-  // (tables that are no offsets may count more tiles than rows allow: those past 32 bits have no workgroup)
-  const uint64_t all = (uint64_t)mts * nt;
-  const int64_t b = tile_of_block(all > 0x7fffffffu ? 0x7fffffffu : (uint32_t)all);
-  if (b < 0) return false;
-  const uint64_t past = __ballot((uint64_t)incl * nt > (uint64_t)b);
-  const int at = __ffsll((unsigned long long)past) - 1;
-  uint32_t before = at ? (uint32_t)__builtin_amdgcn_readlane(incl, at - 1) : 0u;
-  int g = at * per;
-  for (;; ++g) {
-    const Range r = expert_rows(offsets, g, rows);
-    const uint32_t mt = (r.n + BM - 1) / BM;
-    if ((uint64_t)(before + mt) * nt > (uint64_t)b) {
-      int m;
-      band_order((uint32_t)(b - (int64_t)before * nt), mt, nt, m, t.n);
-      t.g = __builtin_amdgcn_readfirstlane(g);
-      t.row0 = __builtin_amdgcn_readfirstlane(r.first + m * BM);
-      t.rows = __builtin_amdgcn_readfirstlane(min(BM, r.n - m * BM));
-      t.n = __builtin_amdgcn_readfirstlane(t.n);
-      return true;
+  return incl;
+}
+
+// The i-th tile of this workgroup's XCD; false: it has no more.
+template <int OP, int BM, int COLS>
+__device__ __forceinline__ bool find_place(const ProductArgs& p, uint32_t counts, uint32_t i, Place& at) {
+  const int nt = (p.N + COLS - 1) / COLS;
+  int m, n;
+  if constexpr (OP == OP_DW) {
+    const int mt = (p.M + BM - 1) / BM;
+    const int64_t b = dealt_tile((uint32_t)p.E * mt * nt, mt * nt, i);
+    if (b < 0) return false;
+    at.g = (int)((uint32_t)b / (uint32_t)(mt * nt));
+    band_order((uint32_t)b % (uint32_t)(mt * nt), mt, nt, m, n);
+    const Range r = expert_rows_uniform(p.offsets, at.g, p.rows);
+    at.row0 = r.first;
+    at.K = r.n;
+    at.m0 = m * BM;
+    at.M = min(BM, p.M - at.m0);
+  } else {
+    at.K = p.K;
+    at.m0 = 0;
+    if (!p.offsets) {
+      const int mt = (p.rows + BM - 1) / BM;
+      const int64_t b = tile_of_list((uint32_t)mt * nt, i);
+      if (b < 0) return false;
+      band_order((uint32_t)b, mt, nt, m, n);
+      at.g = 0;
+      at.row0 = m * BM;
+      at.M = min(BM, p.rows - m * BM);
+    } else {
+      // (a table that is no offsets may count more tiles than rows allow: no more than those are done)
+      const uint64_t all = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(counts, 63) * nt;
+      const int64_t b = tile_of_list((uint32_t)min(all, (uint64_t)p.tiles), i);
+      if (b < 0) return false;
+      const uint64_t past = __ballot((uint64_t)counts * nt > (uint64_t)b);
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)past) - 1);
+      uint32_t before = l ? (uint32_t)__builtin_amdgcn_readlane(counts, l - 1) : 0u;
+      for (int g = l * ((p.E + 63) / 64);; ++g) {
+        const Range r = expert_rows_uniform(p.offsets, g, p.rows);
+        const uint32_t mt = (r.n + BM - 1) / BM;
+        if ((uint64_t)(before + mt) * nt > (uint64_t)b) {
+          band_order((uint32_t)(b - (int64_t)before * nt), mt, nt, m, n);
+          at.g = g;
+          at.row0 = r.first + m * BM;
+          at.M = min(BM, r.n - m * BM);
+          break;
+        }
+        before += mt;
+      }
     }
-    before += mt;
   }
+  at.n0 = n * COLS;
+  at.N = min(COLS, p.N - at.n0);
+  at.g = __builtin_amdgcn_readfirstlane(at.g);
+  at.row0 = __builtin_amdgcn_readfirstlane(at.row0);
+  at.m0 = __builtin_amdgcn_readfirstlane(at.m0);
+  at.n0 = __builtin_amdgcn_readfirstlane(at.n0);
+  at.M = __builtin_amdgcn_readfirstlane(at.M);
+  at.N = __builtin_amdgcn_readfirstlane(at.N);
+  at.K = __builtin_amdgcn_readfirstlane(at.K);
+  return true;
 }
 
 // ---------------------------------------------------------------- operands
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
-// An operand in LDS: R tile rows by 128 bytes of k, in 16-byte pieces.
-//  k in a row (KMAJ = false): piece c of tile row r at (8 r + (c ^ r % 8)): the eight rows that
-//    eight lanes read at one c lie in eight different pieces of a 128-byte line of banks;
-//  a tile row per k (KMAJ = true): k's R elements in R / n pieces (n elements each), piece c at
-//    c ^ f(k): the rows that one transposing read (16-bit) or the two halves of a wavefront
-//    (fp32) take together lie 64 or 128 bytes apart.
+// An operand in LDS: R tile rows by 128 bytes of k, in 16-byte pieces.  Sixteen lanes' pieces (or 8 bytes
+// of thirty-two) lie in different banks, whatever the k:
+//  k in a row (KMAJ = false): the pieces of a tile row one after the other, piece c at c ^ f(row);
+//  a tile row per k (KMAJ = true): k's R elements one after the other, piece c at c ^ f(k).
 template <typename E, int R, bool KMAJ>
 struct Operand {
   static constexpr int kEl = 16 / sizeof(E);       // elements of a piece
   static constexpr int kK = 128 / sizeof(E);       // k of a stage
   static constexpr int kBytes = R * 128;
   static constexpr int kPieces = R * 8;
-  static constexpr int kPerK = R * (int)sizeof(E) / 16;  // pieces of one k (KMAJ)
+  static constexpr int kPerRow = KMAJ ? R * (int)sizeof(E) / 16 : 8;
+  static_assert(R >= 32 && R % 32 == 0, "f stays inside a row of pieces");
 
-  __device__ static __forceinline__ int swizzle(int k) {
-    return sizeof(E) == 2 ? 4 * (k & 3) : 8 * ((k >> 2) & 1);
+  __device__ static __forceinline__ int swizzle(int i) {  // of tile row or k i
+    if constexpr (!KMAJ) return (i >> 1) & 7;
+    else if constexpr (sizeof(E) == 4) return 4 * ((i >> 2) & (R >= 64 ? 3 : 1));
+    else if constexpr (R >= 128) return 4 * (i & 3) + 2 * ((i >> 3) & 1);
+    else if constexpr (R == 64) return 2 * (i & 3);
+    else return 2 * ((i >> 3) & 1);
   }
   // Of piece s (16 bytes at 16 s): its tile row and first k, or its k and first tile row.
   __device__ static __forceinline__ void where(int s, int& row, int& k) {
     if constexpr (KMAJ) {
-      k = s / kPerK;
-      row = ((s % kPerK) ^ swizzle(k)) * kEl;
+      k = s / kPerRow;
+      row = ((s % kPerRow) ^ swizzle(k)) * kEl;
     } else {
-      row = s / 8;
-      k = ((s % 8) ^ (row % 8)) * kEl;
+      row = s / kPerRow;
+      k = ((s % kPerRow) ^ swizzle(row)) * kEl;
     }
   }
-  // The matrix instruction's operand of 32 tile rows from r0 (a multiple of 32) at step j of a
-  // stage's four: lane l has row r0 + l % 32 and the 16 bytes of k that follow (32 j + 16 (l / 32)) bytes.
-  // (In fp32 a step is four instructions of two k each, whose order is the same on both sides.)
+  // The matrix instruction's operand of 16 tile rows from r0 (a multiple of 16) at step j of a
+  // stage's two: lane l has row r0 + l % 16 and the 16 bytes of k that follow 64 j + 16 (l / 16) bytes.
+  // (In fp32 a step is four instructions of four k each, whose order is the same on both sides.)
   __device__ static __forceinline__ u32x4 fragment(const uint8_t* lds, int r0, int j, int lane) {
-    const int r = lane & 31, h = lane >> 5;
+    const int r = lane & 15, q = lane >> 4;
     if constexpr (!KMAJ) {
-      return *reinterpret_cast<const u32x4*>(lds + (r0 + r) * 128 + (((2 * j + h) ^ (r & 7)) << 4));
+      return *reinterpret_cast<const u32x4*>(lds + (r0 + r) * 128 + (((4 * j + q) ^ swizzle(r)) << 4));
     } else if constexpr (sizeof(E) == 2) {
       // 16 lanes read four k of 16 tile rows, 8 bytes each, and get four k of one tile row each
-      const int i = lane & 15, c = r0 / 8 + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-      const uint8_t* p = lds + (16 * j + 8 * h + (i >> 2)) * (R * 2) + ((c ^ (4 * (i >> 2))) << 4) + ((i & 1) << 3);
+      const int k = 8 * q + (r >> 2), c = r0 / 8 + ((r & 3) >> 1);
+      const uint8_t* p = lds + (32 * j + k) * (R * 2) + ((c ^ swizzle(k)) << 4) + ((r & 1) << 3);
       typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * (R * 2)));
@@ -257,21 +306,23 @@ struct Operand {
       const int m = r0 + r;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        v[i] = *reinterpret_cast<const uint32_t*>(lds + (8 * j + 4 * h + i) * (R * 4) + (((m >> 2) ^ (8 * h)) << 4) +
+        v[i] = *reinterpret_cast<const uint32_t*>(lds + (16 * j + 4 * q + i) * (R * 4) + (((m >> 2) ^ swizzle(4 * q)) << 4) +
                                                   ((m & 3) << 2));
       return v;
     }
   }
 };
 
+// 16 x 16 outputs: under this card's power limit the 16 x 16 x 32 instruction sustains 2060 TFLOP/s on
+// random operands in registers, the 32 x 32 x 16 one 1820 (2430 and 2460 on zeros).
 template <typename E>
-__device__ __forceinline__ void multiply(u32x4 a, u32x4 b, f32x16& acc) {
+__device__ __forceinline__ void multiply(u32x4 a, u32x4 b, f32x4& acc) {
   if constexpr (sizeof(E) == 2) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i]), __uint_as_float(b[i]), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[i]), __uint_as_float(b[i]), acc, 0, 0, 0);
   }
 }
 
@@ -291,167 +342,60 @@ __device__ __forceinline__ u32x4 read_piece(const uint8_t* p, int n) {
 }
 
 // ---------------------------------------------------------------- the kernel
-// A workgroup has a BM x BN tile of C, a wavefront WM x WN of it in fragments of 32 x 32.  The
+// A workgroup has a BM x BN tile of C, a wavefront WM x WN of it in fragments of 16 x 16.  The
 // matrix instruction's rows are n and its columns m, so that a lane holds four neighbouring
 // outputs of one row.
 template <typename E, int OP, int BM, int BN, int WM, int WN>
 struct ProductTile {
-  static constexpr int kThreads = 64 * (BM / WM) * (BN / WN);
-  static constexpr int kMt = WM / 32, kNt = WN / 32;
-  using OpA = Operand<E, BM, OP == OP_DW>;
-  using OpB = Operand<E, BN, OP == OP_DX || OP == OP_DW>;
-  static constexpr int kStage = OpA::kBytes + OpB::kBytes;
-  static constexpr int kPatch = 32 * WN * 4;  // a wavefront's fragment row in fp32, for the epilogue
-  static constexpr int kLds = 2 * kStage;
-  static_assert(kPatch * (kThreads / 64) <= kLds, "the epilogue's patches take the stages' place");
-  static constexpr int kCols = OP == OP_GLU ? BN / 2 : BN;  // outputs of a tile's row
+  static constexpr int kWaves = (BM / WM) * (BN / WN), kThreads = 64 * kWaves;
+  static constexpr int kMt = WM / 16, kNt = WN / 16;
+  static constexpr bool kKmajA = OP == OP_DW, kKmajB = OP == OP_DX || OP == OP_DW;
+  static constexpr int kStages = 2 * (BM + BN) * 128;          // two stages in LDS
+  static constexpr int kPatch = 16 * WN * 4;                   // sixteen rows of a wavefront in fp32, for the epilogue
+  static_assert(kWaves * kPatch <= kStages, "they take the stages' place");
+  static_assert(WM % 32 == 0 && WN % 32 == 0, "halves of whole fragments");
+  static constexpr int kCols = OP == OP_GLU ? BN / 2 : BN;     // outputs of a tile's row
 };
 
-template <typename E, int OP, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(ProductArgs p) {
-  using T = ProductTile<E, OP, BM, BN, WM, WN>;
-  constexpr int kThreads = T::kThreads, kK = T::OpA::kK, kEl = T::OpA::kEl;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[T::kLds];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
-  const int nt = (p.N + T::kCols - 1) / T::kCols;
-
-  TileAt t;
-  int m0 = 0, M, K = p.K;
-  if constexpr (OP == OP_DW) {
-    const int mt = (p.M + BM - 1) / BM;
-    const int64_t b = tile_of_block((uint32_t)p.E * mt * nt);
-    if (b < 0) return;
-    t.g = (int)(b / (mt * nt));
-    int m;
-    band_order((uint32_t)(b % (mt * nt)), mt, nt, m, t.n);
-    const Range r = expert_rows(p.offsets, t.g, p.rows);
-    t.row0 = r.first;
-    K = r.n;
-    m0 = m * BM;
-    M = min(BM, p.M - m0);
+// The source row of row r of the n side's tile where its k lie in a row.
+template <int OP, int WN>
+__device__ __forceinline__ int64_t n_row(const ProductArgs& p, const Place& at, int r) {
+  if constexpr (OP == OP_GLU) {  // a wavefront's columns: WN / 2 of the gate, then the same of up
+    const int c = r / WN * (WN / 2) + r % (WN / 2);
+    return at.n0 + min(c, at.N - 1) + (r % WN >= WN / 2 ? p.N : 0);
   } else {
-    if (!find_tile<BM>(p.offsets, p.rows, p.E, nt, t)) return;
-    M = t.rows;
+    return at.n0 + min(r, at.N - 1);
   }
-  const int n0 = t.n * T::kCols, N = min(T::kCols, p.N - n0);
+}
 
-  // this thread's pieces: an address (k = 0) and, in `left`, how many of its elements there are
-  constexpr int kPa = T::OpA::kPieces / kThreads, kPb = T::OpB::kPieces / kThreads;
-  const uint8_t *pa[kPa], *pb[kPb];
-  int ka[kPa], kb[kPb];  // k of the piece in a stage; where rows are the k, beside it the elements in the row
-  int la[kPa], lb[kPb];
-  const E* a = static_cast<const E*>(p.a);
-  const E* b = static_cast<const E*>(p.b);
-#pragma unroll
-  for (int i = 0; i < kPa; ++i) {
-    int r;
-    T::OpA::where(i * kThreads + tid, r, ka[i]);
-    if constexpr (OP == OP_DW) {
-      la[i] = M - r;
-      pa[i] = reinterpret_cast<const uint8_t*>(a + (int64_t)(t.row0 + ka[i]) * p.lda + m0 + r);
-    } else {
-      la[i] = 0;
-      pa[i] = reinterpret_cast<const uint8_t*>(a + (int64_t)(t.row0 + min(r, M - 1)) * p.lda + ka[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kPb; ++i) {
-    int r;
-    T::OpB::where(i * kThreads + tid, r, kb[i]);
-    if constexpr (OP == OP_DW) {
-      lb[i] = N - r;
-      pb[i] = reinterpret_cast<const uint8_t*>(b + (int64_t)(t.row0 + kb[i]) * p.ldb + n0 + r);
-    } else if constexpr (OP == OP_DX) {
-      lb[i] = N - r;
-      pb[i] = reinterpret_cast<const uint8_t*>(b + t.g * p.gsb + (int64_t)kb[i] * p.ldb + n0 + r);
-    } else {
-      lb[i] = 0;
-      int64_t row;
-      if constexpr (OP == OP_GLU) {  // a wavefront's columns: WN / 2 of the gate, then the same of up
-        const int c = r / WN * (WN / 2) + r % (WN / 2);
-        row = n0 + min(c, N - 1) + (r % WN >= WN / 2 ? p.N : 0);
-      } else {
-        row = n0 + min(r, N - 1);
-      }
-      pb[i] = reinterpret_cast<const uint8_t*>(b + t.g * p.gsb + row * p.ldb + kb[i]);
-    }
-  }
-  u32x4 qa[kPa], qb[kPb];
-  const auto load = [&](int k0) {
-#pragma unroll
-    for (int i = 0; i < kPa; ++i) {
-      if constexpr (OP == OP_DW) qa[i] = read_piece<E>(pa[i] + (int64_t)k0 * p.lda * sizeof(E), k0 + ka[i] < K ? la[i] : 0);
-      else qa[i] = read_piece<E>(pa[i] + (int64_t)k0 * sizeof(E), K - k0 - ka[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kPb; ++i) {
-      if constexpr (OP == OP_DW || OP == OP_DX)
-        qb[i] = read_piece<E>(pb[i] + (int64_t)k0 * p.ldb * sizeof(E), k0 + kb[i] < K ? lb[i] : 0);
-      else qb[i] = read_piece<E>(pb[i] + (int64_t)k0 * sizeof(E), K - k0 - kb[i]);
-    }
-  };
-  const auto store = [&](uint8_t* stage) {
-#pragma unroll
-    for (int i = 0; i < kPa; ++i) *reinterpret_cast<u32x4*>(stage + 16 * (i * kThreads + tid)) = qa[i];
-#pragma unroll
-    for (int i = 0; i < kPb; ++i) *reinterpret_cast<u32x4*>(stage + T::OpA::kBytes + 16 * (i * kThreads + tid)) = qb[i];
-  };
-
-  f32x16 acc[T::kMt][T::kNt] = {};
-  const int stages = (K + kK - 1) / kK;
-  if (stages) {
-    load(0);
-    store(lds);
-    __syncthreads();
-  }
-  for (int s = 0; s < stages; ++s) {
-    const uint8_t* at = lds + (s & 1) * T::kStage;
-    if (s + 1 < stages) load((s + 1) * kK);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u32x4 fa[T::kMt], fb[T::kNt];
-#pragma unroll
-      for (int i = 0; i < T::kMt; ++i) fa[i] = T::OpA::fragment(at, wm + 32 * i, j, lane);
-#pragma unroll
-      for (int i = 0; i < T::kNt; ++i) fb[i] = T::OpB::fragment(at + T::OpA::kBytes, wn + 32 * i, j, lane);
-#pragma unroll
-      for (int m = 0; m < T::kMt; ++m)
-#pragma unroll
-        for (int n = 0; n < T::kNt; ++n) multiply<E>(fb[n], fa[m], acc[m][n]);
-    }
-    if (s + 1 < stages) store(lds + ((s + 1) & 1) * T::kStage);
-    __syncthreads();
-  }
-
-  // Epilogue: 32 rows of the wavefront's columns at a time go through LDS (16-byte pieces, piece c
-  // of row r at c ^ r), so that eight neighbouring outputs of a row meet in one lane and rows are
-  // written in whole lines.
-  uint8_t* patch = lds + wave * T::kPatch;
-  constexpr int kSwz = (WN / 4 - 1) & 31;
+// Epilogue: 16 rows of a wavefront's columns at a time go through LDS (16-byte pieces, piece c of row r at
+// c ^ r), so that eight neighbouring outputs of a row meet in one lane and rows are written in whole
+// lines.  patch: the wavefront's own.
+template <typename E, int OP, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void write_tile(const ProductArgs& p, const Place& at_, uint8_t* patch, int wave, int lane,
+                                           const f32x4 (&acc)[WM / 16][WN / 16]) {
+  const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
+  constexpr int kSwz = (WN / 4 - 1) & 15;
   constexpr int kOut = OP == OP_GLU ? WN / 2 : WN;        // outputs of a row
   constexpr int kLanes = kOut / 8, kRows = 64 / kLanes;   // lanes of a row, rows at once
   const int cl = 8 * (lane % kLanes);
-  const int col = n0 + (OP == OP_GLU ? wn / 2 : wn) + cl, cols = p.N - col;
+  const int col = at_.n0 + (OP == OP_GLU ? wn / 2 : wn) + cl, cols = p.N - col;
 #pragma unroll
-  for (int m = 0; m < T::kMt; ++m) {
+  for (int m = 0; m < WM / 16; ++m) {
     {
-      const int r = lane & 31, h = lane >> 5;
+      const int r = lane & 15;
 #pragma unroll
-      for (int n = 0; n < T::kNt; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x4 v = {acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
-          *reinterpret_cast<f32x4*>(patch + r * (WN * 4) + (((8 * n + 2 * q + h) ^ (r & kSwz)) << 4)) = v;
-        }
+      for (int n = 0; n < WN / 16; ++n)
+        *reinterpret_cast<f32x4*>(patch + r * (WN * 4) + (((4 * n + (lane >> 4)) ^ (r & kSwz)) << 4)) = acc[m][n];
     }
     __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-    for (int i = 0; i < 32 / kRows; ++i) {
-      const int r = i * kRows + lane / kLanes, row = wm + 32 * m + r;
+#pragma unroll
+    for (int i = 0; i < (16 + kRows - 1) / kRows; ++i) {
+      const int r = i * kRows + lane / kLanes, row = wm + 16 * m + r;
       const auto get = [&](int c, float (&v)[8]) {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(patch + r * (WN * 4) + (((c / 4) ^ (r & kSwz)) << 4));
-        const f32x4 y = *reinterpret_cast<const f32x4*>(patch + r * (WN * 4) + (((c / 4 + 1) ^ (r & kSwz)) << 4));
+        const int q = r & 15;
+        const f32x4 x = *reinterpret_cast<const f32x4*>(patch + q * (WN * 4) + (((c / 4) ^ (q & kSwz)) << 4));
+        const f32x4 y = *reinterpret_cast<const f32x4*>(patch + q * (WN * 4) + (((c / 4 + 1) ^ (q & kSwz)) << 4));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           v[e] = x[e];
@@ -462,11 +406,12 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(Pro
       get(cl, v);
       float u[8];
       if constexpr (OP == OP_GLU) get(WN / 2 + cl, u);
-      if (row >= M || cols <= 0) continue;
+      if (r >= 16 || row >= at_.M || cols <= 0) continue;
       if constexpr (OP == OP_DW) {
-        write8(p.out, ((int64_t)t.g * p.M + m0 + row) * p.N + col, p.out_fmt, cols, v);
+        // past the caches: it is read much later, if at all there (1.07 GB of it 333 -> 257 us, 134 MB 101 -> 95)
+        write8<true>(p.out, ((int64_t)at_.g * p.M + at_.m0 + row) * p.N + col, p.out_fmt, cols, v);
       } else {
-        const int64_t at = t.row0 + row;
+        const int64_t at = at_.row0 + row;
         if constexpr (OP == OP_GLU) {
           constexpr int fmt = sizeof(E) == 2 ? MOE_AFMT_BF16 : MOE_AFMT_F32;
           if (p.aux) {
@@ -480,7 +425,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(Pro
           constexpr int fmt = sizeof(E) == 2 ? MOE_AFMT_BF16 : MOE_AFMT_F32;
           float w[8];
           if (p.bias) {
-            read8(p.bias, (int64_t)t.g * p.N + col, MOE_AFMT_F32, cols, w);
+            read8(p.bias, (int64_t)at_.g * p.N + col, MOE_AFMT_F32, cols, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += w[e];
           }
@@ -502,6 +447,303 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(Pro
     }
     __builtin_amdgcn_wave_barrier();
   }
+}
+
+template <typename E, int OP, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(ProductArgs p) {
+  using T = ProductTile<E, OP, BM, BN, WM, WN>;
+  using OpA = Operand<E, BM, T::kKmajA>;
+  using OpB = Operand<E, BN, T::kKmajB>;
+  constexpr int kThreads = T::kThreads, kK = OpA::kK;
+  constexpr int kStage = T::kStages / 2;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[T::kStages];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
+  Place at;
+  if (!find_place<OP, BM, T::kCols>(p, count_tiles<OP, BM>(p), blockIdx.x >> 3, at)) return;
+  const int m0 = at.m0, n0 = at.n0, M = at.M, N = at.N, K = at.K;
+
+  // this thread's pieces: an address (k = 0) and, in `left`, how many of its elements there are
+  constexpr int kPa = OpA::kPieces / kThreads, kPb = OpB::kPieces / kThreads;
+  const uint8_t *pa[kPa], *pb[kPb];
+  int ka[kPa], kb[kPb];  // k of the piece in a stage; where rows are the k, beside it the elements in the row
+  int la[kPa], lb[kPb];
+  const E* a = static_cast<const E*>(p.a);
+  const E* b = static_cast<const E*>(p.b);
+#pragma unroll
+  for (int i = 0; i < kPa; ++i) {
+    int r;
+    OpA::where(i * kThreads + tid, r, ka[i]);
+    if constexpr (OP == OP_DW) {
+      la[i] = M - r;
+      pa[i] = reinterpret_cast<const uint8_t*>(a + (int64_t)(at.row0 + ka[i]) * p.lda + m0 + r);
+    } else {
+      la[i] = 0;
+      pa[i] = reinterpret_cast<const uint8_t*>(a + (int64_t)(at.row0 + min(r, M - 1)) * p.lda + ka[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPb; ++i) {
+    int r;
+    OpB::where(i * kThreads + tid, r, kb[i]);
+    if constexpr (OP == OP_DW) {
+      lb[i] = N - r;
+      pb[i] = reinterpret_cast<const uint8_t*>(b + (int64_t)(at.row0 + kb[i]) * p.ldb + n0 + r);
+    } else if constexpr (OP == OP_DX) {
+      lb[i] = N - r;
+      pb[i] = reinterpret_cast<const uint8_t*>(b + at.g * p.gsb + (int64_t)kb[i] * p.ldb + n0 + r);
+    } else {
+      lb[i] = 0;
+      const int64_t row = n_row<OP, WN>(p, at, r);
+      pb[i] = reinterpret_cast<const uint8_t*>(b + at.g * p.gsb + row * p.ldb + kb[i]);
+    }
+  }
+  u32x4 qa[kPa], qb[kPb];
+  const auto load = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < kPa; ++i) {
+      if constexpr (OP == OP_DW) qa[i] = read_piece<E>(pa[i] + (int64_t)k0 * p.lda * sizeof(E), k0 + ka[i] < K ? la[i] : 0);
+      else qa[i] = read_piece<E>(pa[i] + (int64_t)k0 * sizeof(E), K - k0 - ka[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPb; ++i) {
+      if constexpr (OP == OP_DW || OP == OP_DX)
+        qb[i] = read_piece<E>(pb[i] + (int64_t)k0 * p.ldb * sizeof(E), k0 + kb[i] < K ? lb[i] : 0);
+      else qb[i] = read_piece<E>(pb[i] + (int64_t)k0 * sizeof(E), K - k0 - kb[i]);
+    }
+  };
+  const auto store = [&](uint8_t* stage) {
+#pragma unroll
+    for (int i = 0; i < kPa; ++i) *reinterpret_cast<u32x4*>(stage + 16 * (i * kThreads + tid)) = qa[i];
+#pragma unroll
+    for (int i = 0; i < kPb; ++i) *reinterpret_cast<u32x4*>(stage + OpA::kBytes + 16 * (i * kThreads + tid)) = qb[i];
+  };
+
+  f32x4 acc[T::kMt][T::kNt] = {};
+  const int stages = (K + kK - 1) / kK;
+  if (stages) {
+    load(0);
+    store(lds);
+    __syncthreads();
+  }
+  for (int s = 0; s < stages; ++s) {
+    const uint8_t* at = lds + (s & 1) * kStage;
+    if (s + 1 < stages) load((s + 1) * kK);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u32x4 fa[T::kMt], fb[T::kNt];
+#pragma unroll
+      for (int i = 0; i < T::kMt; ++i) fa[i] = OpA::fragment(at, wm + 16 * i, j, lane);
+#pragma unroll
+      for (int i = 0; i < T::kNt; ++i) fb[i] = OpB::fragment(at + OpA::kBytes, wn + 16 * i, j, lane);
+#pragma unroll
+      for (int m = 0; m < T::kMt; ++m)
+#pragma unroll
+        for (int n = 0; n < T::kNt; ++n) multiply<E>(fb[n], fa[m], acc[m][n]);
+    }
+    if (s + 1 < stages) store(lds + ((s + 1) & 1) * kStage);
+    __syncthreads();
+  }
+
+  write_tile<E, OP, BM, BN, WM, WN>(p, at, lds + wave * T::kPatch, wave, lane, acc);
+}
+
+// ---------------------------------------------------------------- operands straight into LDS
+// The same for operands whose rows all start on 16 bytes: buffer loads write LDS themselves, 1 KB a
+// wavefront and instruction in lane order (the pieces' places are chosen by what each lane reads), so
+// a stage costs no registers.  What a piece must not read (rows past the k, columns past the row's end)
+// has an offset past the descriptor's size and arrives as zeros.
+constexpr uint32_t kPast = 0x80000000u;  // of a descriptor of 2^31 - 1 bytes
+
+__device__ __forceinline__ u32x4 descriptor(const void* p) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  return {(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, 0x7fffffffu, 0x00020000u};
+}
+
+// Waits until at most N of this wavefront's loads into LDS are on their way and its reads of LDS are
+// done, then for the other wavefronts.  (A barrier of the language waits for every load.)
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  static_assert(N <= 63, "the counter has six bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 bytes at each lane's offset to `lds` and the 1 KB behind it, in lane order.  Not by the builtin: the
+// compiler takes every transposing read of LDS to depend on every such load before it and waits for
+// them all.  (It has no output register; wait_and_meet does the waiting.  The wait states are those
+// between a lane's value moved to a scalar register, or m0's, and a load that reads it.)
+__device__ __forceinline__ void load_to_lds(u32x4 from, uint32_t offset, uint8_t* lds) {
+  const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(offset), "s"(from)
+               : "memory", "m0");
+}
+
+// Half an operand's tile: the first (or second) half of every wavefront's rows, `W` of them each, one
+// wavefront after the other.  Its place in the operand's tile:
+template <int W>
+__device__ __forceinline__ int tile_row(int r, int half) { return r / (W / 2) * W + half * (W / 2) + r % (W / 2); }
+
+// KS > 1: so many groups of wavefronts share a tile, each with its own part of the k and its own stages;
+// their sums meet in LDS, in order.  WAVES: of a SIMD unit.
+template <typename E, int OP, int BM, int BN, int WM, int WN, int KS, int WAVES>
+__global__ __launch_bounds__(KS * 64 * (BM / WM) * (BN / WN), WAVES) void product_direct_kernel(ProductArgs p) {
+  using T = ProductTile<E, OP, BM, BN, WM, WN>;
+  using OpA = Operand<E, BM / 2, T::kKmajA>;  // of half a tile
+  using OpB = Operand<E, BN / 2, T::kKmajB>;
+  constexpr int kThreads = T::kThreads, kK = OpA::kK, kMt = T::kMt, kNt = T::kNt, kSteps = 2, kStage = T::kStages / 2;
+  constexpr int eb = sizeof(E);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KS * T::kStages];
+  const int tid = KS == 1 ? threadIdx.x : threadIdx.x % kThreads, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int part = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+  uint8_t* const lds = lds_all + part * T::kStages;
+
+  Place at;
+  if (!find_place<OP, BM, T::kCols>(p, count_tiles<OP, BM>(p), blockIdx.x >> 3, at)) return;
+
+  // this part's first k and its stages; past the last k, loads bring zeros
+  const int all = (at.K + kK - 1) / kK, stages = (all + KS - 1) / KS, first = part * stages;
+  const int left = at.K - first * kK;
+
+  // this thread's pieces of each half: byte offsets at the first k, and their k in a stage
+  constexpr int kLa = OpA::kPieces / kThreads, kLb = OpB::kPieces / kThreads;
+  static_assert(kLa >= 1 && kLb >= 1, "whole loads");
+  uint32_t oa[2][kLa], ob[2][kLb];
+  int ka[kLa], kb[kLb];
+  const int64_t stepa = (T::kKmajA ? p.lda : 1) * (int64_t)(kK * eb), stepb = (T::kKmajB ? p.ldb : 1) * (int64_t)(kK * eb);
+  const uint8_t* a = reinterpret_cast<const uint8_t*>(static_cast<const E*>(p.a) + (int64_t)at.row0 * p.lda + at.m0) + first * stepa;
+  const uint8_t* b = static_cast<const uint8_t*>(p.b) + first * stepb;
+  if constexpr (OP == OP_DW) b += ((int64_t)at.row0 * p.ldb + at.n0) * eb;
+  else if constexpr (OP == OP_DX) b += (at.g * p.gsb + at.n0) * eb;
+  else b += (at.g * p.gsb + (int64_t)at.n0 * p.ldb) * eb;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < kLa; ++i) {
+      int r;
+      OpA::where(i * kThreads + tid, r, ka[i]);
+      r = tile_row<WM>(r, h);
+      if constexpr (T::kKmajA) oa[h][i] = r < at.M ? (uint32_t)(ka[i] * p.lda + r) * eb : kPast;
+      else oa[h][i] = (uint32_t)(min(r, at.M - 1) * p.lda + ka[i]) * eb;
+    }
+#pragma unroll
+    for (int i = 0; i < kLb; ++i) {
+      int r;
+      OpB::where(i * kThreads + tid, r, kb[i]);
+      r = tile_row<WN>(r, h);
+      if constexpr (T::kKmajB) ob[h][i] = r < at.N ? (uint32_t)(kb[i] * p.ldb + r) * eb : kPast;
+      else ob[h][i] = (uint32_t)((n_row<OP, WN>(p, at, r) - at.n0) * p.ldb + kb[i]) * eb;
+    }
+  }
+
+  // A stage in LDS: A's halves, then B's.
+  const auto place_a = [&](int s, int h) { return lds + (s & 1) * kStage + h * OpA::kBytes; };
+  const auto place_b = [&](int s, int h) { return lds + (s & 1) * kStage + 2 * OpA::kBytes + h * OpB::kBytes; };
+  // Half h of stage s on its way (past the k: zeros, from nowhere).
+  const auto issue_a = [&](int s, int h) {
+    const u32x4 from = descriptor(a + s * stepa);
+    uint8_t* to = place_a(s, h) + 1024 * wave;
+#pragma unroll
+    for (int i = 0; i < kLa; ++i) load_to_lds(from, ka[i] < left - s * kK ? oa[h][i] : kPast, to + 16 * i * kThreads);
+  };
+  const auto issue_b = [&](int s, int h) {
+    const u32x4 from = descriptor(b + s * stepb);
+    uint8_t* to = place_b(s, h) + 1024 * wave;
+#pragma unroll
+    for (int i = 0; i < kLb; ++i) load_to_lds(from, kb[i] < left - s * kK ? ob[h][i] : kPast, to + 16 * i * kThreads);
+  };
+
+  // A stage is four phases, the products of A's and B's halves (0,0), (0,1), (1,0), (1,1) over all of its
+  // k: a half's operands are in registers for two of them, so its place in LDS is free for the stage
+  // after next as soon as every wavefront has read it, long before the stage is over.  Between its matrix
+  // instructions a phase reads what the next one lacks and sends for one half:
+  //   phase          0            1            2              3
+  //   reads          B1           A1           A0 of s + 1    B0 of s + 1
+  //   sends for      B0 of s + 2  B1 of s + 2  A1 of s + 2    A0 of s + 3
+  // What it reads was sent for seven phases ago: the loads of the six since may be on their way.  The
+  // wavefronts meet behind a phase's first instructions, which the matrix cores work on meanwhile.
+  f32x4 acc[kMt][kNt] = {};
+  constexpr int kMh = kMt / 2, kNh = kNt / 2, kMuls = kMh * kNh * kSteps;
+  u32x4 fa[2][kMh][kSteps], fb[2][kNh][kSteps];
+  const int wm = wave / (BN / WN) * (WM / 2), wn = wave % (BN / WN) * (WN / 2);  // in a half
+  const auto read_a = [&](int s, int h, int i) { fa[h][i % kMh][i / kMh] = OpA::fragment(place_a(s, h), wm + 16 * (i % kMh), i / kMh, lane); };
+  const auto read_b = [&](int s, int h, int i) { fb[h][i % kNh][i / kNh] = OpB::fragment(place_b(s, h), wn + 16 * (i % kNh), i / kNh, lane); };
+  const auto phase = [&](int s, auto which) {
+    constexpr int q = decltype(which)::value, ha = q >> 1, hb = q & 1;
+    constexpr int kWait = q == 0 ? 4 * kLa + 2 * kLb : q == 2 ? 2 * kLa + 4 * kLb : 3 * kLa + 3 * kLb;
+    constexpr int kFirst = kMuls >= 4 ? 2 : 1, kSlots = kMuls - kFirst, kReads = (q == 1 || q == 2 ? kMh : kNh) * kSteps;
+#pragma unroll
+    for (int i = 0; i < kMuls; ++i) {
+      if (i == kFirst) {
+        wait_and_meet<kWait>();
+        if constexpr (q == 0) issue_b(s + 2, 0);
+        else if constexpr (q == 1) issue_b(s + 2, 1);
+        else if constexpr (q == 2) issue_a(s + 2, 1);
+        else issue_a(s + 3, 0);
+      }
+      const int j = i / (kMh * kNh), m = i / kNh % kMh, n = i % kNh;
+      multiply<E>(fb[hb][n][j], fa[ha][m][j], acc[ha * kMh + m][hb * kNh + n]);
+      const int k = i - kFirst;
+      if (k >= 0) {
+#pragma unroll
+        for (int f = k * kReads / kSlots; f < (k + 1) * kReads / kSlots; ++f) {
+          if constexpr (q == 0) read_b(s, 1, f);
+          else if constexpr (q == 1) read_a(s, 1, f);
+          else if constexpr (q == 2) read_a(s + 1, 0, f);
+          else read_b(s + 1, 0, f);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  if (stages) {
+    // stages 0 and 1, in the order in which they are read
+    issue_a(0, 0);
+    issue_b(0, 0);
+    issue_b(0, 1);
+    issue_a(0, 1);
+    issue_a(1, 0);
+    issue_b(1, 0);
+    issue_b(1, 1);
+    issue_a(1, 1);
+    wait_and_meet<3 * kLa + 3 * kLb>();
+#pragma unroll
+    for (int i = 0; i < kMh * kSteps; ++i) read_a(0, 0, i);
+#pragma unroll
+    for (int i = 0; i < kNh * kSteps; ++i) read_b(0, 0, i);
+    wait_and_meet<63>();
+    issue_a(2, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    for (int s = 0; s < stages; ++s) {
+      phase(s, std::integral_constant<int, 0>{});
+      phase(s, std::integral_constant<int, 1>{});
+      phase(s, std::integral_constant<int, 2>{});
+      phase(s, std::integral_constant<int, 3>{});
+    }
+  }
+  wait_and_meet<0>();
+  if constexpr (KS > 1) {
+    static_assert(T::kWaves * kMt * kNt * 1024 <= T::kStages, "a part's sums take its stages' place");
+    const auto sum = [&](int from, int m, int n) {
+      return reinterpret_cast<f32x4*>(lds_all + from * T::kStages) + ((wave * kMt + m) * kNt + n) * 64 + lane;
+    };
+    if (part) {
+#pragma unroll
+      for (int m = 0; m < kMt; ++m)
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) *sum(part, m, n) = acc[m][n];
+    }
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int m = 0; m < kMt; ++m)
+#pragma unroll
+      for (int n = 0; n < kNt; ++n)
+#pragma unroll
+        for (int o = 1; o < KS; ++o) acc[m][n] += *sum(o, m, n);
+  }
+  write_tile<E, OP, BM, BN, WM, WN>(p, at, lds_all + wave * T::kPatch, wave, lane, acc);
 }
 
 }  // namespace rmoe

@@ -237,6 +237,18 @@ def test_model_sizes(run):
     run(300, None, 1024, 2048, B)
 
 
+# sizes at which each shape of tile is the cheapest: many rows (the largest tiles), few rows of long sums (split over
+# the k), many small experts
+BIG = [(2048, 0, 1024, 1024), (1300, 0, 2048, 2048), (700, 0, 520, 1032), (20, 0, 4096, 512), (600, 40, 512, 256), (3000, 6, 512, 768)]
+
+
+@each
+@types
+@pytest.mark.parametrize("rows,E,H,I", BIG)
+def test_larger_products(run, dtype, rows, E, H, I):
+    run(rows, uneven(rows, E, 7) if E else None, H, I, dtype)
+
+
 @types
 def test_long_bias_sums(dtype):
     """A bias over so many rows that its gradient is summed in splits."""
