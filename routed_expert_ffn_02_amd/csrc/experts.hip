@@ -28,20 +28,11 @@ __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restric
   const int end = offsets ? min(max(offsets[E], 0), rows) : rows;
   if (c >= n) return;
   const int all = GLU ? 2 * n : n;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = blockIdx.x * 8 + 4 * i + (threadIdx.x >> 6);
-    if (row >= end) return;
-    if (c + 8 >= n)  // the last of the row
-      for (int e = all; e < ld_d; ++e) {
-        if (fmt == MOE_AFMT_BF16) static_cast<uint16_t*>(d)[row * ld_d + e] = 0;
-        else static_cast<float*>(d)[row * ld_d + e] = 0.f;
-      }
-    float g[8], v[8];
+  for (int row = 4 * blockIdx.x + (threadIdx.x >> 6); row < end; row += 4 * gridDim.x) {
+    float g[8], u[8], v[8];
     read8(dy, (int64_t)row * ld_dy + c, dy_fmt, n - c, v);
+    if (GLU || act != MOE_ACT_NONE) read8(z, (int64_t)row * ld_z + c, fmt, n - c, g);
     if constexpr (GLU) {
-      float u[8];
-      read8(z, (int64_t)row * ld_z + c, fmt, n - c, g);
       read8(z, (int64_t)row * ld_z + n + c, fmt, n - c, u);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -53,22 +44,26 @@ __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restric
       write8(d, (int64_t)row * ld_d + n + c, fmt, n - c, v);
     } else {
       if (act != MOE_ACT_NONE) {
-        read8(z, (int64_t)row * ld_z + c, fmt, n - c, g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= act_of(g[e], act).grad;
       }
       write8(d, (int64_t)row * ld_d + c, fmt, n - c, v);
     }
+    if (c + 8 >= n)  // the last of the row
+      for (int e = all; e < ld_d; ++e) {
+        if (fmt == MOE_AFMT_BF16) static_cast<uint16_t*>(d)[row * ld_d + e] = 0;
+        else static_cast<float*>(d)[row * ld_d + e] = 0.f;
+      }
   }
 }
 
 // ---------------------------------------------------------------- the bias's gradient
 // Column sums of dz in fp32, from dy and z as given (dz is not rounded here).  A workgroup has 64
 // columns, eight lanes of eight, and 32 rows at once; its rows' sums meet in LDS in a fixed order.
-// Splits of a long expert write their own sums, which bias_join adds in order: 128 rows a split and
+// Splits of a long expert write their own sums, which bias_join adds in order: 32 rows a split and
 // more, up to 64 splits, put about as many loads in flight as there are (777 rows of 1001 in bf16 with
-// gelu: 19 us in one split of sixteen wavefronts).
-constexpr int kBiasRows = 128;  // rows of a split, at least
+// gelu: 19 us in one split of sixteen wavefronts, 12 in splits of 128 rows).
+constexpr int kBiasRows = 32;  // rows of a split, at least
 
 __global__ __launch_bounds__(256) void bias_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
                                                             const void* __restrict__ z, int fmt, int64_t ld_z,
@@ -197,7 +192,7 @@ constexpr TileCost kCosts[2][3][TILES] = {
 static_assert(MOE_AFMT_F32 == 0 && MOE_AFMT_BF16 == 1, "kCosts' first index");
 
 template <typename E, int OP>
-int choose_tile(const ProductArgs& p, std::initializer_list<int> from) {
+int choose_tile(const ProductArgs& p, std::initializer_list<int> from, float* estimate) {
   constexpr int kCus = 256, kK = 128 / sizeof(E);
   const TileCost* costs = kCosts[sizeof(E) == 2][OP == OP_DW ? 2 : OP == OP_DX];
   const float rows = p.rows, used = std::min(p.E, p.rows);  // experts with a row, at most
@@ -218,19 +213,45 @@ int choose_tile(const ProductArgs& p, std::initializer_list<int> from) {
       least = time;
     }
   }
+  *estimate = least;
   return best;
+}
+
+// Whether few_rows_kernel is the faster one: its time is a launch and the CU's share of workgroups, each of
+// which reads sixteen rows of weights.  Measured against the tiles (us, bf16): one row of 512 x 2048 4.9 and
+// 5.3, sixteen 6.2 and 5.3; one row of 2048 x 1024 4.8 and 9.3, 64 rows 6.5 and 9.9; one row of 4096 x 4096 7.8
+// and 14.9, 64 rows 31 and 16.
+template <typename E, int OP>
+bool few_rows_ok(const ProductArgs& p, float tiles_time) {
+  if constexpr (OP != OP_GLU && OP != OP_LINEAR) return false;
+  if (p.K % (16 / (int)sizeof(E))) return false;
+  const float used = std::min(p.E, p.rows), mt = p.E == 1 ? std::ceil(p.rows / 16.f) : std::max(p.rows / 16.f + .5f * used, used);
+  const float per_cu = std::ceil(mt * ((p.N + kFewCols<OP> - 1) / kFewCols<OP>) / 256);
+  return 3.9f + .06f * std::min(p.rows, 16) + per_cu * (.5f + .7e-3f * sizeof(E) * p.K) < tiles_time;
+}
+
+template <typename E, int OP>
+moe_status few_rows(ProductArgs p, hipStream_t s) {
+  if constexpr (OP == OP_GLU || OP == OP_LINEAR) {
+    const int64_t tiles = tiles_of<OP, 16, kFewCols<OP>>(p), blocks = (tiles + 7) / 8 * 8;
+    if (blocks > kMaxBlocks) return MOE_EINVAL;
+    p.tiles = (uint32_t)tiles;
+    return launch(few_rows_kernel<E, OP>, dim3((unsigned)blocks), dim3(64 * kFewWaves), s, p);
+  }
+  return MOE_EINVAL;
 }
 
 template <typename E, int OP>
 moe_status product_of(const ProductArgs& p, hipStream_t s) {
+  float time;
   if (direct_ok<E, OP>(p)) {
     int tile;
+    if constexpr (sizeof(E) == 2) tile = choose_tile<E, OP>(p, {TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &time);
+    else tile = choose_tile<E, OP>(p, {TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &time);
+    if (few_rows_ok<E, OP>(p, time)) return few_rows<E, OP>(p, s);
     if constexpr (sizeof(E) == 2) {
-      tile = choose_tile<E, OP>(p, {TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS});
       if (tile == TILE_256) return direct<E, OP, 256, 256, 128, 64, 1, 1>(p, s);
       if (tile == TILE_128_256) return direct<E, OP, 128, 256, 64, 64, 1, 1>(p, s);
-    } else {
-      tile = choose_tile<E, OP>(p, {TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS});
     }
     if (tile == TILE_128) return direct<E, OP, 128, 128, 64, 64, 1, 2>(p, s);
     if (tile == TILE_64_128) return direct<E, OP, 64, 128, 32, 64, 1, 3>(p, s);
@@ -239,7 +260,9 @@ moe_status product_of(const ProductArgs& p, hipStream_t s) {
   }
   // rows that start anywhere: 4096 x 2048 x 4096 in bf16 176 us in 128 x 128, 250 in 64 x 64; the gradient of 333 x
   // 999 x 257 in fp32 74 us and 39
-  if (choose_tile<E, OP>(p, {TILE_128, TILE_64}) == TILE_64) return staged<E, OP, 64, 64, 32, 32>(p, s);
+  const int tile = choose_tile<E, OP>(p, {TILE_128, TILE_64}, &time);
+  if (few_rows_ok<E, OP>(p, time)) return few_rows<E, OP>(p, s);
+  if (tile == TILE_64) return staged<E, OP, 64, 64, 32, 32>(p, s);
   return staged<E, OP, 128, 128, 64, 64>(p, s);
 }
 template <int OP>
@@ -359,7 +382,7 @@ moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz,
 template <bool GLU>
 moe_status pre_gradient(const moe_product_config* c, const Dims& d, const void* dy, int dy_fmt, const void* z,
                         const int32_t* offsets, void* out, int64_t ld_d, hipStream_t s) {
-  const dim3 grid((unsigned)((c->rows + 7) / 8), (unsigned)((c->N + 511) / 512));
+  const dim3 grid((unsigned)std::min((c->rows + 3) / 4, 1 << 22), (unsigned)((c->N + 511) / 512));
   return launch(pre_gradient_kernel<GLU>, grid, dim3(256), s, dy, dy_fmt, d.ld_y, z, c->fmt, d.ld_z, offsets, c->rows,
                 c->n_experts, c->N, c->act, out, ld_d);
 }

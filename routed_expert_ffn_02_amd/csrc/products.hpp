@@ -118,6 +118,11 @@ __device__ __forceinline__ void write8(void* base, int64_t at, int fmt, int n, c
   }
 }
 
+__device__ __forceinline__ void write1(void* base, int64_t at, int fmt, float v) {
+  if (fmt == MOE_AFMT_BF16) static_cast<uint16_t*>(base)[at] = (uint16_t)pack_bf16(v, v);
+  else static_cast<float*>(base)[at] = v;
+}
+
 // ---------------------------------------------------------------- experts' rows and tiles
 // Expert g's rows as the offsets say, brought into [0, rows]: whatever the table holds, nothing
 // outside the rows is read or written.
@@ -744,6 +749,81 @@ __global__ __launch_bounds__(KS * 64 * (BM / WM) * (BN / WN), WAVES) void produc
         for (int o = 1; o < KS; ++o) acc[m][n] += *sum(o, m, n);
   }
   write_tile<E, OP, BM, BN, WM, WN>(p, at, lds_all + wave * T::kPatch, wave, lane, acc);
+}
+
+// ---------------------------------------------------------------- few rows
+// One token's products, or a few tokens': the weights are read once and everything else is small, so a
+// workgroup has sixteen rows of weights (eight outputs' gate and up, or sixteen outputs) and up to
+// sixteen rows of x, its eight wavefronts deal out the k in lines of 128 bytes, and operands go from
+// memory to registers: no stage to fill, no barrier but the one before the wavefronts' sums are added, in
+// order.  Loads of four lines are on their way at once.  (Thirty-two rows of x a workgroup were slower at
+// almost every size.)
+constexpr int kFewWaves = 8, kFewLines = 4;
+template <int OP>
+constexpr int kFewCols = OP == OP_GLU ? 8 : 16;
+
+template <typename E, int OP>
+__global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(ProductArgs p) {
+  constexpr int kEl = 16 / sizeof(E), kLine = 128 / sizeof(E), kCols = kFewCols<OP>;
+  __shared__ f32x4 sums[kFewWaves][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Place at;
+  if (!find_place<OP, 16, kCols>(p, count_tiles<OP, 16>(p), blockIdx.x >> 3, at)) return;
+  const int r = lane & 15, q = lane >> 4, K = p.K;
+  const int64_t wrow = at.n0 + min(r % kCols, at.N - 1) + (r < kCols ? 0 : p.N);
+  const uint8_t* pw = reinterpret_cast<const uint8_t*>(static_cast<const E*>(p.b) + at.g * p.gsb + wrow * p.ldb);
+  const uint8_t* px = reinterpret_cast<const uint8_t*>(static_cast<const E*>(p.a) + (int64_t)(at.row0 + min(r, at.M - 1)) * p.lda);
+  f32x4 acc = {};
+  const int lines = (K + kLine - 1) / kLine;
+  for (int l0 = wave; l0 < lines; l0 += kFewWaves * kFewLines) {
+    u32x4 w[kFewLines][2], x[kFewLines][2];
+#pragma unroll
+    for (int l = 0; l < kFewLines; ++l)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // a piece past the k is the row's last one instead, and then zeros
+        const int64_t k = (int64_t)min((l0 + l * kFewWaves) * kLine + (4 * j + q) * kEl, K - kEl) * sizeof(E);
+        w[l][j] = load16<false>(pw + k);
+        x[l][j] = load16<false>(px + k);
+      }
+#pragma unroll
+    for (int l = 0; l < kFewLines; ++l)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool in = (l0 + l * kFewWaves) * kLine + (4 * j + q) * kEl < K;
+        multiply<E>(in ? w[l][j] : u32x4{0, 0, 0, 0}, in ? x[l][j] : u32x4{0, 0, 0, 0}, acc);
+      }
+  }
+  sums[wave][lane] = acc;
+  __syncthreads();
+  // a lane of the sums has rows of weights 4 (l / 16) + 0..3 of x's row l % 16; here, one output a thread
+  const int row = threadIdx.x / kCols, c = threadIdx.x % kCols;
+  if (row >= at.M || c >= at.N) return;
+  const auto sum = [&](int n) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kFewWaves; ++k) v += sums[k][row + 16 * (n >> 2)][n & 3];
+    return v;
+  };
+  const int64_t i = at.row0 + row;
+  const int col = at.n0 + c;
+  constexpr int fmt = sizeof(E) == 2 ? MOE_AFMT_BF16 : MOE_AFMT_F32;
+  float v = sum(c);
+  if constexpr (OP == OP_GLU) {
+    const float u = sum(c + kCols);
+    if (p.aux) {
+      write1(p.aux, i * p.ld_aux + col, fmt, v);
+      write1(p.aux, i * p.ld_aux + p.N + col, fmt, u);
+    }
+    write1(p.out, i * p.ldo + col, fmt, act_of(v, p.act).value * u);
+  } else {
+    if (p.bias) v += p.bias[(int64_t)at.g * p.N + col];
+    if (p.aux) write1(p.aux, i * p.ld_aux + col, fmt, v);
+    v = act_of(v, p.act).value;
+    if (p.residual) v += p.out_fmt == MOE_AFMT_BF16 ? load_act<MOE_AFMT_BF16>(p.residual, i * p.ld_res + col)
+                                                    : load_act<MOE_AFMT_F32>(p.residual, i * p.ld_res + col);
+    write1(p.out, i * p.ldo + col, p.out_fmt, v);
+  }
 }
 
 }  // namespace rmoe

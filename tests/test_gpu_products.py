@@ -249,6 +249,19 @@ def test_larger_products(run, dtype, rows, E, H, I):
     run(rows, uneven(rows, E, 7) if E else None, H, I, dtype)
 
 
+# few rows: each over a long sum, with and without experts, sizes at the edges of its workgroups
+FEW = [(1, 0, 2048, 512), (1, 0, 4096, 100), (3, 0, 1024, 17), (16, 0, 2056, 64), (17, 0, 2048, 40), (50, 0, 4096, 24), (6, 4, 2048, 72),
+       (20, 9, 1024, 48), (40, 2, 4096, 33)]
+
+
+@pytest.mark.parametrize("run", [run_glu, run_linear])
+@types
+@hows
+@pytest.mark.parametrize("rows,E,H,I", FEW)
+def test_few_rows(run, dtype, how, rows, E, H, I):
+    run(rows, uneven(rows, E, rows // 6) if E else None, H, I, dtype, how, act="gelu")
+
+
 @types
 def test_long_bias_sums(dtype):
     """A bias over so many rows that its gradient is summed in splits."""
