@@ -119,7 +119,7 @@ int bias_splits(int64_t rows, int E) {
 }
 
 // ---------------------------------------------------------------- launches
-constexpr int64_t kMaxBlocks = (1ll << 32) / 256 - 1;  // a launch's threads are counted in 32 bits
+constexpr int64_t kMaxThreads = (1ll << 32) - 1;  // a launch's are counted in 32 bits
 
 // Row tiles of BM (every expert with a row may end in a part of one) and the grid over them.
 template <int OP, int BM, int COLS>
@@ -135,7 +135,7 @@ moe_status run_tiles(void (*kernel)(ProductArgs), ProductArgs p, int threads, hi
   // whole runs on every XCD
   const int64_t eight = 8 * (OP == OP_DW ? (int64_t)dealt_run((uint32_t)std::min<int64_t>(tiles / p.E, 1 << 30)) : 1);
   const int64_t blocks = (tiles + eight - 1) / eight * eight;
-  if (blocks > kMaxBlocks) return MOE_EINVAL;
+  if (blocks * threads > kMaxThreads) return MOE_EINVAL;
   p.tiles = (uint32_t)tiles;
   return launch(kernel, dim3((unsigned)blocks), dim3(threads), s, p);
 }
@@ -184,11 +184,11 @@ constexpr TileCost kCosts[2][3][TILES] = {
      {{}, {}, {128, 128, 2, 1, 2.47f, 2.39f, 1.80f}, {64, 128, 3, 1, 2.74f, 1.06f, .90f}, {64, 64, 5, 1, 2.92f, .88f, .45f}, {64, 64, 1, 4, 4.13f, 1.77f, 1.69f}},
      {{}, {}, {128, 128, 2, 1, 4.41f, 2.39f, 1.48f}, {64, 128, 3, 1, 2.91f, 1.09f, .74f}, {64, 64, 5, 1, 1.95f, .99f, .42f}, {64, 64, 1, 4, 4.77f, 1.77f, 1.58f}}},
     {{{256, 256, 1, 1, 4.33f, .90f, 1.64f}, {128, 256, 1, 1, 4.11f, .61f, .94f}, {128, 128, 2, 1, 4.19f, .56f, .47f}, {64, 128, 3, 1, 3.18f, .31f, .29f},
-      {64, 64, 5, 1, 2.77f, .32f, .20f}, {64, 64, 1, 4, 4.46f, .60f, .56f}},
+      {64, 64, 5, 1, 2.77f, .32f, .20f}, {64, 64, 1, 4, 5.f, .75f, .56f}},
      {{256, 256, 1, 1, 3.75f, 1.44f, 1.35f}, {128, 256, 1, 1, 5.08f, .68f, .79f}, {128, 128, 2, 1, 2.47f, .43f, .44f}, {64, 128, 3, 1, 3.06f, .57f, .25f},
-      {64, 64, 5, 1, 3.51f, .26f, .21f}, {64, 64, 1, 4, 3.85f, .80f, .92f}},
+      {64, 64, 5, 1, 3.51f, .26f, .21f}, {64, 64, 1, 4, 5.f, .90f, .92f}},
      {{256, 256, 1, 1, 3.75f, .94f, 1.54f}, {128, 256, 1, 1, 3.58f, .70f, 1.f}, {128, 128, 2, 1, 3.38f, .67f, .58f}, {64, 128, 3, 1, 3.51f, .45f, .40f},
-      {64, 64, 5, 1, 2.98f, .46f, .20f}, {64, 64, 1, 4, 5.07f, .66f, .81f}}}};
+      {64, 64, 5, 1, 2.98f, .46f, .20f}, {64, 64, 1, 4, 5.f, 1.05f, .81f}}}};
 static_assert(MOE_AFMT_F32 == 0 && MOE_AFMT_BF16 == 1, "kCosts' first index");
 
 template <typename E, int OP>
@@ -234,7 +234,7 @@ template <typename E, int OP>
 moe_status few_rows(ProductArgs p, hipStream_t s) {
   if constexpr (OP == OP_GLU || OP == OP_LINEAR) {
     const int64_t tiles = tiles_of<OP, 16, kFewCols<OP>>(p), blocks = (tiles + 7) / 8 * 8;
-    if (blocks > kMaxBlocks) return MOE_EINVAL;
+    if (blocks * 64 * kFewWaves > kMaxThreads) return MOE_EINVAL;
     p.tiles = (uint32_t)tiles;
     return launch(few_rows_kernel<E, OP>, dim3((unsigned)blocks), dim3(64 * kFewWaves), s, p);
   }

@@ -505,15 +505,22 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(Pro
   }
   u32x4 qa[kPa], qb[kPb];
   const auto load = [&](int k0) {
+    // a stage inside the operands, as most are, is loads without a branch between them
+    if (k0 + kK <= K && (!T::kKmajA || M == BM) && (!T::kKmajB || N == BN)) {
+#pragma unroll
+      for (int i = 0; i < kPa; ++i) qa[i] = load16<false>(pa[i] + (int64_t)k0 * (T::kKmajA ? p.lda : 1) * sizeof(E));
+#pragma unroll
+      for (int i = 0; i < kPb; ++i) qb[i] = load16<false>(pb[i] + (int64_t)k0 * (T::kKmajB ? p.ldb : 1) * sizeof(E));
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kPa; ++i) {
-      if constexpr (OP == OP_DW) qa[i] = read_piece<E>(pa[i] + (int64_t)k0 * p.lda * sizeof(E), k0 + ka[i] < K ? la[i] : 0);
+      if constexpr (T::kKmajA) qa[i] = read_piece<E>(pa[i] + (int64_t)k0 * p.lda * sizeof(E), k0 + ka[i] < K ? la[i] : 0);
       else qa[i] = read_piece<E>(pa[i] + (int64_t)k0 * sizeof(E), K - k0 - ka[i]);
     }
 #pragma unroll
     for (int i = 0; i < kPb; ++i) {
-      if constexpr (OP == OP_DW || OP == OP_DX)
-        qb[i] = read_piece<E>(pb[i] + (int64_t)k0 * p.ldb * sizeof(E), k0 + kb[i] < K ? lb[i] : 0);
+      if constexpr (T::kKmajB) qb[i] = read_piece<E>(pb[i] + (int64_t)k0 * p.ldb * sizeof(E), k0 + kb[i] < K ? lb[i] : 0);
       else qb[i] = read_piece<E>(pb[i] + (int64_t)k0 * sizeof(E), K - k0 - kb[i]);
     }
   };
