@@ -112,6 +112,20 @@ __global__ __launch_bounds__(256) void bias_join_kernel(const float* __restrict_
   out[i] = s;
 }
 
+// The sums of splits over the k, in order: [splits][rows][n] in fp32, of which rows between the first
+// expert's and the last one's are written (offsets NULL: all).
+__global__ __launch_bounds__(256) void split_join_kernel(const float* __restrict__ part, int64_t plane, int splits,
+                                                         const int32_t* __restrict__ offsets, int E, int rows, int n,
+                                                         void* __restrict__ out, int64_t ldo, int fmt) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int row = (int)(i / n), col = (int)(i - (int64_t)row * n);
+  if (row >= rows || (offsets && (row < offsets[0] || row >= offsets[E]))) return;
+  float s = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < splits; ++k) s += part[k * plane + i];
+  write1(out, row * ldo + col, fmt, s);
+}
+
 namespace {
 
 int bias_splits(int64_t rows, int E) {
@@ -135,9 +149,9 @@ moe_status run_tiles(void (*kernel)(ProductArgs), ProductArgs p, int threads, hi
   // whole runs on every XCD
   const int64_t eight = 8 * (OP == OP_DW ? (int64_t)dealt_run((uint32_t)std::min<int64_t>(tiles / p.E, 1 << 30)) : 1);
   const int64_t blocks = (tiles + eight - 1) / eight * eight;
-  if (blocks * threads > kMaxThreads) return MOE_EINVAL;
+  if (blocks * threads * p.splits > kMaxThreads) return MOE_EINVAL;
   p.tiles = (uint32_t)tiles;
-  return launch(kernel, dim3((unsigned)blocks), dim3(threads), s, p);
+  return launch(kernel, dim3((unsigned)blocks, p.splits), dim3(threads), s, p);
 }
 
 // Whether the operands' rows start on 16 bytes, whole pieces make up every row (a d of the workspace
@@ -160,10 +174,10 @@ moe_status direct(const ProductArgs& p, hipStream_t s) {
   using T = ProductTile<E, OP, BM, BN, WM, WN>;
   return run_tiles<T, OP, BM>(product_direct_kernel<E, OP, BM, BN, WM, WN, KS, KS * T::kWaves * PER_CU / 4>, p, KS * T::kThreads, s);
 }
-template <typename E, int OP, int BM, int BN, int WM, int WN>
+template <typename E, int OP, int BM, int BN, int WM, int WN, int DEPTH>
 moe_status staged(const ProductArgs& p, hipStream_t s) {
   using T = ProductTile<E, OP, BM, BN, WM, WN>;
-  return run_tiles<T, OP, BM>(product_kernel<E, OP, BM, BN, WM, WN>, p, T::kThreads, s);
+  return run_tiles<T, OP, BM>(product_kernel<E, OP, BM, BN, WM, WN, DEPTH>, p, T::kThreads, s);
 }
 
 // A tile's shape, chosen by its estimated time: rounds of workgroups x what a tile costs beside its
@@ -172,50 +186,71 @@ moe_status staged(const ProductArgs& p, hipStream_t s) {
 // rows, up to 256 experts, sizes 512 to 8192), where the choice is within 1 to 3% of the best shape on
 // average and 21% at worst.  In bf16, 4096^3: 256 x 256 107 us, 128 x 256 122, 128 x 128 124, 64 x 128
 // 161, 64 x 64 199; 1024 x 4096 x 4096: 86, 53, 44, 44, 54; one row of 4096 x 4096: 83, 50, 37, 28, 24,
-// and 17 where four groups of wavefronts share the k.
+// and 17 where four groups of wavefronts share the k.  The last two are product_kernel's: 2048^3 in bf16
+// with rows of 2047 takes 44 us forward, 39 and 38 the gradients, where rows on 16 bytes take 25, 26 and 26.
 struct TileCost {
   int bm, bn, per_cu, parts;
   float fixed, alone, shared;
 };
-enum { TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS, TILES };
+enum { TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS, STAGED_128, STAGED_64, TILES };
 constexpr TileCost kCosts[2][3][TILES] = {
-    {// fp32: forward, rows' gradient, weights' gradient (the two large shapes have no kernel)
-     {{}, {}, {128, 128, 2, 1, 2.47f, 2.33f, 1.96f}, {64, 128, 3, 1, 2.09f, .90f, 1.f}, {64, 64, 5, 1, 3.51f, .62f, .50f}, {64, 64, 1, 4, 4.71f, 1.77f, 1.87f}},
-     {{}, {}, {128, 128, 2, 1, 2.47f, 2.39f, 1.80f}, {64, 128, 3, 1, 2.74f, 1.06f, .90f}, {64, 64, 5, 1, 2.92f, .88f, .45f}, {64, 64, 1, 4, 4.13f, 1.77f, 1.69f}},
-     {{}, {}, {128, 128, 2, 1, 4.41f, 2.39f, 1.48f}, {64, 128, 3, 1, 2.91f, 1.09f, .74f}, {64, 64, 5, 1, 1.95f, .99f, .42f}, {64, 64, 1, 4, 4.77f, 1.77f, 1.58f}}},
+    {// fp32: forward, rows' gradient, weights' gradient (no kernel: {})
+     {{}, {}, {128, 128, 2, 1, 2.47f, 2.33f, 1.96f}, {64, 128, 3, 1, 2.09f, .90f, 1.f}, {64, 64, 5, 1, 3.51f, .62f, .50f}, {64, 64, 1, 4, 4.71f, 1.77f, 1.87f},
+      {}, {64, 64, 3, 1, 4.63f, .75f, .59f}},
+     {{}, {}, {128, 128, 2, 1, 2.47f, 2.39f, 1.80f}, {64, 128, 3, 1, 2.74f, 1.06f, .90f}, {64, 64, 5, 1, 2.92f, .88f, .45f}, {64, 64, 1, 4, 4.13f, 1.77f, 1.69f},
+      {}, {64, 64, 3, 1, 4.50f, .78f, .57f}},
+     {{}, {}, {128, 128, 2, 1, 4.41f, 2.39f, 1.48f}, {64, 128, 3, 1, 2.91f, 1.09f, .74f}, {64, 64, 5, 1, 1.95f, .99f, .42f}, {64, 64, 1, 4, 4.77f, 1.77f, 1.58f},
+      {}, {64, 64, 3, 1, 5.43f, .78f, .61f}}},
     {{{256, 256, 1, 1, 4.33f, .90f, 1.64f}, {128, 256, 1, 1, 4.11f, .61f, .94f}, {128, 128, 2, 1, 4.19f, .56f, .47f}, {64, 128, 3, 1, 3.18f, .31f, .29f},
-      {64, 64, 5, 1, 2.77f, .32f, .20f}, {64, 64, 1, 4, 5.f, .75f, .56f}},
+      {64, 64, 5, 1, 2.77f, .32f, .20f}, {64, 64, 1, 4, 5.f, .75f, .56f},
+      {128, 128, 2, 1, 6.39f, .91f, 1.06f}, {64, 64, 3, 1, 3.91f, .52f, .32f}},
      {{256, 256, 1, 1, 3.75f, 1.44f, 1.35f}, {128, 256, 1, 1, 5.08f, .68f, .79f}, {128, 128, 2, 1, 2.47f, .43f, .44f}, {64, 128, 3, 1, 3.06f, .57f, .25f},
-      {64, 64, 5, 1, 3.51f, .26f, .21f}, {64, 64, 1, 4, 5.f, .90f, .92f}},
+      {64, 64, 5, 1, 3.51f, .26f, .21f}, {64, 64, 1, 4, 5.f, .90f, .92f},
+      {128, 128, 2, 1, 6.85f, .46f, .89f}, {64, 64, 3, 1, 4.00f, .61f, .25f}},
      {{256, 256, 1, 1, 3.75f, .94f, 1.54f}, {128, 256, 1, 1, 3.58f, .70f, 1.f}, {128, 128, 2, 1, 3.38f, .67f, .58f}, {64, 128, 3, 1, 3.51f, .45f, .40f},
-      {64, 64, 5, 1, 2.98f, .46f, .20f}, {64, 64, 1, 4, 5.f, 1.05f, .81f}}}};
+      {64, 64, 5, 1, 2.98f, .46f, .20f}, {64, 64, 1, 4, 5.f, 1.05f, .81f},
+      {128, 128, 2, 1, 7.42f, .86f, .58f}, {64, 64, 3, 1, 4.44f, .63f, .31f}}}};
 static_assert(MOE_AFMT_F32 == 0 && MOE_AFMT_BF16 == 1, "kCosts' first index");
+
+// Row tiles of `bm` that rows over E experts come to, about.
+float row_tiles(int64_t rows, int E, int bm) {
+  const float used = std::min<int64_t>(E, rows);  // experts with a row, at most
+  return E == 1 ? std::ceil((float)rows / bm) : std::max((float)rows / bm + .5f * used, used);
+}
+float tile_time(const TileCost& c, float tiles, float stages) {
+  return std::ceil(tiles / (kCus * c.per_cu)) * c.fixed + std::ceil(stages / c.parts) * std::max(c.alone, std::ceil(tiles / kCus) * c.shared);
+}
+template <typename E, int OP>
+const TileCost* costs_of() { return kCosts[sizeof(E) == 2][OP == OP_DW ? 2 : OP == OP_DX]; }
+template <typename E, int OP>
+float stages_of(const ProductArgs& p) { return std::ceil((OP == OP_DW ? (float)p.rows / p.E : p.K) / (128 / (int)sizeof(E))); }
+template <int OP>
+float tiles_like(const ProductArgs& p, int bm, int bn) {
+  const int cols = OP == OP_GLU ? bn / 2 : bn;
+  return (OP == OP_DW ? (float)p.E * ((p.M + bm - 1) / bm) : row_tiles(p.rows, p.E, bm)) * ((p.N + cols - 1) / cols);
+}
 
 template <typename E, int OP>
 int choose_tile(const ProductArgs& p, std::initializer_list<int> from, float* estimate) {
-  constexpr int kCus = 256, kK = 128 / sizeof(E);
-  const TileCost* costs = kCosts[sizeof(E) == 2][OP == OP_DW ? 2 : OP == OP_DX];
-  const float rows = p.rows, used = std::min(p.E, p.rows);  // experts with a row, at most
+  const float stages = stages_of<E, OP>(p);
   int best = -1;
-  float least = 0;
   for (const int i : from) {
-    const TileCost& c = costs[i];
-    const int cols = OP == OP_GLU ? c.bn / 2 : c.bn;
-    const float nt = (p.N + cols - 1) / cols;
-    const float mt = OP == OP_DW  ? (float)p.E * ((p.M + c.bm - 1) / c.bm)
-                     : p.E == 1 ? std::ceil(rows / c.bm)
-                                : std::max(rows / c.bm + .5f * used, used);
-    const float k = OP == OP_DW ? rows / p.E : p.K, stages = std::ceil(std::ceil(k / kK) / c.parts);
-    const float tiles = mt * nt, time = std::ceil(tiles / (kCus * c.per_cu)) * c.fixed +
-                                        stages * std::max(c.alone, std::ceil(tiles / kCus) * c.shared);
-    if (best < 0 || time < least) {
+    const TileCost& c = costs_of<E, OP>()[i];
+    const float time = tile_time(c, tiles_like<OP>(p, c.bm, c.bn), stages);
+    if (best < 0 || time < *estimate) {
       best = i;
-      least = time;
+      *estimate = time;
     }
   }
-  *estimate = least;
   return best;
 }
+
+// A gradient with few tiles and a long k is cut along the k: 64 x 64 tiles times splits fill the CUs once, each
+// split writes its own fp32 sums (some 4 MB in all) to the workspace, and a kernel adds them in order.  From the
+// sizes alone, as the workspace's size is; 1: not at all.  Whole calls in bf16, uncut and cut: dx of 17 rows of
+// 1023 from 4095 45 us and 12, dw of 511 x 511 from 4096 rows 51 and 26; in fp32 107 and 16, 113 and 43.
+constexpr float kJoinUs = 4.f;  // the second launch
+int splits_for(float tiles, float stages) { return (int)std::clamp(std::min(kCus / tiles, stages / 2), 1.f, 64.f); }
 
 // Whether few_rows_kernel is the faster one: its time is a launch and the CU's share of workgroups, each of
 // which reads sixteen rows of weights.  Measured against the tiles (us, bf16): one row of 512 x 2048 4.9 and
@@ -225,8 +260,7 @@ template <typename E, int OP>
 bool few_rows_ok(const ProductArgs& p, float tiles_time) {
   if constexpr (OP != OP_GLU && OP != OP_LINEAR) return false;
   if (p.K % (16 / (int)sizeof(E))) return false;
-  const float used = std::min(p.E, p.rows), mt = p.E == 1 ? std::ceil(p.rows / 16.f) : std::max(p.rows / 16.f + .5f * used, used);
-  const float per_cu = std::ceil(mt * ((p.N + kFewCols<OP> - 1) / kFewCols<OP>) / 256);
+  const float per_cu = std::ceil(row_tiles(p.rows, p.E, 16) * ((p.N + kFewCols<OP> - 1) / kFewCols<OP>) / kCus);
   return 3.9f + .06f * std::min(p.rows, 16) + per_cu * (.5f + .7e-3f * sizeof(E) * p.K) < tiles_time;
 }
 
@@ -242,32 +276,54 @@ moe_status few_rows(ProductArgs p, hipStream_t s) {
 }
 
 template <typename E, int OP>
-moe_status product_of(const ProductArgs& p, hipStream_t s) {
+moe_status product_of(ProductArgs p, float* part, hipStream_t s) {
+  p.splits = 1;
   float time;
-  if (direct_ok<E, OP>(p)) {
-    int tile;
-    if constexpr (sizeof(E) == 2) tile = choose_tile<E, OP>(p, {TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &time);
-    else tile = choose_tile<E, OP>(p, {TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &time);
-    if (few_rows_ok<E, OP>(p, time)) return few_rows<E, OP>(p, s);
-    if constexpr (sizeof(E) == 2) {
-      if (tile == TILE_256) return direct<E, OP, 256, 256, 128, 64, 1, 1>(p, s);
-      if (tile == TILE_128_256) return direct<E, OP, 128, 256, 64, 64, 1, 1>(p, s);
-    }
-    if (tile == TILE_128) return direct<E, OP, 128, 128, 64, 64, 1, 2>(p, s);
-    if (tile == TILE_64_128) return direct<E, OP, 64, 128, 32, 64, 1, 3>(p, s);
-    if (tile == TILE_64) return direct<E, OP, 64, 64, 32, 32, 1, 5>(p, s);
-    return direct<E, OP, 64, 64, 32, 32, 4, 1>(p, s);
+  const bool straight = direct_ok<E, OP>(p);
+  int tile;
+  if constexpr (sizeof(E) == 2) {
+    tile = straight ? choose_tile<E, OP>(p, {TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &time)
+                    : choose_tile<E, OP>(p, {STAGED_128, STAGED_64}, &time);
+  } else {
+    tile = straight ? choose_tile<E, OP>(p, {TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &time)
+                    : choose_tile<E, OP>(p, {STAGED_64}, &time);
   }
-  // rows that start anywhere: 4096 x 2048 x 4096 in bf16 176 us in 128 x 128, 250 in 64 x 64; the gradient of 333 x
-  // 999 x 257 in fp32 74 us and 39
-  const int tile = choose_tile<E, OP>(p, {TILE_128, TILE_64}, &time);
   if (few_rows_ok<E, OP>(p, time)) return few_rows<E, OP>(p, s);
-  if (tile == TILE_64) return staged<E, OP, 64, 64, 32, 32>(p, s);
-  return staged<E, OP, 128, 128, 64, 64>(p, s);
+  if constexpr (OP == OP_DX || OP == OP_DW) {
+    const float tiles = tiles_like<OP>(p, 64, 64), stages = stages_of<E, OP>(p);
+    const int splits = splits_for(tiles, stages);
+    if (splits > 1 && part && kJoinUs + tile_time(costs_of<E, OP>()[straight ? TILE_64 : STAGED_64], tiles * splits, std::ceil(stages / splits)) < time) {
+      const int rows = OP == OP_DW ? p.E * p.M : p.rows;
+      ProductArgs q = p;
+      q.splits = splits;
+      q.plane = (int64_t)rows * p.N;
+      q.out = part;
+      q.out_fmt = MOE_AFMT_F32;
+      q.ldo = p.N;
+      const moe_status st = straight ? direct<E, OP, 64, 64, 32, 32, 1, 5>(q, s) : staged<E, OP, 64, 64, 32, 32, 3>(q, s);
+      if (st != MOE_OK) return st;
+      return launch(split_join_kernel, dim3((unsigned)((q.plane + 255) / 256)), dim3(256), s, part, q.plane, splits,
+                    OP == OP_DW ? nullptr : p.offsets, p.E, rows, p.N, p.out, OP == OP_DW ? p.N : p.ldo, p.out_fmt);
+    }
+  }
+  if (!straight) {
+    if constexpr (sizeof(E) == 2) {
+      if (tile == STAGED_128) return staged<E, OP, 128, 128, 64, 64, 2>(p, s);
+    }
+    return staged<E, OP, 64, 64, 32, 32, 3>(p, s);
+  }
+  if constexpr (sizeof(E) == 2) {
+    if (tile == TILE_256) return direct<E, OP, 256, 256, 128, 64, 1, 1>(p, s);
+    if (tile == TILE_128_256) return direct<E, OP, 128, 256, 64, 64, 1, 1>(p, s);
+  }
+  if (tile == TILE_128) return direct<E, OP, 128, 128, 64, 64, 1, 2>(p, s);
+  if (tile == TILE_64_128) return direct<E, OP, 64, 128, 32, 64, 1, 3>(p, s);
+  if (tile == TILE_64) return direct<E, OP, 64, 64, 32, 32, 1, 5>(p, s);
+  return direct<E, OP, 64, 64, 32, 32, 4, 1>(p, s);
 }
 template <int OP>
-moe_status product(int fmt, const ProductArgs& p, hipStream_t s) {
-  return fmt == MOE_AFMT_BF16 ? product_of<uint16_t, OP>(p, s) : product_of<float, OP>(p, s);
+moe_status product(int fmt, const ProductArgs& p, hipStream_t s, float* part = nullptr) {
+  return fmt == MOE_AFMT_BF16 ? product_of<uint16_t, OP>(p, part, s) : product_of<float, OP>(p, part, s);
 }
 
 // ---------------------------------------------------------------- checks
@@ -328,15 +384,29 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // The workspace: 15 bytes to reach an alignment of 16, d, the bias's partial sums.
 struct Workspace {
-  int64_t ld_d, d, bias, bytes;  // elements; offsets and size in bytes
+  int64_t ld_d, d, bias, part, bytes;  // elements; offsets and size in bytes
 };
-Workspace workspace_of(int64_t rows, int E, int64_t n, int64_t bias_n, int fmt) {
+// Elements of fp32 sums that splits of the k leave, at most.
+template <int OP>
+int64_t partials(int fmt, const ProductArgs& p) {
+  const float tiles = tiles_like<OP>(p, 64, 64);
+  const int splits = splits_for(tiles, fmt == MOE_AFMT_BF16 ? stages_of<uint16_t, OP>(p) : stages_of<float, OP>(p));
+  return splits > 1 ? (OP == OP_DW ? (int64_t)p.E * p.M : p.rows) * p.N * splits : 0;
+}
+// (k: columns of x; n: of d, 2 N for the gated block; bias_n: of the bias or 0)
+Workspace workspace_of(int64_t rows, int E, int64_t k, int64_t n, int64_t bias_n, int fmt) {
   Workspace w;
+  ProductArgs dx{}, dw{};
+  dx.rows = dw.rows = (int)rows;
+  dx.E = dw.E = E;
+  dx.K = dw.M = (int)n;
+  dx.N = dw.N = (int)k;
   w.ld_d = up(n, 8);
   w.d = 0;
   w.bias = up(rows * w.ld_d * fmt_bytes(fmt), 16);
   const int splits = bias_splits(rows, E);
-  w.bytes = 15 + w.bias + (bias_n && splits > 1 ? 4 * (int64_t)splits * E * bias_n : 0);
+  w.part = up(w.bias + (bias_n && splits > 1 ? 4 * (int64_t)splits * E * bias_n : 0), 16);
+  w.bytes = 15 + w.part + 4 * std::max(partials<OP_DX>(fmt, dx), partials<OP_DW>(fmt, dw));
   return w;
 }
 bool sizes_ok(int32_t rows, int32_t E, int32_t K, int32_t N, int32_t fmt) {
@@ -347,7 +417,7 @@ uint8_t* base_of(void* ws) { return reinterpret_cast<uint8_t*>(((uintptr_t)ws + 
 
 // dx = d W and dW = d^T x, each where it is asked for.
 moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz, int64_t ld_dz, bool padded, const void* x, const void* w,
-                     const int32_t* offsets, void* dx, void* dw, hipStream_t s) {
+                     const int32_t* offsets, void* dx, void* dw, float* part, hipStream_t s) {
   ProductArgs p{};
   p.a = dz;
   p.lda = ld_dz;
@@ -364,7 +434,7 @@ moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz,
     p.out = dx;
     p.ldo = d.ld_dx;
     p.out_fmt = c->fmt;
-    const moe_status st = product<OP_DX>(c->fmt, p, s);
+    const moe_status st = product<OP_DX>(c->fmt, p, s, part);
     if (st != MOE_OK) return st;
   }
   if (dw) {
@@ -374,7 +444,7 @@ moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz,
     p.N = c->K;
     p.out = dw;
     p.out_fmt = c->dw_fmt;
-    return product<OP_DW>(c->fmt, p, s);
+    return product<OP_DW>(c->fmt, p, s, part);
   }
   return MOE_OK;
 }
@@ -425,7 +495,7 @@ extern "C" MOE_API moe_status moe_glu(const moe_product_config* cfg, const void*
 
 extern "C" MOE_API int64_t moe_glu_workspace(int32_t rows, int32_t n_experts, int32_t H, int32_t I, int32_t fmt) {
   if (!sizes_ok(rows, n_experts, H, I, fmt)) return -1;
-  return workspace_of(rows, n_experts, 2ll * I, 0, fmt).bytes;
+  return workspace_of(rows, n_experts, H, 2ll * I, 0, fmt).bytes;
 }
 
 extern "C" MOE_API moe_status moe_glu_backward(const moe_product_config* cfg, const void* da, const void* gu, const void* x,
@@ -434,7 +504,7 @@ extern "C" MOE_API moe_status moe_glu_backward(const moe_product_config* cfg, co
   Dims d;
   if (!da || !gu || (!dx && !dw) || (dx && !w) || (dw && !x) || !ws || !dims_ok(cfg, true, offsets, d)) return MOE_EINVAL;
   const int64_t eb = fmt_bytes(cfg->fmt), R = cfg->rows;
-  const Workspace k = workspace_of(R, cfg->n_experts, 2ll * cfg->N, 0, cfg->fmt);
+  const Workspace k = workspace_of(R, cfg->n_experts, cfg->K, 2ll * cfg->N, 0, cfg->fmt);
   if (ws_bytes < (size_t)k.bytes) return MOE_EINVAL;
   if (!all_aligned(eb, da, gu, dx ? w : nullptr, dw ? x : nullptr, dx) || !aligned_to(dw, fmt_bytes(cfg->dw_fmt)) ||
       !aligned_to(offsets, 4))
@@ -448,9 +518,10 @@ extern "C" MOE_API moe_status moe_glu_backward(const moe_product_config* cfg, co
   if (!apart(in, out)) return MOE_EINVAL;
   const hipStream_t s = stream_of(stream);
   const StreamDevice on(s);
-  uint8_t* const dgu = base_of(ws) + k.d;
+  uint8_t* const base = base_of(ws);
+  void* const dgu = base + k.d;
   const moe_status st = pre_gradient<true>(cfg, d, da, cfg->fmt, gu, offsets, dgu, k.ld_d, s);
-  return st == MOE_OK ? gradients(cfg, d, dgu, k.ld_d, true, x, w, offsets, dx, dw, s) : st;
+  return st == MOE_OK ? gradients(cfg, d, dgu, k.ld_d, true, x, w, offsets, dx, dw, reinterpret_cast<float*>(base + k.part), s) : st;
 }
 
 extern "C" MOE_API moe_status moe_linear(const moe_product_config* cfg, const void* x, const void* w, const float* bias,
@@ -495,7 +566,7 @@ extern "C" MOE_API moe_status moe_linear(const moe_product_config* cfg, const vo
 
 extern "C" MOE_API int64_t moe_linear_workspace(int32_t rows, int32_t n_experts, int32_t K, int32_t N, int32_t fmt) {
   if (!sizes_ok(rows, n_experts, K, N, fmt)) return -1;
-  return workspace_of(rows, n_experts, N, N, fmt).bytes;
+  return workspace_of(rows, n_experts, K, N, N, fmt).bytes;
 }
 
 extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg, const void* dy, const void* z, const void* x,
@@ -505,7 +576,7 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
   if (!dy || (!dx && !dw && !dbias) || (dx && !w) || (dw && !x) || !ws || !dims_ok(cfg, false, offsets, d)) return MOE_EINVAL;
   if (cfg->act != MOE_ACT_NONE && !z) return MOE_EINVAL;
   const int64_t eb = fmt_bytes(cfg->fmt), R = cfg->rows;
-  const Workspace k = workspace_of(R, cfg->n_experts, cfg->N, cfg->N, cfg->fmt);
+  const Workspace k = workspace_of(R, cfg->n_experts, cfg->K, cfg->N, cfg->N, cfg->fmt);
   if (ws_bytes < (size_t)k.bytes) return MOE_EINVAL;
   const bool zs = cfg->act != MOE_ACT_NONE;
   if (!all_aligned(eb, zs ? z : nullptr, dx ? w : nullptr, dw ? x : nullptr, dx) || !aligned_to(dy, fmt_bytes(cfg->y_fmt)) ||
@@ -536,7 +607,9 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
   }
   if (!dx && !dw) return st;
   // dy itself where nothing changes it and its rows start on 16 bytes, else dz in the operands' type
-  if (!zs && cfg->y_fmt == cfg->fmt && aligned_to(dy, 16) && (d.ld_y * eb | cfg->N * eb) % 16 == 0) return gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, s);
+  float* const sums = reinterpret_cast<float*>(base + k.part);
+  if (!zs && cfg->y_fmt == cfg->fmt && aligned_to(dy, 16) && (d.ld_y * eb | cfg->N * eb) % 16 == 0)
+    return gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, sums, s);
   st = pre_gradient<false>(cfg, d, dy, cfg->y_fmt, z, offsets, base + k.d, k.ld_d, s);
-  return st == MOE_OK ? gradients(cfg, d, base + k.d, k.ld_d, true, x, w, offsets, dx, dw, s) : st;
+  return st == MOE_OK ? gradients(cfg, d, base + k.d, k.ld_d, true, x, w, offsets, dx, dw, sums, s) : st;
 }

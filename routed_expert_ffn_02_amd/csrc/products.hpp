@@ -31,6 +31,8 @@ struct ProductArgs {
   int32_t out_fmt;           // of out and residual
   bool padded;               // a's rows have zeros up to a multiple of 16 bytes
   uint32_t tiles;            // at most
+  int32_t splits;            // of the k, each with a plane of fp32 outputs of its own if there are more than one
+  int64_t plane;             // elements
 };
 
 // ---------------------------------------------------------------- activations
@@ -414,7 +416,7 @@ __device__ __forceinline__ void write_tile(const ProductArgs& p, const Place& at
       if (r >= 16 || row >= at_.M || cols <= 0) continue;
       if constexpr (OP == OP_DW) {
         // past the caches: it is read much later, if at all there (1.07 GB of it 333 -> 257 us, 134 MB 101 -> 95)
-        write8<true>(p.out, ((int64_t)at_.g * p.M + at_.m0 + row) * p.N + col, p.out_fmt, cols, v);
+        write8<true>(p.out, blockIdx.y * p.plane + ((int64_t)at_.g * p.M + at_.m0 + row) * p.N + col, p.out_fmt, cols, v);
       } else {
         const int64_t at = at_.row0 + row;
         if constexpr (OP == OP_GLU) {
@@ -446,7 +448,7 @@ __device__ __forceinline__ void write_tile(const ProductArgs& p, const Place& at
           }
           write8(p.out, at * p.ldo + col, p.out_fmt, cols, v);
         } else {
-          write8(p.out, at * p.ldo + col, p.out_fmt, cols, v);
+          write8(p.out, blockIdx.y * p.plane + at * p.ldo + col, p.out_fmt, cols, v);
         }
       }
     }
@@ -454,109 +456,142 @@ __device__ __forceinline__ void write_tile(const ProductArgs& p, const Place& at
   }
 }
 
-template <typename E, int OP, int BM, int BN, int WM, int WN>
+// Elements `n` and up of a piece, the first one first, zeros behind them (n = all: zeros).
+template <typename E>
+__device__ __forceinline__ u32x4 elements_from(u32x4 q, int n) {
+  uint64_t lo = q[0] | (uint64_t)q[1] << 32, hi = q[2] | (uint64_t)q[3] << 32;
+  const int bits = n * 8 * (int)sizeof(E), in = bits & 63;
+  const uint64_t up = in ? hi << (64 - in) : 0;
+  lo = bits >= 128 ? 0 : bits >= 64 ? hi >> in : lo >> in | up;
+  hi = bits >= 64 ? 0 : hi >> in;
+  return {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// Operands whose rows start anywhere: pieces go through registers, DEPTH stages ahead.  All but the last
+// stage are plain loads.  There a piece at the columns' edge takes the start of the next row with it,
+// for outputs that are not written.  In the last stage it is its row's last whole piece, shifted.
+// (Rows shorter than a piece: element by element.)
+template <typename E, int OP, int BM, int BN, int WM, int WN, int DEPTH>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(ProductArgs p) {
   using T = ProductTile<E, OP, BM, BN, WM, WN>;
   using OpA = Operand<E, BM, T::kKmajA>;
   using OpB = Operand<E, BN, T::kKmajB>;
-  constexpr int kThreads = T::kThreads, kK = OpA::kK;
-  constexpr int kStage = T::kStages / 2;
+  constexpr int kThreads = T::kThreads, kK = OpA::kK, kEl = OpA::kEl, kStage = T::kStages / 2;
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::kStages];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
   Place at;
   if (!find_place<OP, BM, T::kCols>(p, count_tiles<OP, BM>(p), blockIdx.x >> 3, at)) return;
-  const int m0 = at.m0, n0 = at.n0, M = at.M, N = at.N, K = at.K;
+  const int K = at.K, all = (K + kK - 1) / kK, stages = (all + p.splits - 1) / p.splits, first = blockIdx.y * stages;
 
-  // this thread's pieces: an address (k = 0) and, in `left`, how many of its elements there are
+  // this thread's pieces.  k in a row: the row's start; a row per k: the piece in the first stage's row (or
+  // the last column's, past it), and how many of its elements are behind the row
   constexpr int kPa = OpA::kPieces / kThreads, kPb = OpB::kPieces / kThreads;
-  const uint8_t *pa[kPa], *pb[kPb];
-  int ka[kPa], kb[kPb];  // k of the piece in a stage; where rows are the k, beside it the elements in the row
-  int la[kPa], lb[kPb];
-  const E* a = static_cast<const E*>(p.a);
-  const E* b = static_cast<const E*>(p.b);
+  const E *pa[kPa], *pb[kPb];
+  int ka[kPa], kb[kPb], sa[kPa], sb[kPb];
+  const E* a = static_cast<const E*>(p.a) + (int64_t)at.row0 * p.lda;
+  const E* b = static_cast<const E*>(p.b) + (OP == OP_DW ? (int64_t)at.row0 * p.ldb : at.g * p.gsb);
+  const bool tiny = (T::kKmajA && p.M < kEl) || (T::kKmajB && p.N < kEl) || ((!T::kKmajA || !T::kKmajB) && K < kEl);
+  const auto column = [&](int c, int total, int& behind) {
+    c = tiny ? c : min(c, total - 1);
+    behind = max(c - (total - kEl), 0);
+    return c;
+  };
 #pragma unroll
   for (int i = 0; i < kPa; ++i) {
     int r;
     OpA::where(i * kThreads + tid, r, ka[i]);
-    if constexpr (OP == OP_DW) {
-      la[i] = M - r;
-      pa[i] = reinterpret_cast<const uint8_t*>(a + (int64_t)(at.row0 + ka[i]) * p.lda + m0 + r);
-    } else {
-      la[i] = 0;
-      pa[i] = reinterpret_cast<const uint8_t*>(a + (int64_t)(at.row0 + min(r, M - 1)) * p.lda + ka[i]);
-    }
+    if constexpr (T::kKmajA) pa[i] = a + (int64_t)ka[i] * p.lda + column(at.m0 + r, p.M, sa[i]);
+    else pa[i] = a + (int64_t)min(r, at.M - 1) * p.lda;
   }
 #pragma unroll
   for (int i = 0; i < kPb; ++i) {
     int r;
     OpB::where(i * kThreads + tid, r, kb[i]);
-    if constexpr (OP == OP_DW) {
-      lb[i] = N - r;
-      pb[i] = reinterpret_cast<const uint8_t*>(b + (int64_t)(at.row0 + kb[i]) * p.ldb + n0 + r);
-    } else if constexpr (OP == OP_DX) {
-      lb[i] = N - r;
-      pb[i] = reinterpret_cast<const uint8_t*>(b + at.g * p.gsb + (int64_t)kb[i] * p.ldb + n0 + r);
-    } else {
-      lb[i] = 0;
-      const int64_t row = n_row<OP, WN>(p, at, r);
-      pb[i] = reinterpret_cast<const uint8_t*>(b + at.g * p.gsb + row * p.ldb + kb[i]);
-    }
+    if constexpr (T::kKmajB) pb[i] = b + (int64_t)kb[i] * p.ldb + column(at.n0 + r, p.N, sb[i]);
+    else pb[i] = b + n_row<OP, WN>(p, at, r) * p.ldb;
   }
-  u32x4 qa[kPa], qb[kPb];
-  const auto load = [&](int k0) {
-    // a stage inside the operands, as most are, is loads without a branch between them
-    if (k0 + kK <= K && (!T::kKmajA || M == BM) && (!T::kKmajB || N == BN)) {
+  u32x4 qa[DEPTH][kPa], qb[DEPTH][kPb];
+  constexpr int kMore = T::kKmajA || T::kKmajB;  // rows that a plain stage needs behind it
+  const auto piece = [&](const E* from) { return load16<false>(reinterpret_cast<const uint8_t*>(from)); };
+  const auto load = [&](int s, u32x4 (&ga)[kPa], u32x4 (&gb)[kPb]) {
+    const int k0 = s * kK;
+    if (!tiny && k0 + kK + kMore <= K) {
 #pragma unroll
-      for (int i = 0; i < kPa; ++i) qa[i] = load16<false>(pa[i] + (int64_t)k0 * (T::kKmajA ? p.lda : 1) * sizeof(E));
+      for (int i = 0; i < kPa; ++i) ga[i] = piece(pa[i] + (T::kKmajA ? k0 * p.lda : k0 + ka[i]));
 #pragma unroll
-      for (int i = 0; i < kPb; ++i) qb[i] = load16<false>(pb[i] + (int64_t)k0 * (T::kKmajB ? p.ldb : 1) * sizeof(E));
-      return;
-    }
+      for (int i = 0; i < kPb; ++i) gb[i] = piece(pb[i] + (T::kKmajB ? k0 * p.ldb : k0 + kb[i]));
+    } else if (!tiny) {
+      // k past the last: the last row again, or the row's last piece, and then zeros
 #pragma unroll
-    for (int i = 0; i < kPa; ++i) {
-      if constexpr (T::kKmajA) qa[i] = read_piece<E>(pa[i] + (int64_t)k0 * p.lda * sizeof(E), k0 + ka[i] < K ? la[i] : 0);
-      else qa[i] = read_piece<E>(pa[i] + (int64_t)k0 * sizeof(E), K - k0 - ka[i]);
-    }
+      for (int i = 0; i < kPa; ++i)
+        ga[i] = piece(pa[i] + (T::kKmajA ? (min(k0 + ka[i], K - 1) - ka[i]) * p.lda - sa[i] : max(min(k0 + ka[i], K - kEl), 0)));
 #pragma unroll
-    for (int i = 0; i < kPb; ++i) {
-      if constexpr (T::kKmajB) qb[i] = read_piece<E>(pb[i] + (int64_t)k0 * p.ldb * sizeof(E), k0 + kb[i] < K ? lb[i] : 0);
-      else qb[i] = read_piece<E>(pb[i] + (int64_t)k0 * sizeof(E), K - k0 - kb[i]);
+      for (int i = 0; i < kPb; ++i)
+        gb[i] = piece(pb[i] + (T::kKmajB ? (min(k0 + kb[i], K - 1) - kb[i]) * p.ldb - sb[i] : max(min(k0 + kb[i], K - kEl), 0)));
+#pragma unroll
+      for (int i = 0; i < kPa; ++i)
+        ga[i] = elements_from<E>(ga[i], T::kKmajA ? (k0 + ka[i] < K ? sa[i] : kEl) : min(max(k0 + ka[i] - (K - kEl), 0), kEl));
+#pragma unroll
+      for (int i = 0; i < kPb; ++i)
+        gb[i] = elements_from<E>(gb[i], T::kKmajB ? (k0 + kb[i] < K ? sb[i] : kEl) : min(max(k0 + kb[i] - (K - kEl), 0), kEl));
+    } else {
+      const auto some = [&](const E* row, int64_t at_, int n) { return read_piece<E>(reinterpret_cast<const uint8_t*>(row + at_), n); };
+#pragma unroll
+      for (int i = 0; i < kPa; ++i) {
+        int r, k;
+        OpA::where(i * kThreads + tid, r, k);
+        if constexpr (T::kKmajA) ga[i] = some(pa[i], k0 * p.lda, k0 + k < K ? p.M - at.m0 - r : 0);
+        else ga[i] = some(pa[i], k0 + k, K - k0 - k);
+      }
+#pragma unroll
+      for (int i = 0; i < kPb; ++i) {
+        int r, k;
+        OpB::where(i * kThreads + tid, r, k);
+        if constexpr (T::kKmajB) gb[i] = some(pb[i], k0 * p.ldb, k0 + k < K ? p.N - at.n0 - r : 0);
+        else gb[i] = some(pb[i], k0 + k, K - k0 - k);
+      }
     }
   };
-  const auto store = [&](uint8_t* stage) {
+  const auto store = [&](int t, const u32x4 (&ga)[kPa], const u32x4 (&gb)[kPb]) {
+    uint8_t* stage = lds + (t & 1) * kStage;
 #pragma unroll
-    for (int i = 0; i < kPa; ++i) *reinterpret_cast<u32x4*>(stage + 16 * (i * kThreads + tid)) = qa[i];
+    for (int i = 0; i < kPa; ++i) *reinterpret_cast<u32x4*>(stage + 16 * (i * kThreads + tid)) = ga[i];
 #pragma unroll
-    for (int i = 0; i < kPb; ++i) *reinterpret_cast<u32x4*>(stage + OpA::kBytes + 16 * (i * kThreads + tid)) = qb[i];
+    for (int i = 0; i < kPb; ++i) *reinterpret_cast<u32x4*>(stage + OpA::kBytes + 16 * (i * kThreads + tid)) = gb[i];
   };
 
   f32x4 acc[T::kMt][T::kNt] = {};
-  const int stages = (K + kK - 1) / kK;
   if (stages) {
-    load(0);
-    store(lds);
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (d < stages) load(first + d, qa[d], qb[d]);
+    store(0, qa[0], qb[0]);
     __syncthreads();
   }
-  for (int s = 0; s < stages; ++s) {
-    const uint8_t* at = lds + (s & 1) * kStage;
-    if (s + 1 < stages) load((s + 1) * kK);
+  for (int t0 = 0; t0 < stages; t0 += DEPTH) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      u32x4 fa[T::kMt], fb[T::kNt];
+    for (int d = 0; d < DEPTH; ++d) {
+      const int t = t0 + d;
+      if (t >= stages) break;
+      if (t + DEPTH < stages) load(first + t + DEPTH, qa[d], qb[d]);
+      const uint8_t* stage = lds + (t & 1) * kStage;
 #pragma unroll
-      for (int i = 0; i < T::kMt; ++i) fa[i] = OpA::fragment(at, wm + 16 * i, j, lane);
+      for (int j = 0; j < 2; ++j) {
+        u32x4 fa[T::kMt], fb[T::kNt];
 #pragma unroll
-      for (int i = 0; i < T::kNt; ++i) fb[i] = OpB::fragment(at + OpA::kBytes, wn + 16 * i, j, lane);
+        for (int i = 0; i < T::kMt; ++i) fa[i] = OpA::fragment(stage, wm + 16 * i, j, lane);
 #pragma unroll
-      for (int m = 0; m < T::kMt; ++m)
+        for (int i = 0; i < T::kNt; ++i) fb[i] = OpB::fragment(stage + OpA::kBytes, wn + 16 * i, j, lane);
 #pragma unroll
-        for (int n = 0; n < T::kNt; ++n) multiply<E>(fb[n], fa[m], acc[m][n]);
+        for (int m = 0; m < T::kMt; ++m)
+#pragma unroll
+          for (int n = 0; n < T::kNt; ++n) multiply<E>(fb[n], fa[m], acc[m][n]);
+      }
+      if (t + 1 < stages) store(t + 1, qa[(d + 1) % DEPTH], qb[(d + 1) % DEPTH]);
+      __syncthreads();
     }
-    if (s + 1 < stages) store(lds + ((s + 1) & 1) * kStage);
-    __syncthreads();
   }
-
   write_tile<E, OP, BM, BN, WM, WN>(p, at, lds + wave * T::kPatch, wave, lane, acc);
 }
 
@@ -614,7 +649,8 @@ __global__ __launch_bounds__(KS * 64 * (BM / WM) * (BN / WN), WAVES) void produc
   if (!find_place<OP, BM, T::kCols>(p, count_tiles<OP, BM>(p), blockIdx.x >> 3, at)) return;
 
   // this part's first k and its stages; past the last k, loads bring zeros
-  const int all = (at.K + kK - 1) / kK, stages = (all + KS - 1) / KS, first = part * stages;
+  const int all = (at.K + kK - 1) / kK, parts = KS * p.splits, stages = (all + parts - 1) / parts;
+  const int first = (blockIdx.y * KS + part) * stages;
   const int left = at.K - first * kK;
 
   // this thread's pieces of each half: byte offsets at the first k, and their k in a stage

@@ -262,6 +262,19 @@ def test_few_rows(run, dtype, how, rows, E, H, I):
     run(rows, uneven(rows, E, rows // 6) if E else None, H, I, dtype, how, act="gelu")
 
 
+# gradients of few tiles with a long k: few rows of many outputs (dx), many rows of small weights (dw)
+LONG = [(1, 0, 0, 24, 4000), (3, 0, 0, 117, 2001), (40, 4, 3, 64, 1999), (65, 0, 0, 130, 1536), (2100, 0, 0, 72, 64), (2100, 0, 0, 65, 99),
+        (3000, 3, 200, 40, 33), (5000, 2, 0, 9, 200)]
+
+
+@pytest.mark.parametrize("run", [run_glu_backward, run_linear_backward])
+@types
+@hows
+@pytest.mark.parametrize("rows,E,tail,H,I", LONG)
+def test_long_sums(run, dtype, how, rows, E, tail, H, I):
+    run(rows, uneven(rows, E, tail) if E else None, H, I, dtype, how, act="silu")
+
+
 @types
 def test_long_bias_sums(dtype):
     """A bias over so many rows that its gradient is summed in splits."""
