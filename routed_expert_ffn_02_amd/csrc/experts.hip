@@ -19,6 +19,10 @@ constexpr int kProductMaxSize = 1 << 16;  // of a row of x, of the outputs
 // d = dgu (glu) or dz (linear), rounded to the operands' type: the products that follow take it as
 // an operand, as autograd's do, with zeros up to ld_d behind each row.  Eight elements a lane; rows behind
 // the last expert's are left out.
+__device__ __forceinline__ void pad_row(void* d, int64_t at, int from, int64_t to, int fmt) {
+  for (int e = from; e < to; ++e) write1(d, at + e, fmt, 0.f);
+}
+
 template <bool GLU>
 __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
                                                            const void* __restrict__ z, int fmt, int64_t ld_z,
@@ -49,16 +53,13 @@ __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restric
       }
       write8(d, (int64_t)row * ld_d + c, fmt, n - c, v);
     }
-    if (c + 8 >= n)  // the last of the row
-      for (int e = all; e < ld_d; ++e) {
-        if (fmt == MOE_AFMT_BF16) static_cast<uint16_t*>(d)[row * ld_d + e] = 0;
-        else static_cast<float*>(d)[row * ld_d + e] = 0.f;
-      }
+    if (c + 8 >= n) pad_row(d, row * ld_d, all, ld_d, fmt);
   }
 }
 
 // ---------------------------------------------------------------- the bias's gradient
-// Column sums of dz in fp32, from dy and z as given (dz is not rounded here).  A workgroup has 64
+// Column sums of dz in fp32, from dy and z as given (dz is not rounded before), and, where it is asked
+// for, dz itself as the products take it (d, as pre_gradient_kernel writes it).  A workgroup has 64
 // columns, eight lanes of eight, and 32 rows at once; its rows' sums meet in LDS in a fixed order.
 // Splits of a long expert write their own sums, which bias_join adds in order: 32 rows a split and
 // more, up to 64 splits, put about as many loads in flight as there are (777 rows of 1001 in bf16 with
@@ -68,7 +69,8 @@ constexpr int kBiasRows = 32;  // rows of a split, at least
 __global__ __launch_bounds__(256) void bias_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
                                                             const void* __restrict__ z, int fmt, int64_t ld_z,
                                                             const int32_t* __restrict__ offsets, int rows, int E, int n,
-                                                            int act, int splits, float* __restrict__ out) {
+                                                            int act, int splits, float* __restrict__ out,
+                                                            void* __restrict__ d, int64_t ld_d) {
   __shared__ float part[4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = 64 * blockIdx.x + 8 * (lane & 7);
@@ -87,6 +89,11 @@ __global__ __launch_bounds__(256) void bias_gradient_kernel(const void* __restri
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += v[e];
+      if (d) {
+        const int64_t at = (int64_t)(r.first + i) * ld_d;
+        write8(d, at + c, fmt, n - c, v);
+        if (c + 8 >= n) pad_row(d, at, n, ld_d, fmt);
+      }
     }
   }
 #pragma unroll
@@ -593,23 +600,25 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
   const hipStream_t s = stream_of(stream);
   const StreamDevice on(s);
   uint8_t* const base = base_of(ws);
+  float* const sums = reinterpret_cast<float*>(base + k.part);
   moe_status st = MOE_OK;
+  // dy itself where nothing changes it and its rows start on 16 bytes, else dz in the operands' type
+  const bool products = dx || dw;
+  const bool as_is = !zs && cfg->y_fmt == cfg->fmt && aligned_to(dy, 16) && (d.ld_y * eb | cfg->N * eb) % 16 == 0;
+  void* const dz = products && !as_is ? base + k.d : nullptr;
   if (dbias) {
     const int splits = bias_splits(R, cfg->n_experts);
     float* const part = splits > 1 ? reinterpret_cast<float*>(base + k.bias) : dbias;
     st = launch(bias_gradient_kernel, dim3((cfg->N + 63) / 64, cfg->n_experts, splits), dim3(256), s, dy, cfg->y_fmt, d.ld_y,
-                z, cfg->fmt, d.ld_z, offsets, cfg->rows, cfg->n_experts, cfg->N, cfg->act, splits, part);
+                z, cfg->fmt, d.ld_z, offsets, cfg->rows, cfg->n_experts, cfg->N, cfg->act, splits, part, dz, k.ld_d);
     if (st == MOE_OK && splits > 1) {
       const int64_t total = (int64_t)cfg->n_experts * cfg->N;
       st = launch(bias_join_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), s, part, total, splits, dbias);
     }
-    if (st != MOE_OK) return st;
+  } else if (dz) {
+    st = pre_gradient<false>(cfg, d, dy, cfg->y_fmt, z, offsets, dz, k.ld_d, s);
   }
-  if (!dx && !dw) return st;
-  // dy itself where nothing changes it and its rows start on 16 bytes, else dz in the operands' type
-  float* const sums = reinterpret_cast<float*>(base + k.part);
-  if (!zs && cfg->y_fmt == cfg->fmt && aligned_to(dy, 16) && (d.ld_y * eb | cfg->N * eb) % 16 == 0)
-    return gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, sums, s);
-  st = pre_gradient<false>(cfg, d, dy, cfg->y_fmt, z, offsets, base + k.d, k.ld_d, s);
-  return st == MOE_OK ? gradients(cfg, d, base + k.d, k.ld_d, true, x, w, offsets, dx, dw, sums, s) : st;
+  if (st != MOE_OK || !products) return st;
+  return as_is ? gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, sums, s)
+               : gradients(cfg, d, dz, k.ld_d, true, x, w, offsets, dx, dw, sums, s);
 }
