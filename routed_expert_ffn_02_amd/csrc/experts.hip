@@ -150,14 +150,18 @@ int64_t tiles_of(const ProductArgs& p) {
                                  : ((int64_t)p.rows + (int64_t)std::min(p.E, p.rows) * (BM - 1)) / BM;
   return mt * nt;
 }
+// Workgroups: whole runs on every XCD.
+template <int OP, int BM, int COLS>
+int64_t blocks_of(const ProductArgs& p) {
+  const int64_t tiles = tiles_of<OP, BM, COLS>(p);
+  const int64_t eight = 8 * (OP == OP_DW ? (int64_t)dealt_run((uint32_t)std::min<int64_t>(tiles / p.E, 1 << 30)) : 1);
+  return (tiles + eight - 1) / eight * eight;
+}
 template <typename T, int OP, int BM>
 moe_status run_tiles(void (*kernel)(ProductArgs), ProductArgs p, int threads, hipStream_t s) {
-  const int64_t tiles = tiles_of<OP, BM, T::kCols>(p);
-  // whole runs on every XCD
-  const int64_t eight = 8 * (OP == OP_DW ? (int64_t)dealt_run((uint32_t)std::min<int64_t>(tiles / p.E, 1 << 30)) : 1);
-  const int64_t blocks = (tiles + eight - 1) / eight * eight;
+  const int64_t blocks = blocks_of<OP, BM, T::kCols>(p);
   if (blocks * threads * p.splits > kMaxThreads) return MOE_EINVAL;
-  p.tiles = (uint32_t)tiles;
+  p.tiles = (uint32_t)tiles_of<OP, BM, T::kCols>(p);
   return launch(kernel, dim3((unsigned)blocks, p.splits), dim3(threads), s, p);
 }
 
@@ -282,55 +286,127 @@ moe_status few_rows(ProductArgs p, hipStream_t s) {
   return MOE_EINVAL;
 }
 
-template <typename E, int OP>
-moe_status product_of(ProductArgs p, float* part, hipStream_t s) {
-  p.splits = 1;
+// How a product is done: its tile, the splits of a gradient's k, the estimated time.
+struct Plan {
+  bool straight;  // from memory to LDS
+  int tile, splits;
   float time;
-  const bool straight = direct_ok<E, OP>(p);
-  int tile;
-  if constexpr (sizeof(E) == 2) {
-    tile = straight ? choose_tile<E, OP>(p, {TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &time)
-                    : choose_tile<E, OP>(p, {STAGED_128, STAGED_64}, &time);
+};
+template <typename E, int OP>
+Plan plan_of(const ProductArgs& p) {
+  Plan plan{direct_ok<E, OP>(p), 0, 1, 0.f};
+  if (!plan.straight) {
+    if constexpr (sizeof(E) == 2) plan.tile = choose_tile<E, OP>(p, {STAGED_128, STAGED_64}, &plan.time);
+    else plan.tile = choose_tile<E, OP>(p, {STAGED_64}, &plan.time);
+  } else if constexpr (sizeof(E) == 2) {
+    plan.tile = choose_tile<E, OP>(p, {TILE_256, TILE_128_256, TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &plan.time);
   } else {
-    tile = straight ? choose_tile<E, OP>(p, {TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &time)
-                    : choose_tile<E, OP>(p, {STAGED_64}, &time);
+    plan.tile = choose_tile<E, OP>(p, {TILE_128, TILE_64_128, TILE_64, TILE_64_PARTS}, &plan.time);
   }
-  if (few_rows_ok<E, OP>(p, time)) return few_rows<E, OP>(p, s);
   if constexpr (OP == OP_DX || OP == OP_DW) {
+    const int tile = plan.straight ? TILE_64 : STAGED_64;
     const float tiles = tiles_like<OP>(p, 64, 64), stages = stages_of<E, OP>(p);
     const int splits = splits_for(tiles, stages);
-    if (splits > 1 && part && kJoinUs + tile_time(costs_of<E, OP>()[straight ? TILE_64 : STAGED_64], tiles * splits, std::ceil(stages / splits)) < time) {
-      const int rows = OP == OP_DW ? p.E * p.M : p.rows;
-      ProductArgs q = p;
-      q.splits = splits;
-      q.plane = (int64_t)rows * p.N;
-      q.out = part;
-      q.out_fmt = MOE_AFMT_F32;
-      q.ldo = p.N;
-      const moe_status st = straight ? direct<E, OP, 64, 64, 32, 32, 1, 5>(q, s) : staged<E, OP, 64, 64, 32, 32, 3>(q, s);
-      if (st != MOE_OK) return st;
-      return launch(split_join_kernel, dim3((unsigned)((q.plane + 255) / 256)), dim3(256), s, part, q.plane, splits,
-                    OP == OP_DW ? nullptr : p.offsets, p.E, rows, p.N, p.out, OP == OP_DW ? p.N : p.ldo, p.out_fmt);
-    }
+    const float time = kJoinUs + tile_time(costs_of<E, OP>()[tile], tiles * splits, std::ceil(stages / splits));
+    if (splits > 1 && time < plan.time) plan = {plan.straight, tile, splits, time};
   }
-  if (!straight) {
-    if constexpr (sizeof(E) == 2) {
-      if (tile == STAGED_128) return staged<E, OP, 128, 128, 64, 64, 2>(p, s);
-    }
-    return staged<E, OP, 64, 64, 32, 32, 3>(p, s);
-  }
+  return plan;
+}
+
+// Its arguments with the splits' own outputs, and the kernel that adds those.
+template <int OP>
+ProductArgs split(ProductArgs p, int splits, float* part) {
+  p.splits = splits;
+  if (splits == 1) return p;
+  p.plane = (OP == OP_DW ? (int64_t)p.E * p.M : p.rows) * p.N;
+  p.out = part;
+  p.out_fmt = MOE_AFMT_F32;
+  p.ldo = p.N;
+  return p;
+}
+template <int OP>
+moe_status join(const ProductArgs& p, int splits, const float* part, hipStream_t s) {
+  if (splits == 1) return MOE_OK;
+  const int rows = OP == OP_DW ? p.E * p.M : p.rows;
+  const int64_t plane = (int64_t)rows * p.N;
+  return launch(split_join_kernel, dim3((unsigned)((plane + 255) / 256)), dim3(256), s, part, plane, splits,
+                OP == OP_DW ? nullptr : p.offsets, p.E, rows, p.N, p.out, OP == OP_DW ? p.N : p.ldo, p.out_fmt);
+}
+
+template <typename E, int OP>
+moe_status run_plan(const ProductArgs& p, int tile, hipStream_t s) {
   if constexpr (sizeof(E) == 2) {
     if (tile == TILE_256) return direct<E, OP, 256, 256, 128, 64, 1, 1>(p, s);
     if (tile == TILE_128_256) return direct<E, OP, 128, 256, 64, 64, 1, 1>(p, s);
+    if (tile == STAGED_128) return staged<E, OP, 128, 128, 64, 64, 2>(p, s);
   }
   if (tile == TILE_128) return direct<E, OP, 128, 128, 64, 64, 1, 2>(p, s);
   if (tile == TILE_64_128) return direct<E, OP, 64, 128, 32, 64, 1, 3>(p, s);
   if (tile == TILE_64) return direct<E, OP, 64, 64, 32, 32, 1, 5>(p, s);
-  return direct<E, OP, 64, 64, 32, 32, 4, 1>(p, s);
+  if (tile == TILE_64_PARTS) return direct<E, OP, 64, 64, 32, 32, 4, 1>(p, s);
+  return staged<E, OP, 64, 64, 32, 32, 3>(p, s);
+}
+template <typename E, int OP>
+moe_status product_of(ProductArgs p, hipStream_t s) {
+  p.splits = 1;
+  const Plan plan = plan_of<E, OP>(p);
+  return few_rows_ok<E, OP>(p, plan.time) ? few_rows<E, OP>(p, s) : run_plan<E, OP>(p, plan.tile, s);
 }
 template <int OP>
-moe_status product(int fmt, const ProductArgs& p, hipStream_t s, float* part = nullptr) {
-  return fmt == MOE_AFMT_BF16 ? product_of<uint16_t, OP>(p, part, s) : product_of<float, OP>(p, part, s);
+moe_status product(int fmt, const ProductArgs& p, hipStream_t s) {
+  return fmt == MOE_AFMT_BF16 ? product_of<uint16_t, OP>(p, s) : product_of<float, OP>(p, s);
+}
+
+template <typename E, int OP>
+moe_status gradient(const ProductArgs& p, const Plan& plan, float* part, hipStream_t s) {
+  const moe_status st = run_plan<E, OP>(split<OP>(p, plan.splits, part), plan.tile, s);
+  return st == MOE_OK ? join<OP>(p, plan.splits, part, s) : st;
+}
+template <typename E, int B, int WAVES, bool STAGED>
+moe_status pair(ProductArgs dx, ProductArgs dw, hipStream_t s) {
+  dx.tiles = (uint32_t)tiles_of<OP_DX, B, B>(dx);
+  const int64_t a = blocks_of<OP_DX, B, B>(dx), b = blocks_of<OP_DW, B, B>(dw), blocks = a * dx.splits + b * dw.splits;
+  if (blocks * 256 > kMaxThreads) return MOE_EINVAL;
+  return launch(gradients_kernel<E, B, B, B / 2, B / 2, WAVES, STAGED>, dim3((unsigned)blocks), dim3(256), s, dx, (uint32_t)a, dw, (uint32_t)b);
+}
+// Both gradients, in one launch where that is estimated to be faster: all workgroups' stages over the CUs' rounds,
+// not less than the longest tile alone.
+constexpr float kLaunchUs = 2.f;
+template <typename E>
+moe_status both(const ProductArgs& dx, const ProductArgs& dw, float* part, float* part_dw, hipStream_t s) {
+  const Plan a = plan_of<E, OP_DX>(dx), b = plan_of<E, OP_DW>(dw);
+  if (a.straight == b.straight) {
+    float least = a.time + b.time + kLaunchUs;
+    int best = -1;
+    for (const int i : {TILE_64, TILE_128, STAGED_64}) {
+      if ((i == STAGED_64) == a.straight || (i == TILE_128 && (a.splits > 1 || b.splits > 1))) continue;
+      const TileCost &ca = costs_of<E, OP_DX>()[i], &cb = costs_of<E, OP_DW>()[i];
+      const float ta = a.splits * tiles_like<OP_DX>(dx, ca.bm, ca.bn), tb = b.splits * tiles_like<OP_DW>(dw, cb.bm, cb.bn);
+      const float sa = std::ceil(stages_of<E, OP_DX>(dx) / a.splits), sb = std::ceil(stages_of<E, OP_DW>(dw) / b.splits);
+      const float work = (ta * sa * ca.shared + tb * sb * cb.shared) / (ta + tb) * std::ceil((ta + tb) / kCus);
+      const float time = std::max({work, sa * ca.alone, sb * cb.alone}) + std::ceil((ta + tb) / (kCus * ca.per_cu)) * std::max(ca.fixed, cb.fixed) +
+                         ((a.splits > 1) + (b.splits > 1)) * kJoinUs;
+      if (time < least) {
+        least = time;
+        best = i;
+      }
+    }
+    if (best >= 0) {
+      const ProductArgs p = split<OP_DX>(dx, a.splits, part), q = split<OP_DW>(dw, b.splits, part_dw);
+      moe_status st = best == TILE_64    ? pair<E, 64, 4, false>(p, q, s)
+                      : best == TILE_128 ? pair<E, 128, 2, false>(p, q, s)
+                                         : pair<E, 64, 1, true>(p, q, s);
+      if (st == MOE_OK) st = join<OP_DX>(dx, a.splits, part, s);
+      return st == MOE_OK ? join<OP_DW>(dw, b.splits, part_dw, s) : st;
+    }
+  }
+  const moe_status st = gradient<E, OP_DX>(dx, a, part, s);
+  return st == MOE_OK ? gradient<E, OP_DW>(dw, b, part_dw, s) : st;
+}
+template <typename E>
+moe_status gradients_of(const ProductArgs& dx, const ProductArgs& dw, float* part, float* part_dw, hipStream_t s) {
+  if (dx.out && dw.out) return both<E>(dx, dw, part, part_dw, s);
+  return dx.out ? gradient<E, OP_DX>(dx, plan_of<E, OP_DX>(dx), part, s) : gradient<E, OP_DW>(dw, plan_of<E, OP_DW>(dw), part_dw, s);
 }
 
 // ---------------------------------------------------------------- checks
@@ -391,7 +467,7 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 // The workspace: 15 bytes to reach an alignment of 16, d, the bias's partial sums.
 struct Workspace {
-  int64_t ld_d, d, bias, part, bytes;  // elements; offsets and size in bytes
+  int64_t ld_d, d, bias, part, part_dw, bytes;  // elements; offsets and size in bytes
 };
 // Elements of fp32 sums that splits of the k leave, at most.
 template <int OP>
@@ -413,7 +489,8 @@ Workspace workspace_of(int64_t rows, int E, int64_t k, int64_t n, int64_t bias_n
   w.bias = up(rows * w.ld_d * fmt_bytes(fmt), 16);
   const int splits = bias_splits(rows, E);
   w.part = up(w.bias + (bias_n && splits > 1 ? 4 * (int64_t)splits * E * bias_n : 0), 16);
-  w.bytes = 15 + w.part + 4 * std::max(partials<OP_DX>(fmt, dx), partials<OP_DW>(fmt, dw));
+  w.part_dw = up(w.part + 4 * partials<OP_DX>(fmt, dx), 16);
+  w.bytes = 15 + w.part_dw + 4 * partials<OP_DW>(fmt, dw);
   return w;
 }
 bool sizes_ok(int32_t rows, int32_t E, int32_t K, int32_t N, int32_t fmt) {
@@ -424,7 +501,7 @@ uint8_t* base_of(void* ws) { return reinterpret_cast<uint8_t*>(((uintptr_t)ws + 
 
 // dx = d W and dW = d^T x, each where it is asked for.
 moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz, int64_t ld_dz, bool padded, const void* x, const void* w,
-                     const int32_t* offsets, void* dx, void* dw, float* part, hipStream_t s) {
+                     const int32_t* offsets, void* dx, void* dw, uint8_t* ws, const Workspace& k, hipStream_t s) {
   ProductArgs p{};
   p.a = dz;
   p.lda = ld_dz;
@@ -432,28 +509,23 @@ moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz,
   p.offsets = offsets;
   p.rows = c->rows;
   p.E = c->n_experts;
-  if (dx) {
-    p.b = w;
-    p.ldb = d.ld_w;
-    p.gsb = d.gs_w;
-    p.K = d.wrows;
-    p.N = c->K;
-    p.out = dx;
-    p.ldo = d.ld_dx;
-    p.out_fmt = c->fmt;
-    const moe_status st = product<OP_DX>(c->fmt, p, s, part);
-    if (st != MOE_OK) return st;
-  }
-  if (dw) {
-    p.b = x;
-    p.ldb = d.ld_x;
-    p.M = d.wrows;
-    p.N = c->K;
-    p.out = dw;
-    p.out_fmt = c->dw_fmt;
-    return product<OP_DW>(c->fmt, p, s, part);
-  }
-  return MOE_OK;
+  p.N = c->K;
+  p.splits = 1;
+  ProductArgs q = p;
+  p.b = w;
+  p.ldb = d.ld_w;
+  p.gsb = d.gs_w;
+  p.K = d.wrows;
+  p.out = dx;
+  p.ldo = d.ld_dx;
+  p.out_fmt = c->fmt;
+  q.b = x;
+  q.ldb = d.ld_x;
+  q.M = d.wrows;
+  q.out = dw;
+  q.out_fmt = c->dw_fmt;
+  float *const part = reinterpret_cast<float*>(ws + k.part), *const part_dw = reinterpret_cast<float*>(ws + k.part_dw);
+  return c->fmt == MOE_AFMT_BF16 ? gradients_of<uint16_t>(p, q, part, part_dw, s) : gradients_of<float>(p, q, part, part_dw, s);
 }
 
 template <bool GLU>
@@ -528,7 +600,7 @@ extern "C" MOE_API moe_status moe_glu_backward(const moe_product_config* cfg, co
   uint8_t* const base = base_of(ws);
   void* const dgu = base + k.d;
   const moe_status st = pre_gradient<true>(cfg, d, da, cfg->fmt, gu, offsets, dgu, k.ld_d, s);
-  return st == MOE_OK ? gradients(cfg, d, dgu, k.ld_d, true, x, w, offsets, dx, dw, reinterpret_cast<float*>(base + k.part), s) : st;
+  return st == MOE_OK ? gradients(cfg, d, dgu, k.ld_d, true, x, w, offsets, dx, dw, base, k, s) : st;
 }
 
 extern "C" MOE_API moe_status moe_linear(const moe_product_config* cfg, const void* x, const void* w, const float* bias,
@@ -600,7 +672,6 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
   const hipStream_t s = stream_of(stream);
   const StreamDevice on(s);
   uint8_t* const base = base_of(ws);
-  float* const sums = reinterpret_cast<float*>(base + k.part);
   moe_status st = MOE_OK;
   // dy itself where nothing changes it and its rows start on 16 bytes, else dz in the operands' type
   const bool products = dx || dw;
@@ -619,6 +690,6 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
     st = pre_gradient<false>(cfg, d, dy, cfg->y_fmt, z, offsets, dz, k.ld_d, s);
   }
   if (st != MOE_OK || !products) return st;
-  return as_is ? gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, sums, s)
-               : gradients(cfg, d, dz, k.ld_d, true, x, w, offsets, dx, dw, sums, s);
+  return as_is ? gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, base, k, s)
+               : gradients(cfg, d, dz, k.ld_d, true, x, w, offsets, dx, dw, base, k, s);
 }

@@ -174,9 +174,9 @@ __device__ __forceinline__ void band_order(uint32_t r, int mt, int nt, int& m, i
 }
 
 // Where a tile of C lies: M x N outputs of K terms from row row0 (or of them) of expert g's; m0: its
-// first row of weights (OP_DW), n0: its first column.
+// first row of weights (OP_DW), n0: its first column; split: which part of the k (ProductArgs::splits).
 struct Place {
-  int g, row0, m0, n0, M, N, K;
+  int g, row0, m0, n0, M, N, K, split;
 };
 
 // The row tiles of all experts, counted: each wavefront's lanes count those of E / 64
@@ -416,7 +416,7 @@ __device__ __forceinline__ void write_tile(const ProductArgs& p, const Place& at
       if (r >= 16 || row >= at_.M || cols <= 0) continue;
       if constexpr (OP == OP_DW) {
         // past the caches: it is read much later, if at all there (1.07 GB of it 333 -> 257 us, 134 MB 101 -> 95)
-        write8<true>(p.out, blockIdx.y * p.plane + ((int64_t)at_.g * p.M + at_.m0 + row) * p.N + col, p.out_fmt, cols, v);
+        write8<true>(p.out, at_.split * p.plane + ((int64_t)at_.g * p.M + at_.m0 + row) * p.N + col, p.out_fmt, cols, v);
       } else {
         const int64_t at = at_.row0 + row;
         if constexpr (OP == OP_GLU) {
@@ -448,7 +448,7 @@ __device__ __forceinline__ void write_tile(const ProductArgs& p, const Place& at
           }
           write8(p.out, at * p.ldo + col, p.out_fmt, cols, v);
         } else {
-          write8(p.out, blockIdx.y * p.plane + at * p.ldo + col, p.out_fmt, cols, v);
+          write8(p.out, at_.split * p.plane + at * p.ldo + col, p.out_fmt, cols, v);
         }
       }
     }
@@ -472,17 +472,17 @@ __device__ __forceinline__ u32x4 elements_from(u32x4 q, int n) {
 // for outputs that are not written.  In the last stage it is its row's last whole piece, shifted.
 // (Rows shorter than a piece: element by element.)
 template <typename E, int OP, int BM, int BN, int WM, int WN, int DEPTH>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(ProductArgs p) {
+__device__ __forceinline__ void staged_product(const ProductArgs& p, uint32_t block, int split, uint8_t* lds) {
   using T = ProductTile<E, OP, BM, BN, WM, WN>;
   using OpA = Operand<E, BM, T::kKmajA>;
   using OpB = Operand<E, BN, T::kKmajB>;
   constexpr int kThreads = T::kThreads, kK = OpA::kK, kEl = OpA::kEl, kStage = T::kStages / 2;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[T::kStages];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
   Place at;
-  if (!find_place<OP, BM, T::kCols>(p, count_tiles<OP, BM>(p), blockIdx.x >> 3, at)) return;
-  const int K = at.K, all = (K + kK - 1) / kK, stages = (all + p.splits - 1) / p.splits, first = blockIdx.y * stages;
+  if (!find_place<OP, BM, T::kCols>(p, count_tiles<OP, BM>(p), block >> 3, at)) return;
+  at.split = split;
+  const int K = at.K, all = (K + kK - 1) / kK, stages = (all + p.splits - 1) / p.splits, first = split * stages;
 
   // this thread's pieces.  k in a row: the row's start; a row per k: the piece in the first stage's row (or
   // the last column's, past it), and how many of its elements are behind the row
@@ -595,6 +595,12 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(Pro
   write_tile<E, OP, BM, BN, WM, WN>(p, at, lds + wave * T::kPatch, wave, lane, acc);
 }
 
+template <typename E, int OP, int BM, int BN, int WM, int WN, int DEPTH>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void product_kernel(ProductArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[ProductTile<E, OP, BM, BN, WM, WN>::kStages];
+  staged_product<E, OP, BM, BN, WM, WN, DEPTH>(p, blockIdx.x, blockIdx.y, lds);
+}
+
 // ---------------------------------------------------------------- operands straight into LDS
 // The same for operands whose rows all start on 16 bytes: buffer loads write LDS themselves, 1 KB a
 // wavefront and instruction in lane order (the pieces' places are chosen by what each lane reads), so
@@ -631,26 +637,26 @@ template <int W>
 __device__ __forceinline__ int tile_row(int r, int half) { return r / (W / 2) * W + half * (W / 2) + r % (W / 2); }
 
 // KS > 1: so many groups of wavefronts share a tile, each with its own part of the k and its own stages;
-// their sums meet in LDS, in order.  WAVES: of a SIMD unit.
-template <typename E, int OP, int BM, int BN, int WM, int WN, int KS, int WAVES>
-__global__ __launch_bounds__(KS * 64 * (BM / WM) * (BN / WN), WAVES) void product_direct_kernel(ProductArgs p) {
+// their sums meet in LDS, in order.
+template <typename E, int OP, int BM, int BN, int WM, int WN, int KS>
+__device__ __forceinline__ void direct_product(const ProductArgs& p, uint32_t block, int split, uint8_t* lds_all) {
   using T = ProductTile<E, OP, BM, BN, WM, WN>;
   using OpA = Operand<E, BM / 2, T::kKmajA>;  // of half a tile
   using OpB = Operand<E, BN / 2, T::kKmajB>;
   constexpr int kThreads = T::kThreads, kK = OpA::kK, kMt = T::kMt, kNt = T::kNt, kSteps = 2, kStage = T::kStages / 2;
   constexpr int eb = sizeof(E);
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_all[KS * T::kStages];
   const int tid = KS == 1 ? threadIdx.x : threadIdx.x % kThreads, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int part = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
   uint8_t* const lds = lds_all + part * T::kStages;
 
   Place at;
-  if (!find_place<OP, BM, T::kCols>(p, count_tiles<OP, BM>(p), blockIdx.x >> 3, at)) return;
+  if (!find_place<OP, BM, T::kCols>(p, count_tiles<OP, BM>(p), block >> 3, at)) return;
+  at.split = split;
 
   // this part's first k and its stages; past the last k, loads bring zeros
   const int all = (at.K + kK - 1) / kK, parts = KS * p.splits, stages = (all + parts - 1) / parts;
-  const int first = (blockIdx.y * KS + part) * stages;
+  const int first = (split * KS + part) * stages;
   const int left = at.K - first * kK;
 
   // this thread's pieces of each half: byte offsets at the first k, and their k in a stage
@@ -792,6 +798,32 @@ __global__ __launch_bounds__(KS * 64 * (BM / WM) * (BN / WN), WAVES) void produc
         for (int o = 1; o < KS; ++o) acc[m][n] += *sum(o, m, n);
   }
   write_tile<E, OP, BM, BN, WM, WN>(p, at, lds_all + wave * T::kPatch, wave, lane, acc);
+}
+
+// (WAVES: of a SIMD unit)
+template <typename E, int OP, int BM, int BN, int WM, int WN, int KS, int WAVES>
+__global__ __launch_bounds__(KS * 64 * (BM / WM) * (BN / WN), WAVES) void product_direct_kernel(ProductArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[KS * ProductTile<E, OP, BM, BN, WM, WN>::kStages];
+  direct_product<E, OP, BM, BN, WM, WN, KS>(p, blockIdx.x, blockIdx.y, lds);
+}
+
+// Both gradients of a projection in one launch, for sizes at which neither fills the CUs for long: the
+// first workgroups have dx's tiles (and splits), the others dw's.
+template <typename E, int BM, int BN, int WM, int WN, int WAVES, bool STAGED>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES) void gradients_kernel(ProductArgs dx, uint32_t dx_blocks, ProductArgs dw,
+                                                                                      uint32_t dw_blocks) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ProductTile<E, OP_DX, BM, BN, WM, WN>::kStages];
+  static_assert(sizeof(lds) == ProductTile<E, OP_DW, BM, BN, WM, WN>::kStages, "one size for both");
+  const uint32_t others = dx_blocks * dx.splits;
+  if (blockIdx.x < others) {
+    const uint32_t split = blockIdx.x / dx_blocks, block = blockIdx.x - split * dx_blocks;
+    if constexpr (STAGED) staged_product<E, OP_DX, BM, BN, WM, WN, 3>(dx, block, split, lds);
+    else direct_product<E, OP_DX, BM, BN, WM, WN, 1>(dx, block, split, lds);
+  } else {
+    const uint32_t i = blockIdx.x - others, split = i / dw_blocks, block = i - split * dw_blocks;
+    if constexpr (STAGED) staged_product<E, OP_DW, BM, BN, WM, WN, 3>(dw, block, split, lds);
+    else direct_product<E, OP_DW, BM, BN, WM, WN, 1>(dw, block, split, lds);
+  }
 }
 
 // ---------------------------------------------------------------- few rows
