@@ -317,6 +317,7 @@ Plan plan_of(const ProductArgs& p) {
 template <int OP>
 ProductArgs split(ProductArgs p, int splits, float* part) {
   p.splits = splits;
+  p.past_caches = OP == OP_DW && splits == 1 && p.out_fmt == MOE_AFMT_BF16 && p.N % 64 == 0 && aligned_to(p.out, 128);
   if (splits == 1) return p;
   p.plane = (OP == OP_DW ? (int64_t)p.E * p.M : p.rows) * p.N;
   p.out = part;

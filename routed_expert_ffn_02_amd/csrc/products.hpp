@@ -33,6 +33,7 @@ struct ProductArgs {
   uint32_t tiles;            // at most
   int32_t splits;            // of the k, each with a plane of fp32 outputs of its own if there are more than one
   int64_t plane;             // elements
+  bool past_caches;          // dw in whole lines of bf16
 };
 
 // ---------------------------------------------------------------- activations
@@ -415,8 +416,16 @@ __device__ __forceinline__ void write_tile(const ProductArgs& p, const Place& at
       if constexpr (OP == OP_GLU) get(WN / 2 + cl, u);
       if (r >= 16 || row >= at_.M || cols <= 0) continue;
       if constexpr (OP == OP_DW) {
-        // past the caches: it is read much later, if at all there (1.07 GB of it 333 -> 257 us, 134 MB 101 -> 95)
-        write8<true>(p.out, at_.split * p.plane + ((int64_t)at_.g * p.M + at_.m0 + row) * p.N + col, p.out_fmt, cols, v);
+        // past the caches in whole lines: it is read much later, if at all there (1.07 GB of it 333 -> 257 us, 134 MB
+        // 101 -> 95).  Parts of lines are put together in the caches: rows of 760 for 109 experts of 512 would take 40 us
+        // past them and 22, in fp32 135 and 46.  The empty asm keeps the two kinds of store apart.
+        const int64_t at = at_.split * p.plane + ((int64_t)at_.g * p.M + at_.m0 + row) * p.N + col;
+        if (p.past_caches) {
+          write8<true>(p.out, at, MOE_AFMT_BF16, cols, v);
+          asm volatile("");
+        } else {
+          write8(p.out, at, p.out_fmt, cols, v);
+        }
       } else {
         const int64_t at = at_.row0 + row;
         if constexpr (OP == OP_GLU) {
