@@ -135,33 +135,33 @@ __global__ __launch_bounds__(256) void split_join_kernel(const float* __restrict
 
 namespace {
 
-int bias_splits(int64_t rows, int E) {
-  return (int)std::clamp<int64_t>(rows / ((int64_t)E * kBiasRows), 1, 64);
+int bias_splits(int64_t rows, int64_t E, int64_t n) {
+  return (int)std::clamp<int64_t>(std::min<int64_t>(rows / (E * kBiasRows), (1ll << 20) / (E * ((n + 63) / 64))), 1, 64);
 }
 
 // ---------------------------------------------------------------- launches
 constexpr int64_t kMaxThreads = (1ll << 32) - 1;  // a launch's are counted in 32 bits
 
-// Row tiles of BM (every expert with a row may end in a part of one) and the grid over them.
-template <int OP, int BM, int COLS>
-int64_t tiles_of(const ProductArgs& p) {
-  const int64_t nt = (p.N + COLS - 1) / COLS;
-  const int64_t mt = OP == OP_DW ? (int64_t)p.E * ((p.M + BM - 1) / BM)
-                                 : ((int64_t)p.rows + (int64_t)std::min(p.E, p.rows) * (BM - 1)) / BM;
+// Row tiles of bm (every expert with a row may end in a part of one) times column tiles of `cols` outputs, and
+// the grid over them: whole runs on every XCD.
+template <int OP>
+int64_t tiles_of(const ProductArgs& p, int bm, int cols) {
+  const int64_t nt = (p.N + cols - 1) / cols;
+  const int64_t mt = OP == OP_DW ? (int64_t)p.E * ((p.M + bm - 1) / bm)
+                                 : ((int64_t)p.rows + (int64_t)std::min(p.E, p.rows) * (bm - 1)) / bm;
   return mt * nt;
 }
-// Workgroups: whole runs on every XCD.
-template <int OP, int BM, int COLS>
-int64_t blocks_of(const ProductArgs& p) {
-  const int64_t tiles = tiles_of<OP, BM, COLS>(p);
+template <int OP>
+int64_t blocks_of(const ProductArgs& p, int bm, int cols) {
+  const int64_t tiles = tiles_of<OP>(p, bm, cols);
   const int64_t eight = 8 * (OP == OP_DW ? (int64_t)dealt_run((uint32_t)std::min<int64_t>(tiles / p.E, 1 << 30)) : 1);
   return (tiles + eight - 1) / eight * eight;
 }
 template <typename T, int OP, int BM>
 moe_status run_tiles(void (*kernel)(ProductArgs), ProductArgs p, int threads, hipStream_t s) {
-  const int64_t blocks = blocks_of<OP, BM, T::kCols>(p);
+  const int64_t blocks = blocks_of<OP>(p, BM, T::kCols);
   if (blocks * threads * p.splits > kMaxThreads) return MOE_EINVAL;
-  p.tiles = (uint32_t)tiles_of<OP, BM, T::kCols>(p);
+  p.tiles = (uint32_t)tiles_of<OP>(p, BM, T::kCols);
   return launch(kernel, dim3((unsigned)blocks, p.splits), dim3(threads), s, p);
 }
 
@@ -278,7 +278,7 @@ bool few_rows_ok(const ProductArgs& p, float tiles_time) {
 template <typename E, int OP>
 moe_status few_rows(ProductArgs p, hipStream_t s) {
   if constexpr (OP == OP_GLU || OP == OP_LINEAR) {
-    const int64_t tiles = tiles_of<OP, 16, kFewCols<OP>>(p), blocks = (tiles + 7) / 8 * 8;
+    const int64_t tiles = tiles_of<OP>(p, 16, kFewCols<OP>), blocks = (tiles + 7) / 8 * 8;
     if (blocks * 64 * kFewWaves > kMaxThreads) return MOE_EINVAL;
     p.tiles = (uint32_t)tiles;
     return launch(few_rows_kernel<E, OP>, dim3((unsigned)blocks), dim3(64 * kFewWaves), s, p);
@@ -365,14 +365,13 @@ moe_status gradient(const ProductArgs& p, const Plan& plan, float* part, hipStre
 }
 template <typename E, int B, int WAVES, bool STAGED>
 moe_status pair(ProductArgs dx, ProductArgs dw, hipStream_t s) {
-  dx.tiles = (uint32_t)tiles_of<OP_DX, B, B>(dx);
-  const int64_t a = blocks_of<OP_DX, B, B>(dx), b = blocks_of<OP_DW, B, B>(dw), blocks = a * dx.splits + b * dw.splits;
-  if (blocks * 256 > kMaxThreads) return MOE_EINVAL;
+  dx.tiles = (uint32_t)tiles_of<OP_DX>(dx, B, B);
+  const int64_t a = blocks_of<OP_DX>(dx, B, B), b = blocks_of<OP_DW>(dw, B, B), blocks = a * dx.splits + b * dw.splits;
   return launch(gradients_kernel<E, B, B, B / 2, B / 2, WAVES, STAGED>, dim3((unsigned)blocks), dim3(256), s, dx, (uint32_t)a, dw, (uint32_t)b);
 }
 // Both gradients, in one launch where that is estimated to be faster: all workgroups' stages over the CUs' rounds,
-// not less than the longest tile alone.
-constexpr float kLaunchUs = 2.f;
+// not less than the longest tile alone.  (Of many tiles the launch is no matter, and they stay apart.)
+constexpr float kLaunchUs = 2.f, kPairTiles = 1 << 16;
 template <typename E>
 moe_status both(const ProductArgs& dx, const ProductArgs& dw, float* part, float* part_dw, hipStream_t s) {
   const Plan a = plan_of<E, OP_DX>(dx), b = plan_of<E, OP_DW>(dw);
@@ -383,6 +382,7 @@ moe_status both(const ProductArgs& dx, const ProductArgs& dw, float* part, float
       if ((i == STAGED_64) == a.straight || (i == TILE_128 && (a.splits > 1 || b.splits > 1))) continue;
       const TileCost &ca = costs_of<E, OP_DX>()[i], &cb = costs_of<E, OP_DW>()[i];
       const float ta = a.splits * tiles_like<OP_DX>(dx, ca.bm, ca.bn), tb = b.splits * tiles_like<OP_DW>(dw, cb.bm, cb.bn);
+      if (ta + tb > kPairTiles) continue;
       const float sa = std::ceil(stages_of<E, OP_DX>(dx) / a.splits), sb = std::ceil(stages_of<E, OP_DW>(dw) / b.splits);
       const float work = (ta * sa * ca.shared + tb * sb * cb.shared) / (ta + tb) * std::ceil((ta + tb) / kCus);
       const float time = std::max({work, sa * ca.alone, sb * cb.alone}) + std::ceil((ta + tb) / (kCus * ca.per_cu)) * std::max(ca.fixed, cb.fixed) +
@@ -408,6 +408,15 @@ template <typename E>
 moe_status gradients_of(const ProductArgs& dx, const ProductArgs& dw, float* part, float* part_dw, hipStream_t s) {
   if (dx.out && dw.out) return both<E>(dx, dw, part, part_dw, s);
   return dx.out ? gradient<E, OP_DX>(dx, plan_of<E, OP_DX>(dx), part, s) : gradient<E, OP_DW>(dw, plan_of<E, OP_DW>(dw), part_dw, s);
+}
+// Whether the launch that its plan asks for is one.
+template <typename E, int OP>
+bool fits(const ProductArgs& p) {
+  if (!p.out) return true;
+  const Plan plan = plan_of<E, OP>(p);
+  const TileCost& c = costs_of<E, OP>()[plan.tile];
+  const int threads = (c.bm * c.bn > 128 * 128 ? 512 : 256) * c.parts;
+  return blocks_of<OP>(p, c.bm, c.bn) * threads * plan.splits <= kMaxThreads;
 }
 
 // ---------------------------------------------------------------- checks
@@ -488,7 +497,7 @@ Workspace workspace_of(int64_t rows, int E, int64_t k, int64_t n, int64_t bias_n
   w.ld_d = up(n, 8);
   w.d = 0;
   w.bias = up(rows * w.ld_d * fmt_bytes(fmt), 16);
-  const int splits = bias_splits(rows, E);
+  const int splits = bias_splits(rows, E, std::max<int64_t>(bias_n, 1));
   w.part = up(w.bias + (bias_n && splits > 1 ? 4 * (int64_t)splits * E * bias_n : 0), 16);
   w.part_dw = up(w.part + 4 * partials<OP_DX>(fmt, dx), 16);
   w.bytes = 15 + w.part_dw + 4 * partials<OP_DW>(fmt, dw);
@@ -501,8 +510,19 @@ bool sizes_ok(int32_t rows, int32_t E, int32_t K, int32_t N, int32_t fmt) {
 uint8_t* base_of(void* ws) { return reinterpret_cast<uint8_t*>(((uintptr_t)ws + 15) & ~(uintptr_t)15); }
 
 // dx = d W and dW = d^T x, each where it is asked for.
-moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz, int64_t ld_dz, bool padded, const void* x, const void* w,
-                     const int32_t* offsets, void* dx, void* dw, uint8_t* ws, const Workspace& k, hipStream_t s) {
+struct Gradients {
+  ProductArgs dx, dw;
+  float *part, *part_dw;
+  int fmt;
+  bool fit() const {
+    return fmt == MOE_AFMT_BF16 ? fits<uint16_t, OP_DX>(dx) && fits<uint16_t, OP_DW>(dw) : fits<float, OP_DX>(dx) && fits<float, OP_DW>(dw);
+  }
+  moe_status run(hipStream_t s) const {
+    return fmt == MOE_AFMT_BF16 ? gradients_of<uint16_t>(dx, dw, part, part_dw, s) : gradients_of<float>(dx, dw, part, part_dw, s);
+  }
+};
+Gradients gradients(const moe_product_config* c, const Dims& d, const void* dz, int64_t ld_dz, bool padded, const void* x, const void* w,
+                    const int32_t* offsets, void* dx, void* dw, uint8_t* ws, const Workspace& k) {
   ProductArgs p{};
   p.a = dz;
   p.lda = ld_dz;
@@ -525,14 +545,14 @@ moe_status gradients(const moe_product_config* c, const Dims& d, const void* dz,
   q.M = d.wrows;
   q.out = dw;
   q.out_fmt = c->dw_fmt;
-  float *const part = reinterpret_cast<float*>(ws + k.part), *const part_dw = reinterpret_cast<float*>(ws + k.part_dw);
-  return c->fmt == MOE_AFMT_BF16 ? gradients_of<uint16_t>(p, q, part, part_dw, s) : gradients_of<float>(p, q, part, part_dw, s);
+  return {p, q, reinterpret_cast<float*>(ws + k.part), reinterpret_cast<float*>(ws + k.part_dw), c->fmt};
 }
 
 template <bool GLU>
 moe_status pre_gradient(const moe_product_config* c, const Dims& d, const void* dy, int dy_fmt, const void* z,
                         const int32_t* offsets, void* out, int64_t ld_d, hipStream_t s) {
-  const dim3 grid((unsigned)std::min((c->rows + 3) / 4, 1 << 22), (unsigned)((c->N + 511) / 512));
+  const int across = (c->N + 511) / 512;
+  const dim3 grid((unsigned)std::min((c->rows + 3) / 4, (1 << 22) / across), (unsigned)across);
   return launch(pre_gradient_kernel<GLU>, grid, dim3(256), s, dy, dy_fmt, d.ld_y, z, c->fmt, d.ld_z, offsets, c->rows,
                 c->n_experts, c->N, c->act, out, ld_d);
 }
@@ -600,8 +620,10 @@ extern "C" MOE_API moe_status moe_glu_backward(const moe_product_config* cfg, co
   const StreamDevice on(s);
   uint8_t* const base = base_of(ws);
   void* const dgu = base + k.d;
+  const Gradients g = gradients(cfg, d, dgu, k.ld_d, true, x, w, offsets, dx, dw, base, k);
+  if (!g.fit()) return MOE_EINVAL;
   const moe_status st = pre_gradient<true>(cfg, d, da, cfg->fmt, gu, offsets, dgu, k.ld_d, s);
-  return st == MOE_OK ? gradients(cfg, d, dgu, k.ld_d, true, x, w, offsets, dx, dw, base, k, s) : st;
+  return st == MOE_OK ? g.run(s) : st;
 }
 
 extern "C" MOE_API moe_status moe_linear(const moe_product_config* cfg, const void* x, const void* w, const float* bias,
@@ -678,8 +700,11 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
   const bool products = dx || dw;
   const bool as_is = !zs && cfg->y_fmt == cfg->fmt && aligned_to(dy, 16) && (d.ld_y * eb | cfg->N * eb) % 16 == 0;
   void* const dz = products && !as_is ? base + k.d : nullptr;
+  const Gradients g = as_is ? gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, base, k)
+                            : gradients(cfg, d, dz, k.ld_d, true, x, w, offsets, dx, dw, base, k);
+  if (!g.fit()) return MOE_EINVAL;
   if (dbias) {
-    const int splits = bias_splits(R, cfg->n_experts);
+    const int splits = bias_splits(R, cfg->n_experts, cfg->N);
     float* const part = splits > 1 ? reinterpret_cast<float*>(base + k.bias) : dbias;
     st = launch(bias_gradient_kernel, dim3((cfg->N + 63) / 64, cfg->n_experts, splits), dim3(256), s, dy, cfg->y_fmt, d.ld_y,
                 z, cfg->fmt, d.ld_z, offsets, cfg->rows, cfg->n_experts, cfg->N, cfg->act, splits, part, dz, k.ld_d);
@@ -690,7 +715,5 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
   } else if (dz) {
     st = pre_gradient<false>(cfg, d, dy, cfg->y_fmt, z, offsets, dz, k.ld_d, s);
   }
-  if (st != MOE_OK || !products) return st;
-  return as_is ? gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, base, k, s)
-               : gradients(cfg, d, dz, k.ld_d, true, x, w, offsets, dx, dw, base, k, s);
+  return st == MOE_OK && products ? g.run(s) : st;
 }

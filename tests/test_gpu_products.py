@@ -491,3 +491,54 @@ def test_replayed_graph_and_two_streams():
     torch.cuda.synchronize()
     for s, w in zip(states, want):
         assert all(torch.equal(s[n], w[n]) for n in OUTS)
+
+
+# rows, experts, H, I: few rows; a long k in parts, of dx and of dw; both gradients in one launch; sizes of their own
+CAPTURED = [(1, 0, 2048, 512), (3, 0, 64, 2000), (2100, 0, 65, 99), (130, 3, 72, 56), (1300, 5, 640, 512), (77, 2, 33, 1001)]
+
+
+@types
+@pytest.mark.parametrize("rows,E,H,I", CAPTURED)
+def test_replayed_calls_need_nothing_of_their_workspaces(dtype, rows, E, H, I):
+    """Every entry point in one graph: replays equal the eager run, whatever outputs and workspaces held before,
+    with workspaces that start anywhere."""
+    L = R()
+    off = dev(uneven(rows, E, rows // 20)) if E else None
+    n = max(E, 1)
+    x, w, rnd = operands(rows, n, H, 2 * I, dtype, "dense")
+    w, v = (w, rnd(n, H, I).to(dtype)) if E else (w[0], rnd(H, I).to(dtype))
+    da, gu, dy, z = (rnd(rows, c).to(dtype) for c in (I, 2 * I, H, H))
+    bias = rnd(n, H) if E else rnd(H)
+    new = lambda *s, dt=dtype: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    outs = dict(a=new(rows, I), gu=new(rows, 2 * I), y=new(rows, H), z=new(rows, H), dx=new(rows, H), dw=torch.zeros_like(w),
+                da=new(rows, I), dv=torch.zeros_like(v), db=torch.zeros_like(bias))
+    wsg = torch.empty(L.moe_glu_workspace(rows, n, H, I, fmt_of(dtype)) + 5, dtype=torch.uint8, device="cuda")[5:]
+    wsl = torch.empty(L.moe_linear_workspace(rows, n, I, H, fmt_of(dtype)) + 3, dtype=torch.uint8, device="cuda")[3:]
+
+    def calls():
+        L.moe_glu(x, w, outs["a"], outs["gu"], off)
+        L.moe_linear(da, v, outs["y"], bias, None, outs["z"], off, act=L.MOE_ACT_GELU)
+        L.moe_glu_backward(da, gu, x, w, outs["dx"], outs["dw"], wsg, off)
+        L.moe_linear_backward(dy, z, da, v, outs["da"], outs["dv"], outs["db"], wsl, off, act=L.MOE_ACT_GELU)
+
+    def refill():
+        for t in outs.values():
+            t.fill_(FILL)
+        for t in (wsg, wsl):
+            t.fill_(255)
+
+    refill()
+    calls()
+    want = {k: t.clone() for k, t in outs.items()}
+    assert all(torch.isfinite(t).all() for t in want.values())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    for turn in range(4):
+        refill()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(outs[k], want[k]) for k in outs), turn
+        refill()
+        calls()
+        assert all(torch.equal(outs[k], want[k]) for k in outs), turn

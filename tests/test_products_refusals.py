@@ -121,6 +121,17 @@ def test_too_many_tiles():
     assert glu(config(rows=1 << 26, N=65536), a=A[3], gu=None, w=1 << 50, x=1 << 52) == R.MOE_EINVAL
 
 
+@pytest.mark.parametrize("out", ["dx", "dw"])
+@pytest.mark.parametrize("fmt", [BF16, F32])
+def test_too_many_tiles_of_a_gradient(fmt, out):
+    """Refused before anything is enqueued: a launch would fail here, and say so with another error."""
+    c = config(rows=1 << 26, n_experts=1, K=65536, N=64, fmt=fmt) if out == "dx" else config(rows=8, n_experts=1024, K=65536, N=65536, fmt=fmt)
+    far = dict(x=1 << 50, w=1 << 52, ws=1 << 54, n=1 << 50, dx=None, dw=None)
+    far[out] = 1 << 56
+    assert glu_backward(c, da=1 << 44, gu=1 << 48, off=None if out == "dx" else A[4], **far) == R.MOE_EINVAL
+    assert linear_backward(c, dy=1 << 44, z=1 << 48, off=None if out == "dx" else A[4], **{**far, "db": 1 << 40}) == R.MOE_EINVAL
+
+
 # --- the binding's own checks ------------------------------------------------
 def refused(f, *a, **kw):
     with pytest.raises(R.MoeError) as e:
