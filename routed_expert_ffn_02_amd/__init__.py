@@ -4,8 +4,8 @@ Argument marshalling only: every function here has the name of a C entry point
 declared in include/routed_moe.h and forwards to it.  Device tensors are passed
 as raw pointers (torch supplies device memory and the HIP stream); every step of
 the hot path runs in the library's kernels.  Calls on a context go through ctypes;
-those around the experts, which check every tensor they are given, through a small
-extension module (_marshal).  There is no fallback: importing this package fails
+those around the experts and the experts' products, which check every tensor they are
+given, through a small extension module (_marshal).  There is no fallback: importing this package fails
 when the compiled library is missing, and the calls around the experts fail when the
 module is missing or was built for another Python or torch (calls on a context need it not).
 """

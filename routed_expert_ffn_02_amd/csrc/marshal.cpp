@@ -1,6 +1,6 @@
 // Torch tensors to the C entry points around the experts (moe_dispatch ... moe_block_norm_backward) and
-// of their products (moe_glu ... moe_linear_backward): checks of type, shape, stride and device, the current stream, and the call.  A Python
-// extension module, since those checks in Python cost more than the launch they precede
+// of their products (moe_glu ... moe_linear_backward): checks of type, shape, stride and device, the
+// current stream, and the call.  A Python extension module, since those checks in Python cost more than the launch they precede
 // (0.4 us a tensor, 4 to 14 tensors a call, against 3 us): nothing is computed here.
 #include <hip/hip_runtime_api.h>
 #include <torch/csrc/autograd/python_variable.h>
