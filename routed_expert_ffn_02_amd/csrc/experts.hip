@@ -215,7 +215,7 @@ constexpr TileCost kCosts[2][3][TILES] = {
     {{{256, 256, 1, 1, 4.33f, .90f, 1.64f}, {128, 256, 1, 1, 4.11f, .61f, .94f}, {128, 128, 2, 1, 4.19f, .56f, .47f}, {64, 128, 3, 1, 3.18f, .31f, .29f},
       {64, 64, 5, 1, 2.77f, .32f, .20f}, {64, 64, 1, 4, 5.f, .75f, .56f},
       {128, 128, 2, 1, 6.39f, .91f, 1.06f}, {64, 64, 3, 1, 3.91f, .52f, .32f}},
-     {{256, 256, 1, 1, 3.75f, 1.44f, 1.35f}, {128, 256, 1, 1, 5.08f, .68f, .79f}, {128, 128, 2, 1, 2.47f, .43f, .44f}, {64, 128, 3, 1, 3.06f, .57f, .25f},
+     {{256, 256, 1, 1, 3.75f, 1.44f, 1.35f}, {128, 256, 1, 1, 5.08f, .68f, .79f}, {128, 128, 2, 1, 2.47f, .43f, .44f}, {64, 128, 3, 1, 3.06f, .57f, .28f},
       {64, 64, 5, 1, 3.51f, .26f, .21f}, {64, 64, 1, 4, 5.f, .90f, .92f},
       {128, 128, 2, 1, 6.85f, .46f, .89f}, {64, 64, 3, 1, 4.00f, .61f, .25f}},
      {{256, 256, 1, 1, 3.75f, .94f, 1.54f}, {128, 256, 1, 1, 3.58f, .70f, 1.f}, {128, 128, 2, 1, 3.38f, .67f, .58f}, {64, 128, 3, 1, 3.51f, .45f, .40f},
