@@ -63,7 +63,8 @@ __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restric
 // columns, eight lanes of eight, and 32 rows at once; its rows' sums meet in LDS in a fixed order.
 // Splits of a long expert write their own sums, which bias_join adds in order: 32 rows a split and
 // more, up to 64 splits, put about as many loads in flight as there are (777 rows of 1001 in bf16 with
-// gelu: 19 us in one split of sixteen wavefronts, 12 in splits of 128 rows).
+// gelu, both kernels: 19 us in one split of sixteen wavefronts, 8.3 here; 9.9 with the loop's body twice, which takes
+// longer to fetch).  32768 rows of 512 take 34 us; 256 splits 27, but the short ones above 9.0.
 constexpr int kBiasRows = 32;  // rows of a split, at least
 
 __global__ __launch_bounds__(256) void bias_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
@@ -78,7 +79,7 @@ __global__ __launch_bounds__(256) void bias_gradient_kernel(const void* __restri
   const int len = (r.n + splits - 1) / splits, from = min(r.n, (int)blockIdx.z * len), to = min(r.n, from + len);
   float sum[8] = {};
   if (c < n) {
-#pragma unroll 2
+#pragma unroll 1
     for (int i = from + 8 * wave + (lane >> 3); i < to; i += 32) {
       float v[8], g[8];
       read8(dy, (int64_t)(r.first + i) * ld_dy + c, dy_fmt, n - c, v);
