@@ -504,6 +504,13 @@ Workspace workspace_of(int64_t rows, int E, int64_t k, int64_t n, int64_t bias_n
   w.bytes = 15 + w.part_dw + 4 * partials<OP_DW>(fmt, dw);
   return w;
 }
+// Of a bias's gradient alone, which has no product: its partial sums.
+Workspace bias_workspace(int64_t rows, int E, int64_t n) {
+  Workspace w{};
+  const int splits = bias_splits(rows, E, n);
+  w.bytes = 15 + (splits > 1 ? 4 * (int64_t)splits * E * n : 0);
+  return w;
+}
 bool sizes_ok(int32_t rows, int32_t E, int32_t K, int32_t N, int32_t fmt) {
   return rows >= 1 && rows <= kProductMaxRows && E >= 1 && E <= kMaxExperts && K >= 1 && K <= kProductMaxSize && N >= 1 &&
          N <= kProductMaxSize && fmt_ok(fmt);
@@ -679,7 +686,8 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
   if (!dy || (!dx && !dw && !dbias) || (dx && !w) || (dw && !x) || !ws || !dims_ok(cfg, false, offsets, d)) return MOE_EINVAL;
   if (cfg->act != MOE_ACT_NONE && !z) return MOE_EINVAL;
   const int64_t eb = fmt_bytes(cfg->fmt), R = cfg->rows;
-  const Workspace k = workspace_of(R, cfg->n_experts, cfg->K, cfg->N, cfg->N, cfg->fmt);
+  const bool products = dx || dw;
+  const Workspace k = products ? workspace_of(R, cfg->n_experts, cfg->K, cfg->N, cfg->N, cfg->fmt) : bias_workspace(R, cfg->n_experts, cfg->N);
   if (ws_bytes < (size_t)k.bytes) return MOE_EINVAL;
   const bool zs = cfg->act != MOE_ACT_NONE;
   if (!all_aligned(eb, zs ? z : nullptr, dx ? w : nullptr, dw ? x : nullptr, dx) || !aligned_to(dy, fmt_bytes(cfg->y_fmt)) ||
@@ -698,7 +706,6 @@ extern "C" MOE_API moe_status moe_linear_backward(const moe_product_config* cfg,
   uint8_t* const base = base_of(ws);
   moe_status st = MOE_OK;
   // dy itself where nothing changes it and its rows start on 16 bytes, else dz in the operands' type
-  const bool products = dx || dw;
   const bool as_is = !zs && cfg->y_fmt == cfg->fmt && aligned_to(dy, 16) && (d.ld_y * eb | cfg->N * eb) % 16 == 0;
   void* const dz = products && !as_is ? base + k.d : nullptr;
   const Gradients g = as_is ? gradients(cfg, d, dy, d.ld_y, false, x, w, offsets, dx, dw, base, k)
