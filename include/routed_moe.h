@@ -776,7 +776,7 @@ typedef struct {
 MOE_API moe_status moe_glu(const moe_product_config* cfg, const void* x, const void* w, const int32_t* offsets, void* a,
                            void* gu, moe_stream_t stream);
 
-/* Bytes of workspace of moe_glu_backward; -1 for shapes out of range.  Pure host function. */
+/* Bytes of workspace of moe_glu_backward for `rows` rows or fewer; -1 for shapes out of range.  Pure host function. */
 MOE_API int64_t moe_glu_workspace(int32_t rows, int32_t n_experts, int32_t H, int32_t I, int32_t fmt);
 
 /*
@@ -796,8 +796,8 @@ MOE_API moe_status moe_glu_backward(const moe_product_config* cfg, const void* d
 MOE_API moe_status moe_linear(const moe_product_config* cfg, const void* x, const void* w, const float* bias,
                               const void* residual, const int32_t* offsets, void* y, void* z, moe_stream_t stream);
 
-/* Bytes of workspace of moe_linear_backward, whichever outputs it has (for dbias alone, whatever K and fmt are said to
- * be); -1 for shapes out of range.  Pure host function. */
+/* Bytes of workspace of moe_linear_backward for `rows` rows or fewer, whichever outputs it has (for dbias alone, whatever
+ * K and fmt are said to be); -1 for shapes out of range.  Pure host function. */
 MOE_API int64_t moe_linear_workspace(int32_t rows, int32_t n_experts, int32_t K, int32_t N, int32_t fmt);
 
 /*

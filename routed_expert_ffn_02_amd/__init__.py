@@ -603,7 +603,7 @@ def moe_glu(x, w, a, gu=None, offsets=None, act: int = MOE_ACT_SILU, stream=None
 
 
 def moe_glu_workspace(rows: int, n_experts: int, H: int, I: int, fmt: int) -> int:
-    """Bytes of workspace of moe_glu_backward (fmt: MOE_AFMT_* of its tensors)."""
+    """Bytes of workspace of moe_glu_backward for `rows` rows or fewer (fmt: MOE_AFMT_* of its tensors)."""
     return _workspace(lib.moe_glu_workspace, rows, n_experts, H, I, fmt)
 
 
@@ -620,7 +620,7 @@ def moe_linear(x, w, y, bias=None, residual=None, z=None, offsets=None, act: int
 
 
 def moe_linear_workspace(rows: int, n_experts: int, K: int, N: int, fmt: int) -> int:
-    """Bytes of workspace of moe_linear_backward (fmt: MOE_AFMT_* of x and w)."""
+    """Bytes of workspace of moe_linear_backward for `rows` rows or fewer (fmt: MOE_AFMT_* of x and w)."""
     return _workspace(lib.moe_linear_workspace, rows, n_experts, K, N, fmt)
 
 

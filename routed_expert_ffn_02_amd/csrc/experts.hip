@@ -480,12 +480,14 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 struct Workspace {
   int64_t ld_d, d, bias, part, part_dw, bytes;  // elements; offsets and size in bytes
 };
-// Elements of fp32 sums that splits of the k leave, at most.
+// Elements of fp32 sums that splits of the k leave, at most, for these rows or fewer: splits_for's tiles times splits,
+// 64 x 64 outputs each, are no more than the CUs.  (What these rows need alone may be less: enough of them are not split.)
 template <int OP>
 int64_t partials(int fmt, const ProductArgs& p) {
-  const float tiles = tiles_like<OP>(p, 64, 64);
-  const int splits = splits_for(tiles, fmt == MOE_AFMT_BF16 ? stages_of<uint16_t, OP>(p) : stages_of<float, OP>(p));
-  return splits > 1 ? (OP == OP_DW ? (int64_t)p.E * p.M : p.rows) * p.N * splits : 0;
+  const float stages = fmt == MOE_AFMT_BF16 ? stages_of<uint16_t, OP>(p) : stages_of<float, OP>(p);
+  const int splits = splits_for(1.f, stages);
+  const int64_t plane = (OP == OP_DW ? (int64_t)p.E * p.M : p.rows) * p.N;
+  return splits > 1 ? std::min<int64_t>(plane * splits, kCus * 64 * 64) : 0;
 }
 // (k: columns of x; n: of d, 2 N for the gated block; bias_n: of the bias or 0)
 Workspace workspace_of(int64_t rows, int E, int64_t k, int64_t n, int64_t bias_n, int fmt) {

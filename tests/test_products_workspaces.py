@@ -1,7 +1,8 @@
 """Workspaces of the experts' products, on the CPU: what moe_*_workspace gives for a call's sizes is enough for it,
-whichever of its outputs it leaves out.  (Pointers here are never followed: where nothing is refused, a call ends at
-its launch, which fails without a device.)"""
+whichever of its outputs it leaves out, and for fewer rows.  (Pointers here are never followed: where nothing is
+refused, a call ends at its launch, which fails without a device.)"""
 import ctypes
+import random
 
 import pytest
 import torch
@@ -41,3 +42,28 @@ def test_a_bias_alone_still_needs_its_sums(fmt):
     """3000 rows are summed in 64 parts of 70 columns, 4 bytes each, and 15 bytes reach an alignment."""
     for act in (R.MOE_ACT_NONE, R.MOE_ACT_SILU):
         assert bias_alone(3000, 1, 8, 70, fmt, fmt, 64 * 70 * 4 + 14, act) == R.MOE_EINVAL
+
+
+@pytest.mark.parametrize("f", [R.moe_glu_workspace, R.moe_linear_workspace])
+def test_a_workspace_does_for_fewer_rows(f):
+    """A program keeps the workspace of its largest batch: the sums of products split along the k, which the largest one
+    may not have, find place in it (140 rows of 3995 and 3819 are not split, 120 are)."""
+    rng = random.Random(5)
+    for i in range(4000):
+        K, N, fmt = rng.randint(1, 4096), rng.randint(1, 4096), rng.choice([F32, BF16])
+        E, rows = rng.choice([1, rng.randint(2, 256)]), int(2 ** rng.uniform(0, 14))
+        if i == 0:
+            E, K, N, fmt, rows = 1, 3995, 3819, BF16, 140
+        most = f(rows, E, K, N, fmt)
+        for fewer in {120 if i == 0 else rng.randint(1, rows), rng.randint(1, rows), max(rows - 1, 1)}:
+            if fewer <= rows:
+                assert f(fewer, E, K, N, fmt) <= most, (fewer, rows, E, K, N, fmt)
+
+
+@no_device
+def test_the_calls_take_it():
+    n = R.moe_glu_workspace(140, 1, 3995, 3819, BF16)
+    cfg = R.moe_product_config(120, 1, 3995, 3819, BF16, BF16, BF16, R.MOE_ACT_SILU, 0, 0, 0, 0, 0, 0, 0)
+    assert L.moe_glu_backward(ctypes.byref(cfg), *A[:4], None, A[4], A[5], A[6], n, None) == R.MOE_EHIP
+    n = R.moe_linear_workspace(140, 1, 3995, 3819, BF16)
+    assert L.moe_linear_backward(ctypes.byref(cfg), *A[:4], None, A[4], A[5], A[6], A[7], n, None) == R.MOE_EHIP
