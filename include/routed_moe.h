@@ -744,8 +744,8 @@ MOE_API moe_status moe_decode_block(moe_ctx* ctx, int32_t layer, const void* x, 
  *  - Sums are fp32 (matrix cores; products of bf16 are exact in them); each output is rounded once.
  *    With bf16 operands the gradient before a projection (dgu, dz) is rounded to bf16 where it
  *    becomes the operand of dx and dw, whatever their formats; dbias sums it unrounded.
- *  - Limits: 1 <= rows <= 2^26, n_experts <= 1024, K and N <= 65536, strides <= 2^36, and 2^32 threads a
- *    launch: products of more than some 2^37 outputs are refused.
+ *  - Limits: 1 <= rows <= 2^26, n_experts <= 1024, K and N <= 65536, strides <= 2^36, rows x stride <= 2^58,
+ *    and 2^32 threads a launch: products of more than some 2^37 outputs are refused.
  *  - Alignment beyond the element's is not needed; operands whose rows all start on 16 bytes are
  *    read faster.
  */

@@ -426,7 +426,11 @@ struct Dims {
   int wrows, zcols;  // rows of an expert's weights; columns of gu or z
 };
 
-int64_t stride_of(int64_t ld, int64_t n) { return ld == 0 ? n : (ld >= n && ld <= kMaxStride ? ld : -1); }
+constexpr int64_t kMaxReach = 1ll << 58;  // elements from a matrix's first row to its end: bytes, and sums of them, stay in 64 bits
+
+int64_t stride_of(int64_t ld, int64_t n, int64_t rows) {
+  return ld == 0 ? n : (ld >= n && ld <= std::min(kMaxStride, kMaxReach / rows) ? ld : -1);
+}
 
 bool dims_ok(const moe_product_config* c, bool glu, bool offsets, Dims& d) {
   if (!c || c->rows < 1 || c->rows > kProductMaxRows || c->n_experts < 1 || c->n_experts > kMaxExperts) return false;
@@ -436,15 +440,15 @@ bool dims_ok(const moe_product_config* c, bool glu, bool offsets, Dims& d) {
   if (c->act < MOE_ACT_NONE || c->act > MOE_ACT_GELU) return false;
   d.wrows = glu ? 2 * c->N : c->N;
   d.zcols = d.wrows;
-  d.ld_x = stride_of(c->ld_x, c->K);
-  d.ld_dx = stride_of(c->ld_dx, c->K);
-  d.ld_w = stride_of(c->ld_w, c->K);
+  d.ld_x = stride_of(c->ld_x, c->K, c->rows);
+  d.ld_dx = stride_of(c->ld_dx, c->K, c->rows);
+  d.ld_w = stride_of(c->ld_w, c->K, d.wrows);
   if (d.ld_w < 0) return false;
   const int64_t dense = (int64_t)d.wrows * d.ld_w;
   d.gs_w = c->gs_w == 0 ? dense : c->gs_w;
-  d.ld_y = stride_of(c->ld_y, c->N);
-  d.ld_r = stride_of(c->ld_residual, c->N);
-  d.ld_z = stride_of(c->ld_z, d.zcols);
+  d.ld_y = stride_of(c->ld_y, c->N, c->rows);
+  d.ld_r = stride_of(c->ld_residual, c->N, c->rows);
+  d.ld_z = stride_of(c->ld_z, d.zcols, c->rows);
   if (d.ld_x < 0 || d.ld_dx < 0 || d.ld_y < 0 || d.ld_r < 0 || d.ld_z < 0) return false;
   // experts' weights lie apart, and the last one's end is an address of 2^46 elements at most
   return d.gs_w >= (int64_t)(d.wrows - 1) * d.ld_w + c->K && d.gs_w <= kMaxStride;
