@@ -17,10 +17,28 @@ constexpr int kProductMaxSize = 1 << 16;  // of a row of x, of the outputs
 
 // ---------------------------------------------------------------- the gradient before the projection
 // d = dgu (glu) or dz (linear), rounded to the operands' type: the products that follow take it as
-// an operand, as autograd's do, with zeros up to ld_d behind each row.  Eight elements a lane; rows behind
-// the last expert's are left out.
+// an operand, as autograd's do, with zeros up to ld_d behind each row.  Eight elements a lane; rows before
+// the first expert's and behind the last one's are left out.
 __device__ __forceinline__ void pad_row(void* d, int64_t at, int from, int64_t to, int fmt) {
   for (int e = from; e < to; ++e) write1(d, at + e, fmt, 0.f);
+}
+
+// From the first row that any expert has to the last one: offsets[0] and offsets[E] of a table that ascends; the least and
+// the greatest entry of another, so that no expert's d is missing.  All of a wavefront's lanes take part.
+__device__ __forceinline__ Range rows_in_use(const int32_t* offsets, int E, int rows) {
+  if (!offsets) return {0, rows};
+  int lo = rows, hi = 0;
+  for (int i = threadIdx.x & 63; i <= E; i += 64) {
+    const int o = min(max(offsets[i], 0), rows);
+    lo = min(lo, o);
+    hi = max(hi, o);
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    lo = min(lo, __shfl_xor(lo, o));
+    hi = max(hi, __shfl_xor(hi, o));
+  }
+  return {lo, hi - lo};
 }
 
 template <bool GLU>
@@ -29,10 +47,10 @@ __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restric
                                                            const int32_t* __restrict__ offsets, int rows, int E, int n,
                                                            int act, void* __restrict__ d, int64_t ld_d) {
   const int c = 8 * (blockIdx.y * 64 + (threadIdx.x & 63));
-  const int end = offsets ? min(max(offsets[E], 0), rows) : rows;
+  const Range r = rows_in_use(offsets, E, rows);
   if (c >= n) return;
-  const int all = GLU ? 2 * n : n;
-  for (int row = 4 * blockIdx.x + (threadIdx.x >> 6); row < end; row += 4 * gridDim.x) {
+  const int all = GLU ? 2 * n : n, end = r.first + r.n;
+  for (int row = r.first + 4 * blockIdx.x + (threadIdx.x >> 6); row < end; row += 4 * gridDim.x) {
     float g[8], u[8], v[8];
     read8(dy, (int64_t)row * ld_dy + c, dy_fmt, n - c, v);
     if (GLU || act != MOE_ACT_NONE) read8(z, (int64_t)row * ld_z + c, fmt, n - c, g);
