@@ -237,8 +237,8 @@ def test_model_sizes(run):
     run(300, None, 1024, 2048, B)
 
 
-# sizes at which each shape of tile is the cheapest: many rows (the largest tiles), few rows of long sums (split over
-# the k), many small experts
+# larger sizes: many rows, few rows of long sums (split over the k), many small experts.  (The sizes that take each
+# kernel and tile are product_sizes.py's.)
 BIG = [(2048, 0, 1024, 1024), (1300, 0, 2048, 2048), (700, 0, 520, 1032), (20, 0, 4096, 512), (600, 40, 512, 256), (3000, 6, 512, 768)]
 
 
