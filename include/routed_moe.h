@@ -745,7 +745,7 @@ MOE_API moe_status moe_decode_block(moe_ctx* ctx, int32_t layer, const void* x, 
  *    With bf16 operands the gradient before a projection (dgu, dz) is rounded to bf16 where it
  *    becomes the operand of dx and dw, whatever their formats; dbias sums it unrounded.
  *  - Limits: 1 <= rows <= 2^26, n_experts <= 1024, K and N <= 65536, strides <= 2^36, rows x stride <= 2^58,
- *    and 2^32 threads a launch: products of more than some 2^37 outputs are refused.
+ *    and 2^32 threads a launch: products of more than some 2^36 outputs are refused.
  *  - Alignment beyond the element's is not needed; operands whose rows all start on 16 bytes are
  *    read faster.
  */
@@ -758,7 +758,7 @@ typedef struct {
   int32_t rows, n_experts;
   int32_t K, N;        /* moe_glu: H and I; moe_linear: inputs and outputs */
   int32_t fmt;         /* moe_afmt of x, w, dx, and of a, da, gu (moe_glu) or z (moe_linear) */
-  int32_t y_fmt;       /* moe_linear: of y, residual and dy (moe_glu: any, not used) */
+  int32_t y_fmt;       /* moe_linear: of y, residual and dy (moe_glu: a valid one, not used) */
   int32_t dw_fmt;      /* of dw */
   int32_t act;         /* moe_act */
   int64_t ld_x, ld_dx; /* row strides in elements (0: dense) of x and dx */

@@ -79,10 +79,10 @@ __global__ __launch_bounds__(256) void pre_gradient_kernel(const void* __restric
 // Column sums of dz in fp32, from dy and z as given (dz is not rounded before), and, where it is asked
 // for, dz itself as the products take it (d, as pre_gradient_kernel writes it).  A workgroup has 64
 // columns, eight lanes of eight, and 32 rows at once; its rows' sums meet in LDS in a fixed order.
-// Splits of a long expert write their own sums, which bias_join adds in order: 32 rows a split and
-// more, up to 64 splits, put about as many loads in flight as there are (777 rows of 1001 in bf16 with
-// gelu, both kernels: 19 us in one split of sixteen wavefronts, 8.3 here; 9.9 with the loop's body twice, which takes
-// longer to fetch).  32768 rows of 512 take 34 us; 256 splits 27, but the short ones above 9.0.
+// Splits of a long expert write their own sums, which bias_join adds in order: 32 rows a split and more, up to 64
+// splits.  Calls for the bias alone, in bf16, with up to 64 splits and up to 256: 777 rows of 1001 with gelu 8.9 us and 8.9 (19 in
+// one split of sixteen wavefronts), 4096 x 4096 13.2 and 19.7, 32768 x 512 14.3 and 20.7, with gelu 40 and 38; in fp32 65536 x 128
+// with gelu 52 and 28, 8192 x 2048 19.4 and 26.7.  (Unrolled as the compiler likes, the loop takes the same at all of these.)
 constexpr int kBiasRows = 32;  // rows of a split, at least
 
 __global__ __launch_bounds__(256) void bias_gradient_kernel(const void* __restrict__ dy, int dy_fmt, int64_t ld_dy,
@@ -212,12 +212,14 @@ moe_status staged(const ProductArgs& p, hipStream_t s) {
 
 // A tile's shape, chosen by its estimated time: rounds of workgroups x what a tile costs beside its
 // stages, and per stage (128 bytes of k) the longer of what it takes alone on a CU and of what the CU's
-// share of all tiles takes.  The figures (us) fit measured times of 45 to 90 shapes a row (1 to 32768
-// rows, up to 256 experts, sizes 512 to 8192), where the choice is within 1 to 3% of the best shape on
-// average and 21% at worst.  In bf16, 4096^3: 256 x 256 107 us, 128 x 256 122, 128 x 128 124, 64 x 128
-// 161, 64 x 64 199; 1024 x 4096 x 4096: 86, 53, 44, 44, 54; one row of 4096 x 4096: 83, 50, 37, 28, 24,
-// and 17 where four groups of wavefronts share the k.  The last two are product_kernel's: 2048^3 in bf16
-// with rows of 2047 takes 44 us forward, 39 and 38 the gradients, where rows on 16 bytes take 25, 26 and 26.
+// share of all tiles takes.  The figures (us) were fitted to measured times of 45 to 90 shapes a row (1 to 32768
+// rows, up to 256 experts, sizes 512 to 8192).  They rank shapes and do not tell times: no term counts bytes, so what
+// memory bounds (grouped products, a short k) is estimated at down to 0.4 of its time.  Of 62 products timed in every
+// shape, most of them random ones, the choice is 3% above the best on average and 36% at worst (dw of 2384 rows, 448 x 2112).  In
+// bf16, 4096^3: 256 x 256 111 us, 128 x 256 130, 128 x 128 135, 64 x 128 173, 64 x 64 220; 1024 x 4096 x 4096: 83, 51, 41, 43, 52;
+// one row of 4096 x 4096: 83, 50, 37, 28, 24, and 17 where four groups of wavefronts share the k.  The last two are
+// product_kernel's: 2048^3 in bf16 with rows of 2047 takes 44 us forward, 39 and 38 the gradients, where rows on 16 bytes
+// take 25, 26 and 26.
 struct TileCost {
   int bm, bn, per_cu, parts;
   float fixed, alone, shared;

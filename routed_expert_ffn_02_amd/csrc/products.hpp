@@ -33,7 +33,7 @@ struct ProductArgs {
   uint32_t tiles;            // at most
   int32_t splits;            // of the k, each with a plane of fp32 outputs of its own if there are more than one
   int64_t plane;             // elements
-  bool past_caches;          // dw in whole lines of bf16
+  bool past_caches;          // dw in bf16 whose rows are whole lines
 };
 
 // ---------------------------------------------------------------- activations
@@ -416,9 +416,10 @@ __device__ __forceinline__ void write_tile(const ProductArgs& p, const Place& at
       if constexpr (OP == OP_GLU) get(WN / 2 + cl, u);
       if (r >= 16 || row >= at_.M || cols <= 0) continue;
       if constexpr (OP == OP_DW) {
-        // past the caches in whole lines: it is read much later, if at all there (1.07 GB of it 333 -> 257 us, 134 MB
-        // 101 -> 95).  Parts of lines are put together in the caches: rows of 760 for 109 experts of 512 would take 40 us
-        // past them and 22, in fp32 135 and 46.  The empty asm keeps the two kinds of store apart.
+        // past the caches where rows are whole lines: it is read much later, if at all there (1.07 GB of it 333 -> 257 us, 134
+        // MB 101 -> 95).  So do wavefronts of 32 columns, each of which has half of a line: 228 MB over 249 experts 97 -> 84,
+        // smaller ones level.  Lines that two rows share are put together in the caches: rows of 760 for 109 experts of
+        // 512 would take 40 us past them and 22, in fp32 135 and 46.  The empty asm keeps the two kinds of store apart.
         const int64_t at = at_.split * p.plane + ((int64_t)at_.g * p.M + at_.m0 + row) * p.N + col;
         if (p.past_caches) {
           write8<true>(p.out, at, MOE_AFMT_BF16, cols, v);
